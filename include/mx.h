@@ -347,6 +347,146 @@ mx_status_t mx_gemm_layout(const void *a_codes, mx_layout_t a_layout, const void
                            const void *b_codes, mx_layout_t b_layout, const void *b_scales, mx_format_t fb,
                            int64_t M, int64_t N, int64_t K, void *c, mx_out_t out, int64_t ldc, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Block-128 FP8: one fp32 scale for each block of 128.
+ *
+ * The other widespread FP8 recipe for a linear layer, beside MX: activations
+ * and gradients in blocks of 128 elements along the reduction dimension,
+ * weights in 128 x 128 tiles, every block with its own fp32 scale.  Element
+ * formats E4M3 and E5M2 (MX_E2M1 is MX_ERR_INVALID_ARG in these calls).
+ *   amax  = max(largest |v| of the block, 2^-100)
+ *   scale = amax / FMAX                (FMAX = 448 for E4M3, 57344 for E5M2)
+ *   code  = cast(clamp(v * (FMAX / amax), -FMAX, FMAX))
+ * each operation rounded once in fp32, the cast to nearest, ties to even.  A
+ * block that holds an Inf or NaN gets scale NaN and codes 0 (so every product
+ * it enters is NaN); an all-zero block gets scale 2^-100 / FMAX and codes +-0.
+ * No size has to be a multiple of anything: the last block (tile) of a row
+ * may be shorter.
+ *
+ * Operands.  Codes are rows of bytes, the reduction dimension contiguous, row
+ * r at codes + r * ld_codes (any ld_codes >= the row's length; a multiple of
+ * 16 with 16-byte aligned codes is the fast case of mx_block_gemm).  Scales
+ * have the reduction dimension's blocks outermost: block b of row r (tile b of
+ * tile row r) is scales[b * ld_scales + r], ld_scales in floats, >= the number
+ * of rows (tile rows).  Bytes between the end of a row and the next row, and
+ * floats between the last row's scale and the next block's, are neither read
+ * as values nor written.
+ */
+typedef enum {
+    MX_BLOCK_ROW = 0,            /* blocks of 128 along cols; codes [rows x cols]; scales [ceil(cols/128)][rows]  */
+    MX_BLOCK_TRANSPOSE = 1,      /* blocks of 128 along rows; codes [cols x rows]; scales [ceil(rows/128)][cols]  */
+    MX_BLOCK_TILE = 2,           /* 128 x 128; codes [rows x cols]; scales [ceil(cols/128)][ceil(rows/128)]       */
+    MX_BLOCK_TILE_TRANSPOSE = 3  /* 128 x 128; codes [cols x rows]; scales [ceil(rows/128)][ceil(cols/128)]       */
+} mx_block_mode_t;
+
+/*
+ * mx_block_quantize -- x (bf16, rows x cols, leading dimension ldx) as one
+ * block-128 operand, per `mode`.  MX_BLOCK_ROW: activations and output
+ * gradients as the left operand of Fprop and Dgrad.  MX_BLOCK_TRANSPOSE: both
+ * operands of Wgrad (reduction over tokens).  MX_BLOCK_TILE and its transposed
+ * form: the weight in Fprop and Dgrad; the tiles of one weight are the same in
+ * both forms, so their codes agree and their scales are each other's
+ * transpose.  Codes and scales must not overlap x or each other.
+ */
+mx_status_t mx_block_quantize(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx, mx_format_t fmt,
+                              mx_block_mode_t mode, void *codes, int64_t ld_codes, float *scales, int64_t ld_scales,
+                              void *stream);
+
+/*
+ * mx_block_quantize_dual -- both forms of x from one read: with tile = 0 the
+ * row form (as MX_BLOCK_ROW, format fmt_row) and the transposed form (as
+ * MX_BLOCK_TRANSPOSE, fmt_t); with tile = 1 MX_BLOCK_TILE and
+ * MX_BLOCK_TILE_TRANSPOSE.  Each exactly as the single call gives it.
+ */
+mx_status_t mx_block_quantize_dual(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx, int tile,
+                                   mx_format_t fmt_row, void *codes_row, int64_t ld_codes_row, float *scales_row,
+                                   int64_t ld_scales_row, mx_format_t fmt_t, void *codes_t, int64_t ld_codes_t,
+                                   float *scales_t, int64_t ld_scales_t, void *stream);
+
+/*
+ * mx_block_gemm -- C[m, n] = sum over blocks b of
+ *     sa[b][m] * sb[b][n] * sum_{k in block b} A[m, k] * B[n, k]
+ * with A [M x K] in blocks of 128 along K and B [N x K] likewise (b_tile = 0)
+ * or in 128 x 128 tiles (b_tile = 1: sb[b][n / 128]).  Any M, N and K (K = 0
+ * writes C = 0); lda, ldb in bytes, ldsa, ldsb in floats, c [M x ldc] per
+ * `out`, ldc >= N.  Every block's sum is multiplied by its scales and added to
+ * an fp32 accumulator.
+ *   MX_OUT_F32   every product is exact and sums are fp32: |C - sum| <=
+ *                1e-5 * sum |terms|.  The codes travel as bf16 (exact) through
+ *                the bf16 matrix instruction.
+ *   MX_OUT_BF16  the FP8 matrix instruction, at twice that rate.  It adds the
+ *                32 products of a step in a window that ends 2^-13 below the
+ *                largest, so a block's sum may be off by 2^-8 of its sum of
+ *                |terms| in the worst case (2^-11 and less on random data):
+ *                below the result's own rounding to bf16 unless the sum cancels
+ *                far.  Call with MX_OUT_F32 where that matters.
+ * Products of two scales outside fp32's range are Inf or 0.  A NaN scale makes
+ * every element of C that it contributes to NaN.
+ */
+mx_status_t mx_block_gemm(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa, mx_format_t fa,
+                          const void *b_codes, int64_t ldb, const float *b_scales, int64_t ldsb, mx_format_t fb,
+                          int b_tile, int64_t M, int64_t N, int64_t K, void *c, mx_out_t out, int64_t ldc,
+                          void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The norm in front of a linear layer, forward and backward.
+ *
+ *   mean = sum_j x_j / cols (0 for MX_NORM_RMS),
+ *   rstd = 1 / sqrt(sum_j (x_j - mean)^2 / cols + eps),
+ *   y_j = (x_j - mean) * rstd * weight_j + bias_j
+ * for every row of x (bf16, rows x cols, leading dimension ldx), all in fp32,
+ * mean before the squares are summed.  weight and bias: `cols` values of
+ * `param` type each, either may be NULL (1 and 0).  mean and rstd: fp32, one
+ * per row, for the backward pass; mean is not written for MX_NORM_RMS, either
+ * may be NULL.  eps >= 0, finite.
+ */
+typedef enum {
+    MX_NORM_LAYER = 0, /* mean and variance                        */
+    MX_NORM_RMS = 1    /* mean taken as 0: y = x / rms(x) * weight */
+} mx_norm_t;
+
+/* y: bf16 [rows x ldy], rounded once, ldy >= cols. */
+mx_status_t mx_layer_norm(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx, const void *weight,
+                          const void *bias, mx_out_t param, mx_norm_t kind, float eps, void *y_bf16, int64_t ldy,
+                          float *mean, float *rstd, void *stream);
+
+/*
+ * mx_layer_norm_quantize, mx_layer_norm_block_quantize -- the norm written as
+ * the next product's operand, without the trip through bf16: y stays in fp32
+ * (no bf16 rounding, as the rotated quantizer's y does) and is quantized as
+ * mx_quantize would (any format, cols a multiple of 32, dense codes and
+ * scales), or as mx_block_quantize with MX_BLOCK_ROW would (E4M3 or E5M2).
+ * Same rules for blocks that hold an Inf or NaN.
+ */
+mx_status_t mx_layer_norm_quantize(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx, const void *weight,
+                                   const void *bias, mx_out_t param, mx_norm_t kind, float eps, mx_format_t fmt,
+                                   void *codes, void *scales, float *mean, float *rstd, void *stream);
+mx_status_t mx_layer_norm_block_quantize(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx,
+                                         const void *weight, const void *bias, mx_out_t param, mx_norm_t kind,
+                                         float eps, mx_format_t fmt, void *codes, int64_t ld_codes, float *scales,
+                                         int64_t ld_scales, float *mean, float *rstd, void *stream);
+
+/*
+ * mx_layer_norm_backward -- with xh = (x - mean) * rstd and g = dy * weight:
+ *     dx = rstd * (g - mean_j(g) - xh * mean_j(g * xh))   (RMS: without mean_j(g))
+ *     dweight_j = sum over rows of dy * xh,  dbias_j = sum over rows of dy
+ * dy, x: bf16; dx: bf16 [rows x lddx], rounded once; dweight, dbias: fp32
+ * [cols], overwritten, either may be NULL (rows = 0 writes zeros).  mean (not
+ * read for MX_NORM_RMS, may be NULL there) and rstd as the forward call wrote
+ * them.  The sums over rows go through `workspace`, workspace_bytes >=
+ * mx_layer_norm_backward_workspace(rows, cols) bytes of device memory, 16-byte
+ * aligned, that no other call may use until this one has run on the stream;
+ * its contents need not be initialised.  It may be NULL if neither gradient is
+ * asked for.  Sums are in a fixed order: the same inputs give the same bits.
+ */
+int64_t mx_layer_norm_backward_workspace(int64_t rows, int64_t cols);
+mx_status_t mx_layer_norm_backward(const void *dy_bf16, int64_t lddy, const void *x_bf16, int64_t ldx, int64_t rows,
+                                   int64_t cols, const void *weight, mx_out_t param, mx_norm_t kind,
+                                   const float *mean, const float *rstd, void *dx_bf16, int64_t lddx, float *dweight,
+                                   float *dbias, void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Static, NUL-terminated name of a status code. */
 const char *mx_status_string(mx_status_t s);
 

@@ -2,8 +2,10 @@
 
 OCP-MX micro-scaling quantization (block 32, E8M0 scales, E4M3 / E5M2 / E2M1
 elements), the fixed-sign 32-point block-Hadamard rotation used on the
-weight-gradient path, and the MX-scaled GEMM, as hand-written gfx950 HIP
-kernels behind a C ABI.
+weight-gradient path, and the MX-scaled GEMM; FP8 operands with one fp32 scale
+for each block of 128 (quantizers and product); and the norm in front of a
+linear layer (layer norm or RMS norm, forward, straight to a quantized operand,
+and backward), as hand-written gfx950 HIP kernels behind a C ABI.
 
 This module only marshals arguments: it checks tensor shapes, dtypes and
 devices, allocates outputs with torch (device memory and streams are all
@@ -13,6 +15,7 @@ fails loudly.  Build it with ``python -m precision_block_amax_amd.build``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple, Union
@@ -23,7 +26,8 @@ __all__ = [
     "E4M3", "E5M2", "E2M1", "MXError", "lib", "library_path", "code_cols",
     "quantize", "quantize_transpose", "hadamard32_quantize", "quantize_dual",
     "quantize_transpose_sr", "quantize_pair", "gemm", "fsdp_payload", "payload_views",
-    "payload_width",
+    "payload_width", "block_quantize", "block_quantize_dual", "block_gemm", "layer_norm",
+    "layer_norm_quantize", "layer_norm_backward",
 ]
 
 E4M3, E5M2, E2M1 = 0, 1, 2
@@ -65,6 +69,19 @@ def lib() -> ctypes.CDLL:
         L.mx_hadamard32_quantize_panels.argtypes = [P, i64, i64, i64, u32, i32, P, P, P]
         L.mx_gemm_layout.argtypes = [P, i32, P, i32, P, i32, P, i32, i64, i64, i64, P, i32, i64, P]
         L.mx_quantize_dual_panels.argtypes = [P, i64, i64, i64, i32, P, P, i32, i32, u32, P, P, P]
+        f32 = ctypes.c_float
+        L.mx_block_quantize.argtypes = [P, i64, i64, i64, i32, i32, P, i64, P, i64, P]
+        L.mx_block_quantize_dual.argtypes = [P, i64, i64, i64, i32, i32, P, i64, P, i64, i32, P, i64, P, i64, P]
+        L.mx_block_gemm.argtypes = [P, i64, P, i64, i32, P, i64, P, i64, i32, i32, i64, i64, i64, P, i32, i64, P]
+        L.mx_layer_norm.argtypes = [P, i64, i64, i64, P, P, i32, i32, f32, P, i64, P, P, P]
+        L.mx_layer_norm_quantize.argtypes = [P, i64, i64, i64, P, P, i32, i32, f32, i32, P, P, P, P, P]
+        L.mx_layer_norm_block_quantize.argtypes = [P, i64, i64, i64, P, P, i32, i32, f32, i32, P, i64, P, i64, P, P, P]
+        L.mx_layer_norm_backward.argtypes = [P, i64, P, i64, i64, i64, P, i32, i32, P, P, P, i64, P, P, P, i64, P]
+        L.mx_layer_norm_backward_workspace.argtypes = [i64, i64]
+        L.mx_layer_norm_backward_workspace.restype = i64
+        for fn in (L.mx_block_quantize, L.mx_block_quantize_dual, L.mx_block_gemm, L.mx_layer_norm,
+                   L.mx_layer_norm_quantize, L.mx_layer_norm_block_quantize, L.mx_layer_norm_backward):
+            fn.restype = ctypes.c_int
         for fn in (L.mx_quantize, L.mx_quantize_transpose, L.mx_hadamard32_quantize, L.mx_quantize_dual,
                    L.mx_quantize_transpose_sr, L.mx_quantize_pair, L.mx_gemm, L.mx_quantize_strided,
                    L.mx_gemm_strided, L.mx_quantize_transpose_panels, L.mx_hadamard32_quantize_panels,
@@ -337,3 +354,233 @@ def gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_codes: torch.Tenso
         _check(lib().mx_gemm_strided(_ptr(a_codes), lds[0], _ptr(a_scales), lds[1], fa_, _ptr(b_codes), lds[2],
                                      _ptr(b_scales), lds[3], fb_, M, N, K, _ptr(out), o, ldc, _stream(dev, stream)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# block-128 FP8 operands and the norm in front of a linear layer
+
+BLOCK = 128
+_BLOCK_MODES = {"row": 0, "transpose": 1, "tile": 2, "tile_transpose": 3}
+_NO_SCOPE = contextlib.nullcontext()
+
+
+def _scope(device: torch.device, stream):
+    """What a call allocates and launches in: the operands' device and, if one is given, the
+    stream (so that the memory of the outputs and the workspace belongs to the stream that
+    writes it)."""
+    if stream is None:
+        return _NO_SCOPE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _current(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _fp8(f: Union[str, int]) -> int:
+    f = _fmt(f)
+    if f == E2M1:
+        raise ValueError("block-128 operands are e4m3 or e5m2")
+    return f
+
+
+def _cdiv(a: int, b: int) -> int:
+    return -(-a // b)
+
+
+def _ld(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _rows_of(t: torch.Tensor, dtype: torch.dtype, shape, device, what: str) -> int:
+    """the row stride (elements) of a [rows x width] tensor with contiguous rows"""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError("%s must be %s of shape %s on %s" % (what, dtype, tuple(shape), device))
+    if t.shape[1] > 1 and t.shape[0] > 0 and t.stride(1) != 1:
+        raise ValueError("the rows of %s must be contiguous" % what)
+    return _ld(t)
+
+
+def _block_outputs(device, n: int, k: int, tile: bool, out):
+    """codes [n x k] (rows padded to a multiple of 16 bytes) and scales [blocks of k x n or tiles of n]"""
+    ns = _cdiv(n, BLOCK) if tile else n
+    if out is None:
+        pitch = _cdiv(k, 16) * 16
+        codes = torch.empty((n, pitch), dtype=torch.uint8, device=device)
+        return (codes if pitch == k else codes[:, :k]), torch.empty((_cdiv(k, BLOCK), ns), dtype=torch.float32, device=device)
+    codes, scales = out
+    _rows_of(codes, torch.uint8, (n, k), device, "codes")
+    _rows_of(scales, torch.float32, (_cdiv(k, BLOCK), ns), device, "scales")
+    return codes, scales
+
+
+def block_quantize(x: torch.Tensor, fmt, mode: str = "row", out=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """mx_block_quantize: FP8 codes (uint8) with one fp32 scale for each block of 128.
+    mode "row": blocks along the last dim, codes [R x C], scales [ceil(C/128) x R];
+    "transpose": blocks along dim 0, codes [C x R], scales [ceil(R/128) x C]; "tile" and
+    "tile_transpose": 128 x 128 tiles, scales [ceil(C/128) x ceil(R/128)] or its transpose.
+    `out` = (codes, scales) may have strided rows."""
+    _check_bf16_2d(x)
+    f = _fp8(fmt)
+    if mode not in _BLOCK_MODES:
+        raise ValueError("mode must be one of %s" % sorted(_BLOCK_MODES))
+    rows, cols = x.shape
+    n, k = (cols, rows) if mode.endswith("transpose") else (rows, cols)
+    with _scope(x.device, stream):
+        codes, scales = _block_outputs(x.device, n, k, mode.startswith("tile"), out)
+        _check(lib().mx_block_quantize(_ptr(x), rows, cols, _ldx(x), f, _BLOCK_MODES[mode], _ptr(codes), _ld(codes),
+                                       _ptr(scales), _ld(scales), _current(x.device)))
+    return codes, scales
+
+
+def block_quantize_dual(x: torch.Tensor, fmt_row, fmt_t, tile: bool = False, out=None,
+                        stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """mx_block_quantize_dual: (codes, scales, codes_t, scales_t) from one read of x, as
+    block_quantize(x, fmt_row, "row") and (x, fmt_t, "transpose") give them, or with tile as
+    "tile" and "tile_transpose" do.  `out` is a 4-tuple of output tensors."""
+    _check_bf16_2d(x)
+    fr, ft = _fp8(fmt_row), _fp8(fmt_t)
+    rows, cols = x.shape
+    with _scope(x.device, stream):
+        cr, sr = _block_outputs(x.device, rows, cols, tile, None if out is None else out[:2])
+        ct, st = _block_outputs(x.device, cols, rows, tile, None if out is None else out[2:])
+        _check(lib().mx_block_quantize_dual(_ptr(x), rows, cols, _ldx(x), 1 if tile else 0, fr, _ptr(cr), _ld(cr),
+                                            _ptr(sr), _ld(sr), ft, _ptr(ct), _ld(ct), _ptr(st), _ld(st),
+                                            _current(x.device)))
+    return cr, sr, ct, st
+
+
+def block_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_codes: torch.Tensor, b_scales: torch.Tensor, fb,
+               out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """mx_block_gemm: C[M x N] = A[M x K] . B[N x K]^T on block-128 operands as block_quantize
+    gives them: A in "row" or "transpose" form (scales [ceil(K/128) x M]), B in one of these or in
+    tiles (scales [ceil(K/128) x ceil(N/128)]).  Any sizes; rows may be strided.  float32 output:
+    exact products, fp32 sums.  bfloat16 output: the FP8 matrix instruction, whose sums of 32
+    products are good to 2^-13 of the largest (include/mx.h)."""
+    f_a, f_b = _fp8(fa), _fp8(fb)
+    if a_codes.dim() != 2 or b_codes.dim() != 2 or a_scales.dim() != 2 or b_scales.dim() != 2 or not a_codes.is_cuda:
+        raise ValueError("expected 2-D operands on a GPU")
+    dev = a_codes.device
+    (M, K), N = a_codes.shape, b_codes.shape[0]
+    if b_codes.shape[1] != K:
+        raise ValueError("A and B disagree on K")
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    kb, tiles = _cdiv(K, BLOCK), _cdiv(N, BLOCK)
+    tile = b_scales.shape[1] == tiles and tiles != N
+    lda = _rows_of(a_codes, torch.uint8, (M, K), dev, "A's codes")
+    ldb = _rows_of(b_codes, torch.uint8, (N, K), dev, "B's codes")
+    ldsa = _rows_of(a_scales, torch.float32, (kb, M), dev, "A's scales")
+    ldsb = _rows_of(b_scales, torch.float32, (kb, tiles if tile else N), dev, "B's scales")
+    if out is not None:
+        _rows_of(out, out_dtype, (M, N), dev, "out")
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        _check(lib().mx_block_gemm(_ptr(a_codes), lda, _ptr(a_scales), ldsa, f_a, _ptr(b_codes), ldb, _ptr(b_scales),
+                                   ldsb, f_b, 1 if tile else 0, M, N, K, _ptr(out),
+                                   OUT_BF16 if out_dtype == torch.bfloat16 else OUT_F32, _ld(out), _current(dev)))
+    return out
+
+
+def _params(x: torch.Tensor, weight, bias) -> int:
+    """checks weight and bias against x; their type as the library's enum"""
+    for t, what in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        if t.dtype not in (torch.float32, torch.bfloat16) or tuple(t.shape) != (x.shape[1],) or t.device != x.device:
+            raise ValueError("%s must be float32 or bfloat16 of shape (%d,) on %s" % (what, x.shape[1], x.device))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % what)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have the same type")
+    p = weight if weight is not None else bias
+    return OUT_F32 if p is not None and p.dtype == torch.float32 else OUT_BF16
+
+
+def _stats(x: torch.Tensor, rms: bool):
+    rows = x.shape[0]
+    mean = None if rms else torch.empty((rows,), dtype=torch.float32, device=x.device)
+    return mean, torch.empty((rows,), dtype=torch.float32, device=x.device)
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, rms: bool = False, out: Optional[torch.Tensor] = None,
+               stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor], torch.Tensor]:
+    """mx_layer_norm: (y, mean, rstd) of the rows of x (bf16); y is bf16, mean and rstd float32 for
+    layer_norm_backward.  rms: RMS norm, the mean taken as 0 (mean is then None).  weight and
+    bias: float32 or bfloat16, or None."""
+    _check_bf16_2d(x)
+    p = _params(x, weight, bias)
+    rows, cols = x.shape
+    if out is not None:
+        _rows_of(out, torch.bfloat16, (rows, cols), x.device, "out")
+    with _scope(x.device, stream):
+        if out is None:
+            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
+        mean, rstd = _stats(x, rms)
+        _check(lib().mx_layer_norm(_ptr(x), rows, cols, _ldx(x), _ptr(weight), _ptr(bias), p, 1 if rms else 0, eps,
+                                   _ptr(out), _ld(out), _ptr(mean), _ptr(rstd), _current(x.device)))
+    return out, mean, rstd
+
+
+def layer_norm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                        fmt="e4m3", eps: float = 1e-5, rms: bool = False, scaling: str = "block", out=None,
+                        stream=None) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor], torch.Tensor]:
+    """The norm written as a quantized operand: (codes, scales, mean, rstd).  scaling "block"
+    (mx_layer_norm_block_quantize): codes and scales as block_quantize(y, fmt, "row") lays them out;
+    "mx" (mx_layer_norm_quantize): as quantize(y, fmt).  y is not rounded to bf16 in between."""
+    _check_bf16_2d(x)
+    p = _params(x, weight, bias)
+    rows, cols = x.shape
+    if scaling not in ("block", "mx"):
+        raise ValueError("scaling must be 'block' or 'mx'")
+    f = _fp8(fmt) if scaling == "block" else _fmt(fmt)
+    with _scope(x.device, stream):
+        if scaling == "block":
+            codes, scales = _block_outputs(x.device, rows, cols, False, out)
+        else:
+            codes, scales = _outputs(x.device, rows, cols, f, out)
+        mean, rstd = _stats(x, rms)
+        head = (_ptr(x), rows, cols, _ldx(x), _ptr(weight), _ptr(bias), p, 1 if rms else 0, eps, f)
+        if scaling == "block":
+            _check(lib().mx_layer_norm_block_quantize(*head, _ptr(codes), _ld(codes), _ptr(scales), _ld(scales),
+                                                      _ptr(mean), _ptr(rstd), _current(x.device)))
+        else:
+            _check(lib().mx_layer_norm_quantize(*head, _ptr(codes), _ptr(scales), _ptr(mean), _ptr(rstd),
+                                                _current(x.device)))
+    return codes, scales, mean, rstd
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: Optional[torch.Tensor],
+                        rstd: torch.Tensor, rms: bool = False, weight_grad: bool = True, bias_grad: bool = True,
+                        out: Optional[torch.Tensor] = None, stream=None):
+    """mx_layer_norm_backward: (dx, dweight, dbias) for the output gradient dy (bf16) of
+    layer_norm or layer_norm_quantize, with the mean and rstd they returned; dx is bf16,
+    dweight and dbias float32, None where not asked for."""
+    _check_bf16_2d(dy)
+    _check_bf16_2d(x)
+    if dy.shape != x.shape or dy.device != x.device:
+        raise ValueError("dy and x must agree in shape and device")
+    p = _params(x, weight, None)
+    rows, cols = x.shape
+    for t, what in ((None if rms else mean, "mean"), (rstd, "rstd")):
+        if what == "mean" and rms:
+            continue
+        if t is None or t.dtype != torch.float32 or tuple(t.shape) != (rows,) or t.device != x.device or not t.is_contiguous():
+            raise ValueError("%s must be contiguous float32 of shape (%d,) on %s" % (what, rows, x.device))
+    if out is not None:
+        _rows_of(out, torch.bfloat16, (rows, cols), x.device, "out")
+    with _scope(x.device, stream):
+        if out is None:
+            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
+        dw = torch.empty((cols,), dtype=torch.float32, device=x.device) if weight_grad else None
+        db = torch.empty((cols,), dtype=torch.float32, device=x.device) if bias_grad else None
+        need = lib().mx_layer_norm_backward_workspace(rows, cols) if weight_grad or bias_grad else 0
+        ws = torch.empty((need,), dtype=torch.uint8, device=x.device) if need else None
+        _check(lib().mx_layer_norm_backward(_ptr(dy), _ldx(dy), _ptr(x), _ldx(x), rows, cols, _ptr(weight), p,
+                                            1 if rms else 0, None if rms else _ptr(mean), _ptr(rstd), _ptr(out), _ld(out),
+                                            _ptr(dw), _ptr(db), _ptr(ws), need, _current(x.device)))
+    return out, dw, db

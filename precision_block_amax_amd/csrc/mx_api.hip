@@ -5,57 +5,14 @@
 // current device is checked to be gfx950 (once per device, cached) and the
 // kernels are launched on the caller's stream.  Nothing is allocated and no
 // call synchronizes.
-#include <atomic>
-#include <string.h>
-
-#include "mx.h"
-#include "mx_internal.h"
+#include "mx_check.h"
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_arch_ok[kMaxDevices];  // 0 unknown, 1 gfx950, 2 other
-
-// An enum parameter's value as the caller passed it.  A C caller may pass any
-// int through an enum type, but in C++ a load of an enum object whose value
-// lies outside its enumerators' range has no defined meaning; the entry
-// points therefore read their enum parameters' bytes as an int and validate
-// that.
-template <class E>
-int raw(const E &e) {
-    static_assert(sizeof(E) == sizeof(int), "the ABI's enums are int-sized");
-    int v;
-    memcpy(&v, &e, sizeof v);
-    return v;
-}
-
-bool fmt_ok(int f) { return f == MX_E4M3 || f == MX_E5M2 || f == MX_E2M1; }
-
-int64_t code_bytes(int64_t n, int fmt) { return fmt == MX_E2M1 ? n / 2 : n; }
+using namespace mx;
 
 // K-panel width in elements: 128 code bytes
 int64_t panel_elems(int fmt) { return fmt == MX_E2M1 ? 256 : 128; }
-
-// half-open byte ranges [p, p + n) overlap
-bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
-    if (n <= 0 || m <= 0) return false;
-    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-    return a < b + (uintptr_t)m && b < a + (uintptr_t)n;
-}
-
-mx_status_t check_device() {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return MX_ERR_HIP;
-    if (dev >= kMaxDevices) return MX_ERR_UNSUPPORTED;
-    int st = g_arch_ok[dev].load(std::memory_order_relaxed);
-    if (st == 0) {
-        hipDeviceProp_t prop;
-        if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return MX_ERR_HIP;
-        st = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-        g_arch_ok[dev].store(st, std::memory_order_relaxed);
-    }
-    return st == 1 ? MX_OK : MX_ERR_UNSUPPORTED;
-}
 
 // shared checks of the three quantizers; `blocked` is the dimension cut into
 // 32-element blocks (cols in row mode, rows in transposed mode)
@@ -78,8 +35,6 @@ mx_status_t check_quant(const void *x, int64_t rows, int64_t cols, int64_t ldx, 
         return MX_ERR_INVALID_ARG;
     return MX_OK;
 }
-
-mx_status_t launched(hipError_t e) { return e == hipSuccess ? MX_OK : MX_ERR_HIP; }
 
 // Two strided row patterns, `rows` rows each: row i of the first covers bytes
 // [p + i * lp, p + i * lp + wp), row j of the second [q + j * lq, q + j * lq + wq).
