@@ -229,8 +229,224 @@ __global__ __launch_bounds__(GNT) void k_block_gemm(BlockGemmArgs g) {
                 block_store4<BF16OUT>(g, m0 + wm * 64 + i * 32 + l32, n0 + wn * 64 + j * 32 + 8 * q + 4 * h, &acc[i][j][4 * q]);
 }
 
+// ---------------------------------------------------------------------------
+// Pipelined kernel: codes and scales straight to LDS, two stages of 128 K.
+//
+// WM x WN waves, each TI x 2 tiles of 32 x 32; two waves on every SIMD.  A
+// stage's loads are issued at the top of the stage before it.  Within a
+// stage the tiles follow one another so that the matrix pipe never waits for
+// the vector one: tile t's instructions go out, and while they run, tile
+// t - 1's sum is added to its accumulators (16 multiply-adds, 64 clocks
+// beside 128 of FP8 matrix work).  The last tile's sum is added in the next
+// stage.  The next row of A fragments is read from LDS meanwhile.
+template <int N>
+__device__ __forceinline__ void dma4(pipe::v4i r, void *lds, int voff, int soff) {
+    // N dwords per lane to LDS, as pipe::dma16
+    static_assert(N == 1, "one dword per lane");
+    const uint32_t m = (uint32_t)(uintptr_t)(pipe::lds_t)lds;
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dword %0, %2, %3 offen lds"
+                 :
+                 : "v"(voff), "s"(m), "s"(r), "s"(soff)
+                 : "memory", "m0");
+}
+
+constexpr int kDead = (int)0x80000000u;  // a lane offset beyond every buffer: the load writes zeros
+
+template <int FA, int FB, bool BT, bool BF16OUT, int TI, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_block_gemm_pipe(BlockGemmArgs g) {
+    constexpr int NW = WM * WN, PM = WM * TI * 32, PN = WN * 64;
+    constexpr int NIA = PM / 8 / NW, NIB = PN / 8 / NW;  // 1 KiB loads (8 rows) per wave and stage
+    static_assert(NIA >= 1 && NIB >= 1 && PM % (8 * NW) == 0 && PN % (8 * NW) == 0, "load split");
+    static_assert((PM + PN) / 64 <= NW, "one scale load per wave");
+    constexpr int ST = (PM + PN) * kBlk;
+    // A's two stages of codes, then B's: every fragment read is one of eight lane offsets (four
+    // 32-byte steps of K, two operands) and a constant below 2^16
+    constexpr int OB = 2 * PM * kBlk;
+    __shared__ __attribute__((aligned(16))) uint8_t sC[2 * ST];
+    __shared__ __attribute__((aligned(16))) float sS[2][PM + PN];        // and of scales
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN, l32 = lane & 31, h = lane >> 5;
+    int tm, tn;
+    block_tile_of(g, tm, tn);
+    const int m0 = tm * PM, n0 = tn * PN;
+    const int nk = (g.K + kBlk - 1) / kBlk, ktail = g.K - (nk - 1) * kBlk;  // ktail a multiple of 16
+    const int mrows = min(PM, g.M - m0), nrows = min(PN, g.N - n0);
+    const int lda = (int)g.lda, ldb = (int)g.ldb;
+    const pipe::v4i rA = pipe::rsrc(g.a + (int64_t)m0 * lda, (uint32_t)mrows * lda);
+    const pipe::v4i rB = pipe::rsrc(g.b + (int64_t)n0 * ldb, (uint32_t)nrows * ldb);
+
+    // lane l of a load fills 16-byte slot l % 8 of row l / 8 of its 8 rows, i.e. logical chunk
+    // (l % 8) ^ key(row); the key of the rows of odd loads differs in bit 2.  In K's last stage
+    // the chunks past K are dead, in a stage past it all are.
+    const int rowA = wave * NIA * 8 + lane / 8, rowB = wave * NIB * 8 + lane / 8;
+    int vA[2], vB[2];
+    bool inA[2], inB[2];  // the chunk lies before the end of K in the last stage
+#pragma unroll
+    for (int o = 0; o < 2; o++) {
+        const int ca = ((lane & 7) ^ swz_key<128>(rowA + 8 * o)) << 4, cb = ((lane & 7) ^ swz_key<128>(rowB + 8 * o)) << 4;
+        vA[o] = rowA * lda + ca;
+        vB[o] = rowB * ldb + cb;
+        inA[o] = ca < ktail;
+        inB[o] = cb < ktail;
+    }
+    // scales: wave w < PM / 64 loads those of A's rows 64 w .., the next PN / 64 waves those of B's rows
+    constexpr int WA = PM / 64, WB = PN / 64;
+    const bool isA = wave < WA;
+    const int sw = isA ? wave : (wave - WA) % WB;
+    const float *sbase = isA ? g.as + m0 : g.bs + (BT ? n0 / kBlk : n0);
+    const int64_t lds_ = isA ? g.ldsa : g.ldsb;
+    const int swidth = isA ? mrows : (BT ? (nrows + kBlk - 1) / kBlk : nrows);
+    const pipe::v4i rS = pipe::rsrc(sbase, (uint32_t)(((int64_t)(nk - 1) * lds_ + swidth) * 4));
+    const int srow = 64 * sw + lane;
+    const int vS = (isA || !BT ? srow : srow / kBlk) * 4;
+    float *const sdst = sS[0] + (isA ? 0 : PM) + 64 * sw;
+
+    const auto issue = [&](int u, int kt) {
+        const bool live = kt < nk, last = kt == nk - 1;
+        const int so = live ? kt * kBlk : 0;
+        uint8_t *const dA = sC + u * PM * kBlk + wave * NIA * 1024, *const dB = sC + OB + u * PN * kBlk + wave * NIB * 1024;
+        int a[2], b[2];
+#pragma unroll
+        for (int o = 0; o < 2; o++) {
+            a[o] = live && (!last || inA[o]) ? vA[o] : kDead;
+            b[o] = live && (!last || inB[o]) ? vB[o] : kDead;
+        }
+#pragma unroll
+        for (int q = 0; q < NIA; q++) pipe::dma16(rA, dA + q * 1024, a[q & 1], so + q * 8 * lda);
+#pragma unroll
+        for (int q = 0; q < NIB; q++) pipe::dma16(rB, dB + q * 1024, b[q & 1], so + q * 8 * ldb);
+        dma4<1>(rS, sdst + u * (PM + PN), live ? vS : kDead, live ? kt * (int)lds_ * 4 : 0);
+    };
+
+    float acc[TI][2][16];
+#pragma unroll
+    for (int i = 0; i < TI; i++)
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+#pragma unroll
+            for (int r = 0; r < 16; r++) acc[i][j][r] = 0.f;
+
+    const auto promote = [&](float (&c)[16], const v16f &p, float s) {
+#pragma unroll
+        for (int r = 0; r < 16; r++) c[r] = __builtin_fmaf(p[r], s, c[r]);
+    };
+    v16f pp = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // sum of the tile before
+    float ps = 0.f;                                                                                // its scale
+
+    // lane offsets of the fragments' chunks 2 q + h; rows 32 apart share the key
+    const uint8_t *pa[4], *pb[4];
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        const int ch = ((2 * q + h) ^ swz_key<128>(l32)) << 4;
+        pa[q] = sC + (wm * TI * 32 + l32) * kBlk + ch;
+        pb[q] = sC + OB + (wn * 64 + l32) * kBlk + ch;
+    }
+    const auto frag = [](const uint8_t *const (&p)[4], int off) {
+        Frag f;
+#pragma unroll
+        for (int q = 0; q < 4; q++) f.c[q] = *reinterpret_cast<const uint4 *>(p[q] + off);
+        return f;
+    };
+
+    issue(0, 0);
+    for (int kt0 = 0; kt0 < nk; kt0 += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            pipe::wait_vm<0>();
+            pipe::barrier();
+            const float *const ss = sS[u];
+            Frag fb[2], fa[2];
+            fa[0] = frag(pa, u * PM * kBlk);
+#pragma unroll
+            for (int j = 0; j < 2; j++) fb[j] = frag(pb, u * PN * kBlk + j * 32 * kBlk);
+            float sa[TI];
+#pragma unroll
+            for (int i = 0; i < TI; i++) sa[i] = ss[wm * TI * 32 + i * 32 + l32];
+            const float sbt = ss[PM + wn * 64];
+            issue(u ^ 1, kt0 + u + 1);
+            static_for<0, 2 * TI>([&](auto tt) {
+                constexpr int t = decltype(tt)::value, i = t / 2, j = t % 2;
+                if constexpr (j == 0 && i + 1 < TI) fa[(i + 1) & 1] = frag(pa, u * PM * kBlk + (i + 1) * 32 * kBlk);
+                const v16f p = block_fp8<FA, FB>(fa[i & 1], fb[j]);
+                __builtin_amdgcn_sched_barrier(0);
+                constexpr int pi = t ? (t - 1) / 2 : TI - 1, pj = t ? (t - 1) % 2 : 1;
+                promote(acc[pi][pj], pp, ps);
+                pp = p;
+                ps = sa[i] * sbt;
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        }
+    }
+    promote(acc[TI - 1][1], pp, ps);
+    pipe::wait_vm<0>();
+    pipe::barrier();  // every wave has left the loop: the stages' LDS is free
+
+    // C through LDS, each wave its own part, TI2 x 32 rows at a time, so that rows leave as runs of 64
+    // elements; 16-byte chunks are XOR-swizzled by the row
+    constexpr int ESZ = BF16OUT ? 2 : 4, ROWB = 64 * ESZ, CPR = ROWB / 16, REG = 2 * ST / NW;
+    constexpr int TI2 = TI * 32 * ROWB <= REG ? TI : TI / 2;
+    static_assert(TI2 >= 1 && TI % TI2 == 0 && TI2 * 32 * ROWB <= REG, "staging");
+    uint8_t *const reg = sC + wave * REG;
+    const int mbase = m0 + wm * TI * 32, nbase = n0 + wn * 64;
+    const bool vec = nbase + 64 <= g.N && g.ldc % (16 / ESZ) == 0 && ((uintptr_t)g.c & 15) == 0;
+#pragma unroll
+    for (int pass = 0; pass < TI / TI2; pass++) {
+#pragma unroll
+        for (int ii = 0; ii < TI2; ii++) {
+            const int m = ii * 32 + l32;
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    const float *v = &acc[pass * TI2 + ii][j][4 * q];
+                    if constexpr (BF16OUT)
+                        *reinterpret_cast<uint2 *>(&reg[m * ROWB + (((4 * j + q) ^ (m & 7)) << 4) + 8 * h]) =
+                            make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+                    else
+                        *reinterpret_cast<float4 *>(&reg[m * ROWB + (((8 * j + 2 * q + h) ^ (m & 15)) << 4)]) =
+                            make_float4(v[0], v[1], v[2], v[3]);
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < TI2 * 32 * CPR / 64; k++) {
+            const int m = k * (64 / CPR) + lane / CPR, c = lane % CPR;
+            const uint4 t = *reinterpret_cast<const uint4 *>(&reg[m * ROWB + ((c ^ (m & (CPR - 1))) << 4)]);
+            const int gm = mbase + pass * TI2 * 32 + m, gn = nbase + c * (16 / ESZ);
+            if (gm >= g.M) continue;
+            uint8_t *const d = reinterpret_cast<uint8_t *>(g.c) + ((int64_t)gm * g.ldc + gn) * ESZ;
+            if (vec) {
+                typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+                __builtin_nontemporal_store(u32x4{t.x, t.y, t.z, t.w}, reinterpret_cast<u32x4 *>(d));
+            } else {
+                const uint32_t w4[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                for (int e = 0; e < 16 / ESZ; e++) {
+                    if (gn + e >= g.N) break;
+                    if constexpr (BF16OUT) reinterpret_cast<uint16_t *>(d)[e] = (uint16_t)(w4[e >> 1] >> (16 * (e & 1)));
+                    else reinterpret_cast<uint32_t *>(d)[e] = w4[e];
+                }
+            }
+        }
+    }
+}
+
 template <int FA, int FB, bool BT, bool BF16OUT>
 hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
+    // the pipelined kernel: whole 16-byte chunks of K, aligned rows, offsets in 31 bits
+    const int64_t nk = (g.K + kBlk - 1) / kBlk, lim = (int64_t)1 << 31;
+    const bool pipelined = g.K % 16 == 0 && g.lda % 16 == 0 && g.ldb % 16 == 0 && (uintptr_t)g.a % 16 == 0 &&
+                           (uintptr_t)g.b % 16 == 0 && 256 * g.lda < lim && 256 * g.ldb < lim &&
+                           (nk * g.ldsa + 256) * 4 < lim && (nk * g.ldsb + 256) * 4 < lim;
+    if constexpr (BF16OUT && BT) {
+        if (pipelined) {
+            g.tiles_m = (g.M + 255) / 256;
+            g.tiles_n = (g.N + 255) / 256;
+            hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, BF16OUT, 4, 2, 4>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
+                               dim3(512), 0, s, g);
+            return hipGetLastError();
+        }
+    }
     g.tiles_m = (g.M + GB - 1) / GB;
     g.tiles_n = (g.N + GB - 1) / GB;
     hipLaunchKernelGGL((k_block_gemm<FA, FB, BT, BF16OUT>), dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(GNT), 0, s, g);
