@@ -131,7 +131,7 @@ __device__ __forceinline__ uint4 load16(const uint8_t *p, int n) {
 }
 
 template <int FA, int FB, bool BT, bool BF16OUT>
-__global__ __launch_bounds__(GNT) void k_block_gemm(BlockGemmArgs g) {
+__global__ __launch_bounds__(GNT, 2) void k_block_gemm(BlockGemmArgs g) {
     __shared__ __attribute__((aligned(16))) uint8_t sA[2][GB * kBlk], sB[2][GB * kBlk];
     __shared__ __attribute__((aligned(16))) float sS[2][2 * GB];  // A's rows, B's rows
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -230,19 +230,17 @@ __global__ __launch_bounds__(GNT) void k_block_gemm(BlockGemmArgs g) {
 }
 
 // ---------------------------------------------------------------------------
-// Pipelined kernel: codes and scales straight to LDS, two stages of 128 K.
+// Pipelined kernel: codes and scales straight to LDS, a ring of NS stages of
+// 128 K, of which NS - 1 are in flight.
 //
-// WM x WN waves, each TI x 2 tiles of 32 x 32; two waves on every SIMD.  A
-// stage's loads are issued at the top of the stage before it.  Within a
-// stage the tiles follow one another so that the matrix pipe never waits for
-// the vector one: tile t's instructions go out, and while they run, tile
-// t - 1's sum is added to its accumulators (16 multiply-adds, 64 clocks
-// beside 128 of FP8 matrix work).  The last tile's sum is added in the next
-// stage.  The next row of A fragments is read from LDS meanwhile.
-template <int N>
+// WM x WN waves, each TI x 2 tiles of 32 x 32.  Within a stage the tiles follow
+// one another so that the matrix pipe never waits for the vector one: tile t's
+// instructions go out, and while they run, tile t - 1's sum is added to its
+// accumulators (16 multiply-adds, 64 clocks beside 128 of FP8 matrix work) and
+// the next row of A fragments is read from LDS (and, for fp32 output,
+// converted).  The last tile's sum is added in the next stage.
 __device__ __forceinline__ void dma4(pipe::v4i r, void *lds, int voff, int soff) {
-    // N dwords per lane to LDS, as pipe::dma16
-    static_assert(N == 1, "one dword per lane");
+    // one dword per lane to LDS, as pipe::dma16: lane l lands at lds + 4 l
     const uint32_t m = (uint32_t)(uintptr_t)(pipe::lds_t)lds;
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dword %0, %2, %3 offen lds"
                  :
@@ -252,18 +250,28 @@ __device__ __forceinline__ void dma4(pipe::v4i r, void *lds, int voff, int soff)
 
 constexpr int kDead = (int)0x80000000u;  // a lane offset beyond every buffer: the load writes zeros
 
-template <int FA, int FB, bool BT, bool BF16OUT, int TI, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_block_gemm_pipe(BlockGemmArgs g) {
+// configurations: waves, tiles per wave, ring
+struct Cfg256x256 { static constexpr int TI = 4, WM = 2, WN = 4, NS = 2; };
+struct Cfg256x128 { static constexpr int TI = 2, WM = 4, WN = 2, NS = 2; };
+struct Cfg128x128 { static constexpr int TI = 2, WM = 2, WN = 2, NS = 4; };
+
+template <int FA, int FB, bool BT, bool BF16OUT, class CFG>
+__global__ __launch_bounds__(64 * CFG::WM * CFG::WN, CFG::WM * CFG::WN / 4) void k_block_gemm_pipe(BlockGemmArgs g) {
+    constexpr int TI = CFG::TI, WM = CFG::WM, WN = CFG::WN, NS = CFG::NS;
     constexpr int NW = WM * WN, PM = WM * TI * 32, PN = WN * 64;
     constexpr int NIA = PM / 8 / NW, NIB = PN / 8 / NW;  // 1 KiB loads (8 rows) per wave and stage
     static_assert(NIA >= 1 && NIB >= 1 && PM % (8 * NW) == 0 && PN % (8 * NW) == 0, "load split");
     static_assert((PM + PN) / 64 <= NW, "one scale load per wave");
-    constexpr int ST = (PM + PN) * kBlk;
-    // A's two stages of codes, then B's: every fragment read is one of eight lane offsets (four
-    // 32-byte steps of K, two operands) and a constant below 2^16
-    constexpr int OB = 2 * PM * kBlk;
-    __shared__ __attribute__((aligned(16))) uint8_t sC[2 * ST];
-    __shared__ __attribute__((aligned(16))) float sS[2][PM + PN];        // and of scales
+    static_assert((NS & (NS - 1)) == 0, "ring");
+    constexpr int LPW = NIA + NIB + 1;                   // loads of a wave per stage
+    constexpr int ST = (PM + PN) * kBlk, SR = 2 * NS;
+    // A's stages of codes, then B's: a fragment read is one of eight lane offsets (four 32-byte
+    // steps of K, two operands), the stage's place and a constant
+    constexpr int OB = NS * PM * kBlk;
+    __shared__ __attribute__((aligned(16))) uint8_t sC[NS * ST];
+    // scales, in a ring of their own: the last tile of a stage is scaled in the next one, while the
+    // loads that reuse the stage's codes are under way
+    __shared__ __attribute__((aligned(16))) float sS[SR * (PM + PN)];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN, l32 = lane & 31, h = lane >> 5;
@@ -291,6 +299,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_block_gemm_pipe(BlockGemmAr
         inB[o] = cb < ktail;
     }
     // scales: wave w < PM / 64 loads those of A's rows 64 w .., the next PN / 64 waves those of B's rows
+    // (waves beyond repeat them)
     constexpr int WA = PM / 64, WB = PN / 64;
     const bool isA = wave < WA;
     const int sw = isA ? wave : (wave - WA) % WB;
@@ -300,9 +309,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_block_gemm_pipe(BlockGemmAr
     const pipe::v4i rS = pipe::rsrc(sbase, (uint32_t)(((int64_t)(nk - 1) * lds_ + swidth) * 4));
     const int srow = 64 * sw + lane;
     const int vS = (isA || !BT ? srow : srow / kBlk) * 4;
-    float *const sdst = sS[0] + (isA ? 0 : PM) + 64 * sw;
+    float *const sdst = sS + (isA ? 0 : PM) + 64 * sw;
 
-    const auto issue = [&](int u, int kt) {
+    const auto issue = [&](int u, int kt) {  // stage kt into place u
         const bool live = kt < nk, last = kt == nk - 1;
         const int so = live ? kt * kBlk : 0;
         uint8_t *const dA = sC + u * PM * kBlk + wave * NIA * 1024, *const dB = sC + OB + u * PN * kBlk + wave * NIB * 1024;
@@ -316,7 +325,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_block_gemm_pipe(BlockGemmAr
         for (int q = 0; q < NIA; q++) pipe::dma16(rA, dA + q * 1024, a[q & 1], so + q * 8 * lda);
 #pragma unroll
         for (int q = 0; q < NIB; q++) pipe::dma16(rB, dB + q * 1024, b[q & 1], so + q * 8 * ldb);
-        dma4<1>(rS, sdst + u * (PM + PN), live ? vS : kDead, live ? kt * (int)lds_ * 4 : 0);
+        dma4(rS, sdst + (kt & (SR - 1)) * (PM + PN), live ? vS : kDead, live ? kt * (int)lds_ * 4 : 0);
     };
 
     float acc[TI][2][16];
@@ -327,12 +336,35 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_block_gemm_pipe(BlockGemmAr
 #pragma unroll
             for (int r = 0; r < 16; r++) acc[i][j][r] = 0.f;
 
-    const auto promote = [&](float (&c)[16], const v16f &p, float s) {
-#pragma unroll
-        for (int r = 0; r < 16; r++) c[r] = __builtin_fmaf(p[r], s, c[r]);
-    };
     v16f pp = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // sum of the tile before
-    float ps = 0.f;                                                                                // its scale
+    float ps = 0.f;                                                                                // its scale (A's, without BT)
+    const int scol = PM + wn * 64 + (BT ? 0 : 4 * h);
+    // without BT: the scales of its columns.  There is no tile before the first: its sum is 0 and so
+    // are its scales, in the place that the ring fills last.
+    const float *psb = sS + (SR - 1) * (PM + PN) + scol;
+    if constexpr (!BT) {
+        for (int i = tid; i < PN; i += 64 * NW) sS[(SR - 1) * (PM + PN) + PM + i] = 0.f;
+    }
+    // acc += scale * sum of the tile before
+    const auto promote = [&](float (&c)[16], const float4 (&sb)[4]) {
+        if constexpr (BT) {
+#pragma unroll
+            for (int r = 0; r < 16; r++) c[r] = __builtin_fmaf(pp[r], ps, c[r]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const float s4[4] = {sb[q].x, sb[q].y, sb[q].z, sb[q].w};
+#pragma unroll
+                for (int e = 0; e < 4; e++) c[4 * q + e] = __builtin_fmaf(pp[4 * q + e], ps * s4[e], c[4 * q + e]);
+            }
+        }
+    };
+    const auto read_sb = [&](float4 (&sb)[4]) {
+        if constexpr (!BT) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) sb[q] = *reinterpret_cast<const float4 *>(psb + 8 * q);
+        }
+    };
 
     // lane offsets of the fragments' chunks 2 q + h; rows 32 apart share the key
     const uint8_t *pa[4], *pb[4];
@@ -349,42 +381,68 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_block_gemm_pipe(BlockGemmAr
         return f;
     };
 
-    issue(0, 0);
-    for (int kt0 = 0; kt0 < nk; kt0 += 2) {
+    const auto stage = [&](int u, int kt) {
+        pipe::wait_vm<(NS - 2) * LPW>();
+        pipe::barrier();
+        const float *const ss = sS + (kt & (SR - 1)) * (PM + PN);
+        const int ua = u * PM * kBlk, ub = u * PN * kBlk;
+        Frag fa[2], fb[2];
+        Frag16 ga, gb[2];
+        fa[0] = frag(pa, ua);
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-            pipe::wait_vm<0>();
-            pipe::barrier();
-            const float *const ss = sS[u];
-            Frag fb[2], fa[2];
-            fa[0] = frag(pa, u * PM * kBlk);
+        for (int j = 0; j < 2; j++) fb[j] = frag(pb, ub + j * 32 * kBlk);
+        float sa[TI];
 #pragma unroll
-            for (int j = 0; j < 2; j++) fb[j] = frag(pb, u * PN * kBlk + j * 32 * kBlk);
-            float sa[TI];
+        for (int i = 0; i < TI; i++) sa[i] = ss[wm * TI * 32 + i * 32 + l32];
+        const float sbt = BT ? ss[scol] : 1.0f;
+        issue((u + NS - 1) & (NS - 1), kt + NS - 1);
+        if constexpr (!BF16OUT) {
+            ga = to_bf16<FA>(fa[0]);
 #pragma unroll
-            for (int i = 0; i < TI; i++) sa[i] = ss[wm * TI * 32 + i * 32 + l32];
-            const float sbt = ss[PM + wn * 64];
-            issue(u ^ 1, kt0 + u + 1);
-            static_for<0, 2 * TI>([&](auto tt) {
-                constexpr int t = decltype(tt)::value, i = t / 2, j = t % 2;
-                if constexpr (j == 0 && i + 1 < TI) fa[(i + 1) & 1] = frag(pa, u * PM * kBlk + (i + 1) * 32 * kBlk);
-                const v16f p = block_fp8<FA, FB>(fa[i & 1], fb[j]);
-                __builtin_amdgcn_sched_barrier(0);
-                constexpr int pi = t ? (t - 1) / 2 : TI - 1, pj = t ? (t - 1) % 2 : 1;
-                promote(acc[pi][pj], pp, ps);
-                pp = p;
-                ps = sa[i] * sbt;
-                __builtin_amdgcn_sched_barrier(0);
-            });
+            for (int j = 0; j < 2; j++) gb[j] = to_bf16<FB>(fb[j]);
         }
+        static_for<0, 2 * TI>([&](auto tt) {
+            constexpr int t = decltype(tt)::value, i = t / 2, j = t % 2;
+            constexpr int pi = t ? (t - 1) / 2 : TI - 1, pj = t ? (t - 1) % 2 : 1;  // the tile before
+            if constexpr (j == 0 && i + 1 < TI) fa[(i + 1) & 1] = frag(pa, ua + (i + 1) * 32 * kBlk);
+            float4 sb[4];
+            read_sb(sb);
+            v16f p;
+            if constexpr (BF16OUT) p = block_fp8<FA, FB>(fa[i & 1], fb[j]);
+            else p = block_bf16(ga, gb[j]);
+            __builtin_amdgcn_sched_barrier(0);
+            promote(acc[pi][pj], sb);
+            if constexpr (!BF16OUT && j == 1 && i + 1 < TI) ga = to_bf16<FA>(fa[(i + 1) & 1]);
+            pp = p;
+            ps = BT ? sa[i] * sbt : sa[i];
+            psb = ss + scol + j * 32;
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+
+#pragma unroll
+    for (int u = 0; u < NS - 1; u++) issue(u, u);
+    if constexpr (NS == 2) {
+        // two stages at a time, so that their places are constants; with an odd number of them the
+        // last one is all zeros
+        for (int kt = 0; kt < nk; kt += 2) {
+            stage(0, kt);
+            stage(1, kt + 1);
+        }
+    } else {
+        for (int kt = 0; kt < nk; kt++) stage(kt & (NS - 1), kt);
     }
-    promote(acc[TI - 1][1], pp, ps);
+    {
+        float4 sb[4];
+        read_sb(sb);
+        promote(acc[TI - 1][1], sb);
+    }
     pipe::wait_vm<0>();
     pipe::barrier();  // every wave has left the loop: the stages' LDS is free
 
     // C through LDS, each wave its own part, TI2 x 32 rows at a time, so that rows leave as runs of 64
     // elements; 16-byte chunks are XOR-swizzled by the row
-    constexpr int ESZ = BF16OUT ? 2 : 4, ROWB = 64 * ESZ, CPR = ROWB / 16, REG = 2 * ST / NW;
+    constexpr int ESZ = BF16OUT ? 2 : 4, ROWB = 64 * ESZ, CPR = ROWB / 16, REG = NS * ST / NW;
     constexpr int TI2 = TI * 32 * ROWB <= REG ? TI : TI / 2;
     static_assert(TI2 >= 1 && TI % TI2 == 0 && TI2 * 32 * ROWB <= REG, "staging");
     uint8_t *const reg = sC + wave * REG;
@@ -431,6 +489,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_block_gemm_pipe(BlockGemmAr
     }
 }
 
+template <int FA, int FB, bool BT, bool BF16OUT, class CFG>
+hipError_t launch_block_gemm_pipe(BlockGemmArgs g, hipStream_t s) {
+    constexpr int PM = CFG::WM * CFG::TI * 32, PN = CFG::WN * 64;
+    g.tiles_m = (g.M + PM - 1) / PM;
+    g.tiles_n = (g.N + PN - 1) / PN;
+    hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, BF16OUT, CFG>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
+                       dim3(64 * CFG::WM * CFG::WN), 0, s, g);
+    return hipGetLastError();
+}
+
 template <int FA, int FB, bool BT, bool BF16OUT>
 hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
     // the pipelined kernel: whole 16-byte chunks of K, aligned rows, offsets in 31 bits
@@ -438,14 +506,11 @@ hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
     const bool pipelined = g.K % 16 == 0 && g.lda % 16 == 0 && g.ldb % 16 == 0 && (uintptr_t)g.a % 16 == 0 &&
                            (uintptr_t)g.b % 16 == 0 && 256 * g.lda < lim && 256 * g.ldb < lim &&
                            (nk * g.ldsa + 256) * 4 < lim && (nk * g.ldsb + 256) * 4 < lim;
-    if constexpr (BF16OUT && BT) {
-        if (pipelined) {
-            g.tiles_m = (g.M + 255) / 256;
-            g.tiles_n = (g.N + 255) / 256;
-            hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, BF16OUT, 4, 2, 4>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
-                               dim3(512), 0, s, g);
-            return hipGetLastError();
-        }
+    if (pipelined) {
+        const int64_t t256 = (int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256);
+        if (t256 < 256) return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg128x128>(g, s);
+        if constexpr (BF16OUT && BT) return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg256x256>(g, s);
+        else return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg256x128>(g, s);
     }
     g.tiles_m = (g.M + GB - 1) / GB;
     g.tiles_n = (g.N + GB - 1) / GB;

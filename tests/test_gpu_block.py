@@ -239,6 +239,16 @@ def test_gemm_nan_scales(mx, M, bf16):
     c = mx.block_gemm(*a, "e4m3", *bt, "e4m3", out_dtype=dt)
     want[:, 0:128] = True
     assert torch.equal(c.isnan(), want)
+    # every row and column in turn at the edges of the kernels' tiles, in the first and in the last block
+    for m in {0, 4, 31, 63, 130} & set(range(M)):
+        for blk in (0, 4):
+            a, b = mx.block_quantize(data(M, K, 5), "e4m3"), mx.block_quantize(data(N, K, 6), "e4m3")
+            a[1][blk, m], b[1][blk, 299 - m] = float("nan"), float("inf")
+            c = mx.block_gemm(*a, "e4m3", *b, "e4m3", out_dtype=dt)
+            assert c[m].isnan().all() and not c[:, 299 - m].isfinite().any()
+            rest = torch.ones(M, N, dtype=torch.bool, device="cuda")
+            rest[m], rest[:, 299 - m] = False, False
+            assert c[rest].isfinite().all()
 
 
 @pytest.mark.parametrize("M,N", [(1, 64), (40, 64), (300, 256)])
