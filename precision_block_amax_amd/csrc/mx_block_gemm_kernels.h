@@ -90,6 +90,7 @@ __device__ __forceinline__ v16f block_fp8(const Frag &a, const Frag &b) {
     return p;
 }
 
+typedef float v4f __attribute__((ext_vector_type(4)));
 struct Frag16 {
     v8bf v[8];
 };
@@ -489,6 +490,159 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, CFG::WM * CFG::WN / 4) void
     }
 }
 
+// ---------------------------------------------------------------------------
+// Direct kernel, for few rows: 16 MT x 16 NT of C per workgroup, its eight
+// waves each taking every eighth block of K for the whole tile, fragments
+// straight from memory to registers, the waves' sums joined in LDS.  Any
+// alignment and K.
+//
+// With one row the product is bound by B's bytes; 16 rows of B per workgroup
+// give 256 workgroups from N = 4096 on, and eight waves each with the loads of
+// U blocks in flight (2 KiB of B per block and wave) cover the latency without
+// a split of K over workgroups, which would need memory to join them.
+constexpr int DW = 8;
+
+struct Frag2 {
+    uint4 c[2];
+};
+// bytes [32 h, 32 h + 32) of the block's 128 at p; without FULL, n bytes are left of the row there
+template <bool FULL>
+__device__ __forceinline__ Frag2 direct_frag(const uint8_t *p, int h, int n) {
+    Frag2 f;
+    if constexpr (FULL) {
+        __builtin_memcpy(&f, p + 32 * h, 32);
+    } else {
+        f.c[0] = load16(p + 32 * h, n - 32 * h);
+        f.c[1] = load16(p + 32 * h + 16, n - 32 * h - 16);
+    }
+    return f;
+}
+
+template <int FA, int FB, bool BF16OUT>
+__device__ __forceinline__ v4f direct_block(const Frag2 &a, const Frag2 &b) {
+    v4f p = {0.f, 0.f, 0.f, 0.f};
+    const uint4 x = a.c[0], y = a.c[1], u = b.c[0], v = b.c[1];
+    if constexpr (BF16OUT) {
+        p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)v.x, (int)v.y, (int)v.z, (int)v.w},
+            v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w}, p, FB, FA, 0, 0, 0, 0);
+    } else {
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(u.x, u.y, 1.f), to_bf16x8<FA>(x.x, x.y, 1.f), p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(u.z, u.w, 1.f), to_bf16x8<FA>(x.z, x.w, 1.f), p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(v.x, v.y, 1.f), to_bf16x8<FA>(y.x, y.y, 1.f), p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(v.z, v.w, 1.f), to_bf16x8<FA>(y.z, y.w, 1.f), p, 0, 0, 0);
+    }
+    return p;
+}
+
+template <int FA, int FB, bool BT, bool BF16OUT, int MT, int NT, int U>
+__global__ __launch_bounds__(64 * DW) void k_block_gemm_direct(BlockGemmArgs g) {
+    constexpr int DM = 16 * MT, DN = 16 * NT;
+    __shared__ __attribute__((aligned(16))) float sJ[DW][DM][DN + 4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int l16 = lane & 15, h = lane >> 4;
+    int tm, tn;
+    block_tile_of(g, tm, tn);
+    const int m0 = tm * DM, n0 = tn * DN;
+    const int nk = (g.K + kBlk - 1) / kBlk;
+    // rows past the edge repeat the last one; their results are not stored
+    const uint8_t *pa[MT], *pb[NT];
+    const float *qa[MT], *qb[NT];
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+        const int m = min(m0 + 16 * i + l16, g.M - 1);
+        pa[i] = g.a + (int64_t)m * g.lda;
+        qa[i] = g.as + m;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+        pb[j] = g.b + (int64_t)min(n0 + 16 * j + l16, g.N - 1) * g.ldb;
+        // a tiled B: 16 columns lie in one tile; else the scales of this lane's four columns
+        qb[j] = g.bs + (BT ? min(n0 + 16 * j, g.N - 1) / kBlk : n0 + 16 * j + 4 * h);
+    }
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) acc[i][j][r] = 0.f;
+
+    // NB blocks from k0 on, DW apart; FULL: all of them whole, so that their loads go out together
+    const auto run = [&](int k0, auto nb, auto full) {
+        constexpr int NB = decltype(nb)::value;
+        constexpr bool FULL = decltype(full)::value;
+        Frag2 fa[NB][MT], fb[NB][NT];
+        float sa[NB][MT], sb[NB][NT][BT ? 1 : 4];
+#pragma unroll
+        for (int u = 0; u < NB; u++) {
+            const int kt = k0 + u * DW;
+            const int64_t k = (int64_t)kt * kBlk;
+            const int n = FULL ? kBlk : g.K - kt * kBlk;
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+                fb[u][j] = direct_frag<FULL>(pb[j] + k, h, n);
+#pragma unroll
+                for (int r = 0; r < (BT ? 1 : 4); r++)
+                    sb[u][j][r] = BT || n0 + 16 * j + 4 * h + r < g.N ? qb[j][kt * g.ldsb + r] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < MT; i++) {
+                fa[u][i] = direct_frag<FULL>(pa[i] + k, h, n);
+                sa[u][i] = qa[i][kt * g.ldsa];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < NB; u++)
+#pragma unroll
+            for (int i = 0; i < MT; i++)
+#pragma unroll
+                for (int j = 0; j < NT; j++) {
+                    const v4f p = direct_block<FA, FB, BF16OUT>(fa[u][i], fb[u][j]);
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        acc[i][j][r] = __builtin_fmaf(p[r], sa[u][i] * sb[u][j][BT ? 0 : r], acc[i][j][r]);
+                }
+    };
+    using I1 = std::integral_constant<int, 1>;
+    const int nfull = g.K / kBlk;
+    int k0 = wave;
+    for (; k0 + (U - 1) * DW < nfull; k0 += DW * U) run(k0, std::integral_constant<int, U>{}, std::true_type{});
+    for (; k0 < nfull; k0 += DW) run(k0, I1{}, std::true_type{});
+    if (k0 < nk) run(k0, I1{}, std::false_type{});
+
+    // lane: row m = l16 of tile i, columns 4 h .. 4 h + 3 of tile j
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+            *reinterpret_cast<float4 *>(&sJ[wave][16 * i + l16][16 * j + 4 * h]) =
+                make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+    __syncthreads();
+    for (int t = tid; t < DM * DN / 4; t += 64 * DW) {
+        const int m = t / (DN / 4), n = t % (DN / 4) * 4;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < DW; w++) {
+            const float4 x = *reinterpret_cast<const float4 *>(&sJ[w][m][n]);
+            v[0] += x.x;
+            v[1] += x.y;
+            v[2] += x.z;
+            v[3] += x.w;
+        }
+        block_store4<BF16OUT>(g, m0 + m, n0 + n, v);
+    }
+}
+
+template <int FA, int FB, bool BT, bool BF16OUT, int MT, int NT, int U>
+hipError_t launch_block_gemm_direct(BlockGemmArgs g, hipStream_t s) {
+    g.tiles_m = (g.M + 16 * MT - 1) / (16 * MT);
+    g.tiles_n = (g.N + 16 * NT - 1) / (16 * NT);
+    hipLaunchKernelGGL((k_block_gemm_direct<FA, FB, BT, BF16OUT, MT, NT, U>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
+                       dim3(64 * DW), 0, s, g);
+    return hipGetLastError();
+}
+
 template <int FA, int FB, bool BT, bool BF16OUT, class CFG>
 hipError_t launch_block_gemm_pipe(BlockGemmArgs g, hipStream_t s) {
     constexpr int PM = CFG::WM * CFG::TI * 32, PN = CFG::WN * 64;
@@ -501,6 +655,10 @@ hipError_t launch_block_gemm_pipe(BlockGemmArgs g, hipStream_t s) {
 
 template <int FA, int FB, bool BT, bool BF16OUT>
 hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
+    if (g.M <= 16) return launch_block_gemm_direct<FA, FB, BT, BF16OUT, 1, 1, 4>(g, s);
+    if (g.M <= 32) return launch_block_gemm_direct<FA, FB, BT, BF16OUT, 2, 1, 4>(g, s);
+    if (g.M <= 48) return launch_block_gemm_direct<FA, FB, BT, BF16OUT, 3, 1, 2>(g, s);
+    if (g.M <= 64) return launch_block_gemm_direct<FA, FB, BT, BF16OUT, 4, 1, 2>(g, s);
     // the pipelined kernel: whole 16-byte chunks of K, aligned rows, offsets in 31 bits
     const int64_t nk = (g.K + kBlk - 1) / kBlk, lim = (int64_t)1 << 31;
     const bool pipelined = g.K % 16 == 0 && g.lda % 16 == 0 && g.ldb % 16 == 0 && (uintptr_t)g.a % 16 == 0 &&
