@@ -375,7 +375,13 @@ def _scope(device: torch.device, stream):
     return torch.cuda.stream(stream)
 
 
+# the current stream's handle without building a Stream object (0.1 us instead of 2), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _current(device: torch.device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 

@@ -24,13 +24,34 @@ __device__ __forceinline__ void load8_bf16(uint32_t (&w)[4], const uint16_t *p, 
     }
 }
 
+// Vector c .. c + 7 of a row of cols elements at p, zeros past its end and for a row that is not live
+// (p is then any readable row).  A scalar row address and an unsigned 32-bit lane offset make one
+// load without 64-bit vector arithmetic.  WHOLE: cols is a multiple of 8, so a vector lies in the row or past it;
+// the load is unconditional (from the row's last vector where it lies past it) and the zeros a select:
+// a branch per load would keep the loads of a row from going out together.
+template <bool WHOLE>
+__device__ __forceinline__ void load_vec(uint32_t (&w)[4], const uint16_t *p, int c, int cols, bool live) {
+    if constexpr (WHOLE) {
+        __builtin_memcpy(w, reinterpret_cast<const uint8_t *>(p) + 2u * (uint32_t)min(c, cols - 8), 16);
+        const bool in = live && c < cols;
+#pragma unroll
+        for (int k = 0; k < 4; k++) w[k] = in ? w[k] : 0u;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; k++) w[k] = 0u;
+        if (live && c < cols) load8_bf16(w, p + (uint32_t)c, cols - c);
+    }
+}
+
 // the first n of 8 bytes
 __device__ __forceinline__ void store8(uint8_t *p, uint32_t lo, uint32_t hi, int n) {
     if (n >= 8) {
         const uint32_t v[2] = {lo, hi};
         __builtin_memcpy(p, v, 8);
     } else {
-        for (int i = 0; i < n; i++) p[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n) p[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
     }
 }
 

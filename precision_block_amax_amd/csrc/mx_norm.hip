@@ -11,21 +11,35 @@
 // Backward, with xh = (x - mean) * rstd, g = dy * weight:
 //   dx = rstd * (g - mean(g) - xh * mean(g * xh)),
 //   dweight = sum_rows dy * xh, dbias = sum_rows dy.
-// dx takes a row per T threads as above.  The sums over rows are taken in two
-// steps in a fixed order (chunks of rows into the workspace, then the chunks),
-// so that the same inputs give the same bits.
+// One pass: a workgroup takes a chunk of rows, R at a time, each in the
+// registers of T threads, and keeps the parameters' sums of its chunk in
+// registers too (8 U columns per thread); the chunks' sums go through the
+// workspace to a second kernel.  All sums are in a fixed order, so the same
+// inputs give the same bits.
 //
 // All of it is bound by memory: 2 bytes read and 2 (1 for FP8) written per
 // element forward, 4 read and 2 written backward.
+#include <type_traits>
+
 #include "mx_block_util.h"
 
 namespace mx {
 namespace {
 
+// sum over the wave, in every lane: within rows of 16 lanes by DPP (neighbours, pairs, mirrored halves,
+// mirrored row), then row against row and half against half (one swap gives each side both values)
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    return v;
+    const auto dpp = [](float x, auto ctrl) {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(x), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    v += dpp(v, std::integral_constant<int, 0xB1>{});
+    v += dpp(v, std::integral_constant<int, 0x4E>{});
+    v += dpp(v, std::integral_constant<int, 0x141>{});
+    v += dpp(v, std::integral_constant<int, 0x140>{});
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
 // sum over the T threads of a row: T = 64 is one wave; above, the waves meet in `s`
@@ -43,60 +57,59 @@ __device__ __forceinline__ float row_sum(float v, float *s) {
     return v;
 }
 
-// n (up to 8) parameters at index c, as fp32; `other` where there are none
-__device__ __forceinline__ void load_param8(float (&w)[8], const void *p, bool bf16, int c, int n, float other) {
+// parameters c .. c + 7 as fp32; `other` where there are none, anything past cols
+template <bool WHOLE>
+__device__ __forceinline__ void load_param8(float (&w)[8], const void *p, bool bf16, int c, int cols, float other) {
     if (!p) {
 #pragma unroll
         for (int i = 0; i < 8; i++) w[i] = other;
     } else if (bf16) {
         uint32_t t[4];
-        load8_bf16(t, reinterpret_cast<const uint16_t *>(p) + c, n);
+        load_vec<WHOLE>(t, reinterpret_cast<const uint16_t *>(p), c, cols, true);
 #pragma unroll
         for (int i = 0; i < 8; i++) w[i] = (i & 1) ? bf16_hi(t[i >> 1]) : bf16_lo(t[i >> 1]);
     } else {
-        const float *q = reinterpret_cast<const float *>(p) + c;
-        if (n >= 8) {
-            __builtin_memcpy(w, q, 32);
+        const float *q = reinterpret_cast<const float *>(p);
+        if (WHOLE || c + 8 <= cols) {
+            __builtin_memcpy(w, q + min(c, cols - 8), 32);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; i++) w[i] = i < n ? q[i] : 0.f;
+            for (int i = 0; i < 8; i++) w[i] = q[min(c + i, cols - 1)];
         }
     }
 }
 
-__device__ __forceinline__ void store8_bf16(uint16_t *p, const float (&y)[8], int n) {
+// y as bf16 to columns c .. c + 7 of the row at p, those before cols; WHOLE as in load_vec
+template <bool WHOLE>
+__device__ __forceinline__ void store_vec(uint16_t *p, const float (&y)[8], int c, int cols) {
+    typedef float v2f __attribute__((ext_vector_type(2)));
     uint32_t t[4];
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-        typedef float v2f __attribute__((ext_vector_type(2)));
-        t[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{y[2 * k], y[2 * k + 1]}, v2bf));
-    }
-    if (n >= 8) {
-        __builtin_memcpy(p, t, 16);
-    } else {
-        for (int i = 0; i < n; i++) p[i] = (uint16_t)(t[i >> 1] >> (16 * (i & 1)));
+    for (int k = 0; k < 4; k++) t[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{y[2 * k], y[2 * k + 1]}, v2bf));
+    if (WHOLE ? c < cols : c + 8 <= cols) {
+        __builtin_memcpy(reinterpret_cast<uint8_t *>(p) + 2u * (uint32_t)c, t, 16);
+    } else if (!WHOLE) {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (c + i < cols) p[c + i] = (uint16_t)(t[i >> 1] >> (16 * (i & 1)));
     }
 }
 
 // T threads and 8 T U >= cols elements per row; a workgroup of max(T, 256) threads
-template <int T, int U, int TO, int F>
+template <int T, int U, int TO, int F, bool WHOLE>
 __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a) {
     constexpr int NT = T < 256 ? 256 : T, RPW = NT / T;
     __shared__ float s0[NT / 64], s1[NT / 64];
     const int t = threadIdx.x % T;
     const float rn = 1.0f / (float)a.cols;
     for (int64_t row0 = (int64_t)blockIdx.x * RPW; row0 < a.rows; row0 += (int64_t)gridDim.x * RPW) {
-        const int64_t row = row0 + threadIdx.x / T;
+        const int64_t row = row0 + __builtin_amdgcn_readfirstlane(threadIdx.x / T);
         const bool live = row < a.rows;  // with one wave per row the others go on; with more RPW is 1
         float y[U][8];
-        const uint16_t *px = a.x + row * a.ldx;
+        const uint16_t *px = a.x + (live ? row : 0) * a.ldx;
         uint32_t w[U][4];
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int n = a.cols - 8 * (u * T + t);
-            w[u][0] = w[u][1] = w[u][2] = w[u][3] = 0;
-            if (live && n > 0) load8_bf16(w[u], px + 8 * (u * T + t), n);
-        }
+        for (int u = 0; u < U; u++) load_vec<WHOLE>(w[u], px, 8 * (u * T + t), a.cols, live);
         float sum = 0.f;
 #pragma unroll
         for (int u = 0; u < U; u++)
@@ -130,14 +143,12 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a) {
         for (int u = 0; u < U; u++) {
             const int c = 8 * (u * T + t), n = a.cols - c;
             float wt[8], b[8];
-            if (n > 0) {
-                load_param8(wt, a.weight, a.param_bf16, c, n, 1.f);
-                load_param8(b, a.bias, a.param_bf16, c, n, 0.f);
-            }
+            load_param8<WHOLE>(wt, a.weight, a.param_bf16, c, a.cols, 1.f);
+            load_param8<WHOLE>(b, a.bias, a.param_bf16, c, a.cols, 0.f);
 #pragma unroll
             for (int i = 0; i < 8; i++) y[u][i] = i < n ? __builtin_fmaf(y[u][i] * rstd, wt[i], b[i]) : 0.f;
             if constexpr (TO == TO_BF16) {
-                if (live && n > 0) store8_bf16(reinterpret_cast<uint16_t *>(a.out) + row * a.ld_out + c, y[u], n);
+                if (live) store_vec<WHOLE>(reinterpret_cast<uint16_t *>(a.out) + row * a.ld_out, y[u], c, a.cols);
             } else {
                 uint32_t m = 0;
 #pragma unroll
@@ -185,7 +196,8 @@ hipError_t launch_norm_tu(const NormArgs &a, hipStream_t s) {
     constexpr int NT = T < 256 ? 256 : T, RPW = NT / T;
     const int64_t wgs = (a.rows + RPW - 1) / RPW;
     const dim3 grid((unsigned)(wgs < (1 << 20) ? wgs : (1 << 20))), block(NT);
-    hipLaunchKernelGGL((k_norm<T, U, TO, F>), grid, block, 0, s, a);
+    if (a.cols % 8 == 0) hipLaunchKernelGGL((k_norm<T, U, TO, F, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_norm<T, U, TO, F, false>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -201,77 +213,166 @@ hipError_t launch_norm_to(const NormArgs &a, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-template <int T, int U>
-__global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm_dx(NormBwdArgs a) {
-    constexpr int NT = T < 256 ? 256 : T, RPW = NT / T;
-    __shared__ float s0[NT / 64], s1[NT / 64];
-    const int t = threadIdx.x % T;
+// T threads and 8 T U >= cols elements per row, R rows at a time; workgroup b takes rows
+// [b, b + 1) * per.  PARAMS: the sums of dy * xh and dy over those rows go to ws[b][0 and 1][cols].
+// Without, R is 1 and rows are read where the loop meets them.
+template <int T, int U, int R, bool PARAMS, bool WHOLE>
+__global__ __launch_bounds__(T *R) void k_norm_bwd(NormBwdArgs a, int per) {
+    constexpr int W = T / 64;
+    __shared__ float s0[R][W], s1[R][W];
+    __shared__ __attribute__((aligned(16))) float sP[PARAMS && R > 1 ? (R - 1) * T * 16 : 4];
+    // a wave's lanes share their row: with its number in a scalar register rows are scalar addresses
+    const int t = threadIdx.x % T, grp = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
     const float rn = 1.0f / (float)a.cols;
-    for (int64_t row0 = (int64_t)blockIdx.x * RPW; row0 < a.rows; row0 += (int64_t)gridDim.x * RPW) {
-        const int64_t row = row0 + threadIdx.x / T;
-        const bool live = row < a.rows;
-        uint32_t wx[U][4], wd[U][4];
+    const int64_t r0 = (int64_t)blockIdx.x * per;
+    const int count = (int)min((int64_t)per, a.rows - r0);  // rows of this workgroup, numbered from 0 below
+    float wt[U][8];
+    float dw[PARAMS ? U : 1][8], db[PARAMS ? U : 1][8];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const int c = 8 * (u * T + t), n = a.cols - c;
+        load_param8<WHOLE>(wt[u], a.weight, a.param_bf16, c, a.cols, 1.f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            wt[u][i] = i < n ? wt[u][i] : 0.f;
+            if constexpr (PARAMS) dw[u][i] = db[u][i] = 0.f;
+        }
+    }
+    uint32_t wx[U][4], wd[U][4];
+    float rstd = 0.f, mean = 0.f;
+    const auto load = [&](int row) {
+        const bool live = row < count;
+        const int64_t r = r0 + (live ? row : 0);
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int c = 8 * (u * T + t), n = a.cols - c;
-#pragma unroll
-            for (int k = 0; k < 4; k++) wx[u][k] = wd[u][k] = 0;
-            if (live && n > 0) {
-                load8_bf16(wx[u], a.x + row * a.ldx + c, n);
-                load8_bf16(wd[u], a.dy + row * a.lddy + c, n);
-            }
+            load_vec<WHOLE>(wx[u], a.x + r * a.ldx, 8 * (u * T + t), a.cols, live);
+            load_vec<WHOLE>(wd[u], a.dy + r * a.lddy, 8 * (u * T + t), a.cols, live);
         }
-        const float rstd = live ? a.rstd[row] : 0.f;
-        const float mean = live && !a.rms ? a.mean[row] : 0.f;
+        rstd = a.rstd[r];
+        mean = a.rms ? 0.f : a.mean[r];
+    };
+    const auto get = [](const uint32_t(&w)[4], int i) { return (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); };
+    load(grp);
+    for (int rb = 0; rb < count; rb += R) {
+        const int row = rb + grp;
+        uint32_t cx[U][4], cd[U][4];
+        const float rs = rstd, mn = mean;
         float sg = 0.f, sgx = 0.f;
-        float g[U][8], xh[U][8];
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int c = 8 * (u * T + t), n = a.cols - c;
-            float wt[8];
-            if (n > 0) load_param8(wt, a.weight, a.param_bf16, c, n, 1.f);
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const float xv = (i & 1) ? bf16_hi(wx[u][i >> 1]) : bf16_lo(wx[u][i >> 1]);
-                const float dv = (i & 1) ? bf16_hi(wd[u][i >> 1]) : bf16_lo(wd[u][i >> 1]);
-                xh[u][i] = i < n ? (xv - mean) * rstd : 0.f;
-                g[u][i] = i < n ? dv * wt[i] : 0.f;
-                sg += g[u][i];
-                sgx = __builtin_fmaf(g[u][i], xh[u][i], sgx);
+            for (int k = 0; k < 4; k++) {
+                cx[u][k] = wx[u][k];
+                cd[u][k] = wd[u][k];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++) {  // past the row's end dy is 0, and so is every term
+                const float d = get(cd[u], i), xh = (get(cx[u], i) - mn) * rs, g = d * wt[u][i];
+                sg += g;
+                sgx = __builtin_fmaf(g, xh, sgx);
+                if constexpr (PARAMS) {
+                    dw[u][i] = __builtin_fmaf(d, xh, dw[u][i]);
+                    db[u][i] += d;
+                    // here and now: left alone, the compiler moves these sums to the end of the loop and
+                    // holds every d and xh until then
+                    asm volatile("" : "+v"(dw[u][i]), "+v"(db[u][i]));
+                }
             }
         }
-        const float mg = a.rms ? 0.f : row_sum<T>(sg, s0) * rn;
-        const float mgx = row_sum<T>(sgx, s1) * rn;
+        load(row + R);  // the next rows, under this one's sums and stores
+        sg = wave_sum(sg);
+        sgx = wave_sum(sgx);
+        if constexpr (T > 64) {
+            if ((t & 63) == 0) {
+                s0[grp][t >> 6] = sg;
+                s1[grp][t >> 6] = sgx;
+            }
+            __syncthreads();
+            sg = sgx = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; i++) {
+                sg += s0[grp][i];
+                sgx += s1[grp][i];
+            }
+            __syncthreads();  // the slots are written again for the next rows
+        }
+        const float mg = a.rms ? 0.f : sg * rn, mgx = sgx * rn;
+        // g and xh are made again from the packed values: kept, they would cost 16 U registers (the
+        // empty asm keeps the compiler from keeping them)
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int c = 8 * (u * T + t), n = a.cols - c;
-            if (!live || n <= 0) continue;
+            const int c = 8 * (u * T + t);
+            if (row >= count) continue;
             float d[8];
 #pragma unroll
-            for (int i = 0; i < 8; i++) d[i] = (g[u][i] - mg - xh[u][i] * mgx) * rstd;
-            store8_bf16(a.dx + row * a.lddx + c, d, n);
+            for (int k = 0; k < 4; k++) asm volatile("" : "+v"(cx[u][k]), "+v"(cd[u][k]));
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float xh = (get(cx[u], i) - mn) * rs, g = get(cd[u], i) * wt[u][i];
+                d[i] = __builtin_fmaf(-xh, mgx, g - mg) * rs;
+            }
+            store_vec<WHOLE>(a.dx + (r0 + row) * a.lddx, d, c, a.cols);
         }
-        // the slots of the sums are written again for the next row
-        if (T > 64 && row0 + (int64_t)gridDim.x * RPW < a.rows) __syncthreads();
+    }
+    if constexpr (PARAMS) {
+        float *const d = a.ws + (int64_t)blockIdx.x * 2 * a.cols;
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if constexpr (R > 1) {  // the R rows' sums meet in group 0
+                if (u > 0) __syncthreads();
+                if (grp > 0) {
+                    float *p = sP + (grp - 1) * T * 16 + t;
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        p[i * T] = dw[u][i];
+                        p[(8 + i) * T] = db[u][i];
+                    }
+                }
+                __syncthreads();
+                if (grp == 0) {
+#pragma unroll 1
+                    for (int q = 0; q < R - 1; q++)
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            dw[u][i] += sP[q * T * 16 + t + i * T];
+                            db[u][i] += sP[q * T * 16 + t + (8 + i) * T];
+                        }
+                }
+            }
+            const int c = 8 * (u * T + t), n = a.cols - c;
+            if (grp > 0 || n <= 0) continue;
+            if (n >= 8) {
+                __builtin_memcpy(d + c, dw[u], 32);
+                __builtin_memcpy(d + a.cols + c, db[u], 32);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (i < n) {
+                        d[c + i] = dw[u][i];
+                        d[a.cols + c + i] = db[u][i];
+                    }
+            }
+        }
     }
 }
 
-constexpr int kPartCols = 512;  // columns per workgroup of the partial sums, 8 per lane
+// Rows wider than that kernel holds: the parameters' sums in a kernel of their own
+constexpr int kPartCols = 512;  // columns per workgroup, 8 per lane
 
 // sums of chunk blockIdx.y of the rows: ws[chunk][0 or 1][cols]
-__global__ __launch_bounds__(256) void k_norm_dparam(NormBwdArgs a, int64_t rows_per_chunk) {
+__global__ __launch_bounds__(256) void k_norm_dparam(NormBwdArgs a, int64_t per) {
     __shared__ float s[3][2][kPartCols];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = blockIdx.x * kPartCols + 8 * lane, n = a.cols - c;
-    const int64_t r0 = (int64_t)blockIdx.y * rows_per_chunk, r1 = min(a.rows, r0 + rows_per_chunk);
+    const int64_t r0 = (int64_t)blockIdx.y * per, r1 = min(a.rows, r0 + per);
     float dw[8], db[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) dw[i] = db[i] = 0.f;
     if (n > 0) {
         for (int64_t r = r0 + wave; r < r1; r += 4) {
             uint32_t wx[4], wd[4];
-            load8_bf16(wx, a.x + r * a.ldx + c, n);
-            load8_bf16(wd, a.dy + r * a.lddy + c, n);
+            load_vec<false>(wx, a.x + r * a.ldx, c, a.cols, true);
+            load_vec<false>(wd, a.dy + r * a.lddy, c, a.cols, true);
             const float rstd = a.rstd[r], mean = a.rms ? 0.f : a.mean[r];
 #pragma unroll
             for (int i = 0; i < 8; i++) {
@@ -301,33 +402,54 @@ __global__ __launch_bounds__(256) void k_norm_dparam(NormBwdArgs a, int64_t rows
     }
 }
 
-// the chunks' sums: 64 columns of one of the two gradients per workgroup
-__global__ __launch_bounds__(256) void k_norm_dparam_sum(NormBwdArgs a, int chunks) {
-    __shared__ float s[4][64];
+// the chunks' sums: 64 columns of one of the two gradients per workgroup, sixteen waves taking every
+// sixteenth chunk
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void k_norm_dparam_sum(NormBwdArgs a, int chunks) {
+    __shared__ float s[kSumWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = blockIdx.x * 64 + lane;
     float *out = blockIdx.y ? a.db : a.dw;
     if (!out) return;  // uniform
     float v = 0.f;
-    if (c < a.cols)
-        for (int k = wave; k < chunks; k += 4) v += a.ws[((int64_t)k * 2 + blockIdx.y) * a.cols + c];
+    if (c < a.cols) {
+#pragma unroll 8
+        for (int k = wave; k < chunks; k += kSumWaves) v += a.ws[((int64_t)k * 2 + blockIdx.y) * a.cols + c];
+    }
     s[wave][lane] = v;
     __syncthreads();
-    if (wave == 0 && c < a.cols) out[c] = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
+    if (wave == 0 && c < a.cols) {
+        v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSumWaves; w++) v += s[w][lane];
+        out[c] = v;
+    }
 }
 
-// chunks of rows of the partial sums: 16 rows at least, 128 chunks at most
-int64_t dparam_chunks(int64_t rows) {
-    const int64_t n = (rows + 15) / 16;
-    return n < 128 ? n : 128;
+// rows of a workgroup at a time (R), and the chunks that the rows are cut into: one workgroup per CU
+int norm_rows_at_once(int64_t cols) {
+    return cols <= 1024 ? 8 : cols <= 2048 ? 8 : cols <= 4096 ? 4 : cols <= 8192 ? 2 : 1;
+}
+int64_t dparam_chunks(int64_t rows, int64_t cols) {
+    const int64_t r = cols <= 16384 ? norm_rows_at_once(cols) : 16, n = (rows + r - 1) / r;
+    return n < 256 ? n : 256;
 }
 
 template <int T, int U>
 hipError_t launch_dx(const NormBwdArgs &a, hipStream_t s) {
-    constexpr int NT = T < 256 ? 256 : T, RPW = NT / T;
-    const int64_t wgs = (a.rows + RPW - 1) / RPW;
-    const dim3 grid((unsigned)(wgs < (1 << 20) ? wgs : (1 << 20))), block(NT);
-    hipLaunchKernelGGL((k_norm_dx<T, U>), grid, block, 0, s, a);
+    const int per = (int)((a.rows + (1 << 20) - 1) >> 20);
+    const dim3 grid((unsigned)((a.rows + per - 1) / per));
+    if (a.cols % 8 == 0) hipLaunchKernelGGL((k_norm_bwd<T, U, 1, false, true>), grid, dim3(T), 0, s, a, per);
+    else hipLaunchKernelGGL((k_norm_bwd<T, U, 1, false, false>), grid, dim3(T), 0, s, a, per);
+    return hipGetLastError();
+}
+
+template <int T, int U, int R>
+hipError_t launch_bwd(const NormBwdArgs &a, int64_t chunks, hipStream_t s) {
+    if (!a.dw && !a.db) return launch_dx<T, U>(a, s);
+    const int per = (int)((a.rows + chunks - 1) / chunks);
+    if (a.cols % 8 == 0) hipLaunchKernelGGL((k_norm_bwd<T, U, R, true, true>), dim3((unsigned)chunks), dim3(T * R), 0, s, a, per);
+    else hipLaunchKernelGGL((k_norm_bwd<T, U, R, true, false>), dim3((unsigned)chunks), dim3(T * R), 0, s, a, per);
     return hipGetLastError();
 }
 
@@ -344,28 +466,31 @@ hipError_t launch_norm(const NormArgs &a, int to, int fmt, hipStream_t s) {
     }
 }
 
-int64_t norm_backward_workspace(int64_t rows, int64_t cols) { return dparam_chunks(rows) * 2 * cols; }
+int64_t norm_backward_workspace(int64_t rows, int64_t cols) { return dparam_chunks(rows, cols) * 2 * cols; }
 
 hipError_t launch_norm_backward(const NormBwdArgs &a, hipStream_t s) {
+    const bool params = a.dw || a.db;
+    const int64_t chunks = a.rows > 0 ? dparam_chunks(a.rows, a.cols) : 0;
     hipError_t e = hipSuccess;
     if (a.rows > 0) {
-        if (a.cols <= 512) e = launch_dx<64, 1>(a, s);
-        else if (a.cols <= 1024) e = launch_dx<64, 2>(a, s);
-        else if (a.cols <= 2048) e = launch_dx<256, 1>(a, s);
-        else if (a.cols <= 4096) e = launch_dx<256, 2>(a, s);
-        else if (a.cols <= 8192) e = launch_dx<256, 4>(a, s);
-        else if (a.cols <= 16384) e = launch_dx<1024, 2>(a, s);
-        else e = launch_dx<1024, 4>(a, s);
-        if (e != hipSuccess) return e;
+        if (a.cols <= 512) e = launch_bwd<64, 1, 8>(a, chunks, s);
+        else if (a.cols <= 1024) e = launch_bwd<64, 2, 8>(a, chunks, s);
+        else if (a.cols <= 2048) e = launch_bwd<128, 2, 8>(a, chunks, s);
+        else if (a.cols <= 4096) e = launch_bwd<256, 2, 4>(a, chunks, s);
+        else if (a.cols <= 8192) e = launch_bwd<256, 4, 2>(a, chunks, s);
+        else if (a.cols <= 16384) e = launch_bwd<512, 4, 1>(a, chunks, s);
+        else {
+            e = launch_dx<1024, 4>(a, s);
+            if (e == hipSuccess && params) {
+                const dim3 grid((unsigned)((a.cols + kPartCols - 1) / kPartCols), (unsigned)chunks);
+                hipLaunchKernelGGL(k_norm_dparam, grid, dim3(256), 0, s, a, (a.rows + chunks - 1) / chunks);
+                e = hipGetLastError();
+            }
+        }
     }
-    if (!a.dw && !a.db) return e;
-    const int64_t chunks = dparam_chunks(a.rows);
-    if (chunks > 0) {
-        const dim3 grid((unsigned)((a.cols + kPartCols - 1) / kPartCols), (unsigned)chunks);
-        hipLaunchKernelGGL(k_norm_dparam, grid, dim3(256), 0, s, a, (a.rows + chunks - 1) / chunks);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL(k_norm_dparam_sum, dim3((unsigned)((a.cols + 63) / 64), 2), dim3(256), 0, s, a, (int)chunks);
+    if (e != hipSuccess || !params) return e;
+    hipLaunchKernelGGL(k_norm_dparam_sum, dim3((unsigned)((a.cols + 63) / 64), 2), dim3(64 * kSumWaves), 0, s, a,
+                       (int)chunks);
     return hipGetLastError();
 }
 
