@@ -42,21 +42,6 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
-// sum over the T threads of a row: T = 64 is one wave; above, the waves meet in `s`
-// (one slot per wave, a slot array of its own for each use between two barriers)
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float *s) {
-    v = wave_sum(v);
-    if constexpr (T > 64) {
-        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0.f;
-#pragma unroll
-        for (int i = 0; i < T / 64; i++) v += s[i];
-    }
-    return v;
-}
-
 // parameters c .. c + 7 as fp32; `other` where there are none, anything past cols
 template <bool WHOLE>
 __device__ __forceinline__ void load_param8(float (&w)[8], const void *p, bool bf16, int c, int cols, float other) {
@@ -95,21 +80,54 @@ __device__ __forceinline__ void store_vec(uint16_t *p, const float (&y)[8], int 
     }
 }
 
-// T threads and 8 T U >= cols elements per row; a workgroup of max(T, 256) threads
+// T threads and 8 T U >= cols elements per row, NT / T rows at a time; a workgroup takes the `per` rows from
+// blockIdx.x * per on, the next rows' loads under way while it works on these.  Block scales lie
+// rows-innermost, so those of one row are 4-byte stores to as many lines: they are collected in LDS and
+// written as runs of the workgroup's rows (8192 x 4096: row by row 34 us, where the bf16 output with a
+// third more bytes took 27).
+constexpr int kNormRows = 16;  // most rows per workgroup
 template <int T, int U, int TO, int F, bool WHOLE>
-__global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a) {
-    constexpr int NT = T < 256 ? 256 : T, RPW = NT / T;
-    __shared__ float s0[NT / 64], s1[NT / 64];
-    const int t = threadIdx.x % T;
+__global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a, int per) {
+    constexpr int NT = T < 256 ? 256 : T, RPW = NT / T, W = T / 64;
+    constexpr bool KEEP = U <= 2;  // the parameters fit in registers beside a row
+    __shared__ float s0[RPW][W], s1[RPW][W];
+    __shared__ float sSc[TO == TO_BLOCK ? T * U / 16 * kNormRows : 1];  // [block][row]
+    const int t = threadIdx.x % T, grp = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
     const float rn = 1.0f / (float)a.cols;
-    for (int64_t row0 = (int64_t)blockIdx.x * RPW; row0 < a.rows; row0 += (int64_t)gridDim.x * RPW) {
-        const int64_t row = row0 + __builtin_amdgcn_readfirstlane(threadIdx.x / T);
-        const bool live = row < a.rows;  // with one wave per row the others go on; with more RPW is 1
-        float y[U][8];
-        const uint16_t *px = a.x + (live ? row : 0) * a.ldx;
-        uint32_t w[U][4];
+    const int64_t r0 = (int64_t)blockIdx.x * per;
+    const int count = (int)min((int64_t)per, a.rows - r0);
+    float wt[KEEP ? U : 1][8], bs[KEEP ? U : 1][8];
+    if constexpr (KEEP) {
 #pragma unroll
-        for (int u = 0; u < U; u++) load_vec<WHOLE>(w[u], px, 8 * (u * T + t), a.cols, live);
+        for (int u = 0; u < U; u++) {
+            load_param8<WHOLE>(wt[u], a.weight, a.param_bf16, 8 * (u * T + t), a.cols, 1.f);
+            load_param8<WHOLE>(bs[u], a.bias, a.param_bf16, 8 * (u * T + t), a.cols, 0.f);
+        }
+    }
+    uint32_t w[U][4];
+    const auto load = [&](int row) {
+        const bool live = row < count;
+        const uint16_t *p = a.x + (r0 + (live ? row : 0)) * a.ldx;
+#pragma unroll
+        for (int u = 0; u < U; u++) load_vec<WHOLE>(w[u], p, 8 * (u * T + t), a.cols, live);
+    };
+    // sum over the row's threads; `s` is written again only after another barrier
+    const auto row_sum = [&](float v, float (&s)[RPW][W]) {
+        v = wave_sum(v);
+        if constexpr (T > 64) {
+            if ((t & 63) == 0) s[grp][t >> 6] = v;
+            __syncthreads();
+            v = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; i++) v += s[grp][i];
+        }
+        return v;
+    };
+    load(grp);
+    for (int rb = 0; rb < count; rb += RPW) {
+        const bool live = rb + grp < count;
+        const int64_t row = r0 + rb + grp;
+        float y[U][8];
         float sum = 0.f;
 #pragma unroll
         for (int u = 0; u < U; u++)
@@ -118,22 +136,25 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a) {
                 y[u][i] = (i & 1) ? bf16_hi(w[u][i >> 1]) : bf16_lo(w[u][i >> 1]);
                 sum += y[u][i];
             }
+        load(rb + grp + RPW);
         float mean = 0.f;
         if (!a.rms) {
-            mean = row_sum<T>(sum, s0) * rn;
+            mean = row_sum(sum, s0) * rn;
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 const int n = a.cols - 8 * (u * T + t);
 #pragma unroll
-                for (int i = 0; i < 8; i++) y[u][i] = i < n ? y[u][i] - mean : 0.f;
+                for (int i = 0; i < 8; i++) y[u][i] = (WHOLE ? 0 : i) < n ? y[u][i] - mean : 0.f;
             }
+        } else if (T > 64) {
+            __syncthreads();  // the other barrier between two uses of s1
         }
         float sq = 0.f;
 #pragma unroll
         for (int u = 0; u < U; u++)
 #pragma unroll
             for (int i = 0; i < 8; i++) sq = __builtin_fmaf(y[u][i], y[u][i], sq);
-        const float var = row_sum<T>(sq, s1) * rn;
+        const float var = row_sum(sq, s1) * rn;
         const float rstd = 1.0f / __builtin_sqrtf(var + a.eps);
         if (live && t == 0) {
             if (a.mean && !a.rms) a.mean[row] = mean;
@@ -142,11 +163,14 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a) {
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const int c = 8 * (u * T + t), n = a.cols - c;
-            float wt[8], b[8];
-            load_param8<WHOLE>(wt, a.weight, a.param_bf16, c, a.cols, 1.f);
-            load_param8<WHOLE>(b, a.bias, a.param_bf16, c, a.cols, 0.f);
+            if constexpr (!KEEP) {
+                load_param8<WHOLE>(wt[0], a.weight, a.param_bf16, c, a.cols, 1.f);
+                load_param8<WHOLE>(bs[0], a.bias, a.param_bf16, c, a.cols, 0.f);
+            }
+            const int k = KEEP ? u : 0;
 #pragma unroll
-            for (int i = 0; i < 8; i++) y[u][i] = i < n ? __builtin_fmaf(y[u][i] * rstd, wt[i], b[i]) : 0.f;
+            for (int i = 0; i < 8; i++)
+                y[u][i] = (WHOLE ? 0 : i) < n ? __builtin_fmaf(y[u][i] * rstd, wt[k][i], bs[k][i]) : 0.f;
             if constexpr (TO == TO_BF16) {
                 if (live) store_vec<WHOLE>(reinterpret_cast<uint16_t *>(a.out) + row * a.ld_out, y[u], c, a.cols);
             } else {
@@ -154,7 +178,7 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a) {
 #pragma unroll
                 for (int i = 0; i < 8; i++) m = umax(m, __float_as_uint(y[u][i]) & 0x7FFFFFFFu);
                 m = TO == TO_BLOCK ? row16_max(m) : quad_max(m);
-                uint8_t *q = reinterpret_cast<uint8_t *>(a.out) + row * a.ld_out + (F == E2M1 ? c / 2 : c);
+                uint8_t *q = reinterpret_cast<uint8_t *>(a.out) + row * a.ld_out;
                 if constexpr (TO == TO_BLOCK) {
                     float sc, inv;
                     bool ok;
@@ -162,9 +186,13 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a) {
                     const uint32_t lo = block_cvt4<F>(y[u][0], y[u][1], y[u][2], y[u][3], inv, ok);
                     const uint32_t hi = block_cvt4<F>(y[u][4], y[u][5], y[u][6], y[u][7], inv, ok);
                     if (live && n > 0) {
-                        store8(q, lo, hi, n);
-                        if ((t & 15) == 0)
-                            reinterpret_cast<float *>(a.scales)[(int64_t)(c / kBlk) * a.ld_scales + row] = sc;
+                        if (WHOLE) {
+                            const uint32_t v[2] = {lo, hi};
+                            __builtin_memcpy(q + (uint32_t)c, v, 8);
+                        } else {
+                            store8(q + (uint32_t)c, lo, hi, n);
+                        }
+                        if ((t & 15) == 0) sSc[(c / kBlk) * kNormRows + rb + grp] = sc;
                     }
                 } else {
                     const bool ok = m < 0x7F800000u;
@@ -173,12 +201,12 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a) {
                     if (live && n > 0) {  // cols is a multiple of 32: whole vectors
                         if constexpr (F == E2M1) {
                             const uint32_t v = ok ? cvt8_fp4(y[u], sc) : 0u;
-                            __builtin_memcpy(q, &v, 4);
+                            __builtin_memcpy(q + (uint32_t)(c / 2), &v, 4);
                         } else {
                             const float lim = __builtin_amdgcn_ldexpf(MaxNormal<F>::v, e);
                             const uint32_t v[2] = {ok ? cvt4_fp8<F>(y[u][0], y[u][1], y[u][2], y[u][3], sc, lim) : 0u,
                                                    ok ? cvt4_fp8<F>(y[u][4], y[u][5], y[u][6], y[u][7], sc, lim) : 0u};
-                            __builtin_memcpy(q, v, 8);
+                            __builtin_memcpy(q + (uint32_t)c, v, 8);
                         }
                         if ((t & 3) == 0)
                             reinterpret_cast<uint8_t *>(a.scales)[row * a.ld_scales + c / 32] = (uint8_t)(ok ? e + 127 : 0xFF);
@@ -186,18 +214,27 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a) {
                 }
             }
         }
-        // the slots of the sums are written again for the next row
-        if (T > 64 && row0 + (int64_t)gridDim.x * RPW < a.rows) __syncthreads();
+    }
+    if constexpr (TO == TO_BLOCK) {
+        __syncthreads();
+        const int nb = (a.cols + kBlk - 1) / kBlk;
+        for (int i = threadIdx.x; i < nb * kNormRows; i += NT) {
+            const int b = i / kNormRows, r = i % kNormRows;
+            if (r < count) reinterpret_cast<float *>(a.scales)[b * a.ld_scales + r0 + r] = sSc[i];
+        }
     }
 }
 
 template <int T, int U, int TO, int F>
 hipError_t launch_norm_tu(const NormArgs &a, hipStream_t s) {
     constexpr int NT = T < 256 ? 256 : T, RPW = NT / T;
-    const int64_t wgs = (a.rows + RPW - 1) / RPW;
-    const dim3 grid((unsigned)(wgs < (1 << 20) ? wgs : (1 << 20))), block(NT);
-    if (a.cols % 8 == 0) hipLaunchKernelGGL((k_norm<T, U, TO, F, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_norm<T, U, TO, F, false>), grid, block, 0, s, a);
+    // rows per workgroup: as many as leave eight workgroups' worth of threads per CU, RPW at least
+    const int64_t fill = 256 * 2048 / NT;
+    int64_t per = a.rows / fill / RPW * RPW;
+    per = per < RPW ? RPW : per > kNormRows ? kNormRows : per;
+    const dim3 grid((unsigned)((a.rows + per - 1) / per)), block(NT);
+    if (a.cols % 8 == 0) hipLaunchKernelGGL((k_norm<T, U, TO, F, true>), grid, block, 0, s, a, (int)per);
+    else hipLaunchKernelGGL((k_norm<T, U, TO, F, false>), grid, block, 0, s, a, (int)per);
     return hipGetLastError();
 }
 
@@ -341,17 +378,17 @@ __global__ __launch_bounds__(T *R) void k_norm_bwd(NormBwdArgs a, int per) {
             }
             const int c = 8 * (u * T + t), n = a.cols - c;
             if (grp > 0 || n <= 0) continue;
-            if (n >= 8) {
-                __builtin_memcpy(d + c, dw[u], 32);
-                __builtin_memcpy(d + a.cols + c, db[u], 32);
-            } else {
+            const auto put = [&](float *p, const float (&v)[8]) {
+                if (n >= 8) {
+                    __builtin_memcpy(p, v, 32);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    if (i < n) {
-                        d[c + i] = dw[u][i];
-                        d[a.cols + c + i] = db[u][i];
-                    }
-            }
+                    for (int i = 0; i < 8; i++)
+                        if (i < n) p[i] = v[i];
+                }
+            };
+            if (a.dw) put(d + c, dw[u]);
+            if (a.db) put(d + a.cols + c, db[u]);
         }
     }
 }
