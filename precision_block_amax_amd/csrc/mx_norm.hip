@@ -244,7 +244,7 @@ hipError_t launch_norm_to(const NormArgs &a, hipStream_t s) {
     if (a.cols <= 1024) return launch_norm_tu<64, 2, TO, F>(a, s);
     if (a.cols <= 2048) return launch_norm_tu<256, 1, TO, F>(a, s);
     if (a.cols <= 4096) return launch_norm_tu<256, 2, TO, F>(a, s);
-    if (a.cols <= 8192) return launch_norm_tu<256, 4, TO, F>(a, s);
+    if (a.cols <= 8192) return launch_norm_tu<512, 2, TO, F>(a, s);
     if (a.cols <= 16384) return launch_norm_tu<1024, 2, TO, F>(a, s);
     return launch_norm_tu<1024, 4, TO, F>(a, s);
 }
