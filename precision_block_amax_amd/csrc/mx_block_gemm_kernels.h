@@ -251,14 +251,17 @@ __device__ __forceinline__ void dma4(pipe::v4i r, void *lds, int voff, int soff)
 
 constexpr int kDead = (int)0x80000000u;  // a lane offset beyond every buffer: the load writes zeros
 
-// configurations: waves, tiles per wave, ring
-struct Cfg256x256 { static constexpr int TI = 4, WM = 2, WN = 4, NS = 2; };
-struct Cfg256x128 { static constexpr int TI = 2, WM = 4, WN = 2, NS = 2; };
-struct Cfg128x128 { static constexpr int TI = 2, WM = 2, WN = 2, NS = 4; };
+// Configurations: tiles per wave, waves, ring.  KG groups of waves take every KG-th stage each, with
+// rings of their own, and their sums meet at the end: a 128 x 128 tile has work for four waves of 64 x 64
+// only, and a SIMD with one wave neither multiplies while it reads LDS nor the other way round.
+struct Cfg256x256 { static constexpr int TI = 4, WM = 2, WN = 4, NS = 2, KG = 1; };
+struct Cfg256x128 { static constexpr int TI = 2, WM = 4, WN = 2, NS = 2, KG = 1; };
+struct Cfg128x128 { static constexpr int TI = 2, WM = 2, WN = 2, NS = 2, KG = 2; };
 
 template <int FA, int FB, bool BT, bool BF16OUT, class CFG>
-__global__ __launch_bounds__(64 * CFG::WM * CFG::WN, CFG::WM * CFG::WN / 4) void k_block_gemm_pipe(BlockGemmArgs g) {
-    constexpr int TI = CFG::TI, WM = CFG::WM, WN = CFG::WN, NS = CFG::NS;
+__global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN * CFG::KG / 4) void k_block_gemm_pipe(BlockGemmArgs g) {
+    constexpr int TI = CFG::TI, WM = CFG::WM, WN = CFG::WN, NS = CFG::NS, KG = CFG::KG;
+    static_assert(KG == 1 || (KG == 2 && TI == 2), "the join swaps two rows of tiles");
     constexpr int NW = WM * WN, PM = WM * TI * 32, PN = WN * 64;
     constexpr int NIA = PM / 8 / NW, NIB = PN / 8 / NW;  // 1 KiB loads (8 rows) per wave and stage
     static_assert(NIA >= 1 && NIB >= 1 && PM % (8 * NW) == 0 && PN % (8 * NW) == 0, "load split");
@@ -269,12 +272,15 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, CFG::WM * CFG::WN / 4) void
     // A's stages of codes, then B's: a fragment read is one of eight lane offsets (four 32-byte
     // steps of K, two operands), the stage's place and a constant
     constexpr int OB = NS * PM * kBlk;
-    __shared__ __attribute__((aligned(16))) uint8_t sC[NS * ST];
+    __shared__ __attribute__((aligned(16))) uint8_t sCodes[KG * NS * ST];
     // scales, in a ring of their own: the last tile of a stage is scaled in the next one, while the
     // loads that reuse the stage's codes are under way
-    __shared__ __attribute__((aligned(16))) float sS[SR * (PM + PN)];
+    __shared__ __attribute__((aligned(16))) float sScales[KG * SR * (PM + PN)];
     const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave_all = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int grp = KG == 1 ? 0 : wave_all / NW, wave = wave_all % NW;
+    uint8_t *const sC = sCodes + grp * NS * ST;
+    float *const sS = sScales + grp * SR * (PM + PN);
     const int wm = wave / WN, wn = wave % WN, l32 = lane & 31, h = lane >> 5;
     int tm, tn;
     block_tile_of(g, tm, tn);
@@ -312,7 +318,8 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, CFG::WM * CFG::WN / 4) void
     const int vS = (isA || !BT ? srow : srow / kBlk) * 4;
     float *const sdst = sS + (isA ? 0 : PM) + 64 * sw;
 
-    const auto issue = [&](int u, int kt) {  // stage kt into place u
+    const auto issue = [&](int u, int it) {  // the group's stage number `it` into place u
+        const int kt = it * KG + grp;
         const bool live = kt < nk, last = kt == nk - 1;
         const int so = live ? kt * kBlk : 0;
         uint8_t *const dA = sC + u * PM * kBlk + wave * NIA * 1024, *const dB = sC + OB + u * PN * kBlk + wave * NIB * 1024;
@@ -326,7 +333,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, CFG::WM * CFG::WN / 4) void
         for (int q = 0; q < NIA; q++) pipe::dma16(rA, dA + q * 1024, a[q & 1], so + q * 8 * lda);
 #pragma unroll
         for (int q = 0; q < NIB; q++) pipe::dma16(rB, dB + q * 1024, b[q & 1], so + q * 8 * ldb);
-        dma4(rS, sdst + (kt & (SR - 1)) * (PM + PN), live ? vS : kDead, live ? kt * (int)lds_ * 4 : 0);
+        dma4(rS, sdst + (it & (SR - 1)) * (PM + PN), live ? vS : kDead, live ? kt * (int)lds_ * 4 : 0);
     };
 
     float acc[TI][2][16];
@@ -344,7 +351,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, CFG::WM * CFG::WN / 4) void
     // are its scales, in the place that the ring fills last.
     const float *psb = sS + (SR - 1) * (PM + PN) + scol;
     if constexpr (!BT) {
-        for (int i = tid; i < PN; i += 64 * NW) sS[(SR - 1) * (PM + PN) + PM + i] = 0.f;
+        for (int i = tid % (64 * NW); i < PN; i += 64 * NW) sS[(SR - 1) * (PM + PN) + PM + i] = 0.f;
     }
     // acc += scale * sum of the tile before
     const auto promote = [&](float (&c)[16], const float4 (&sb)[4]) {
@@ -382,10 +389,10 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, CFG::WM * CFG::WN / 4) void
         return f;
     };
 
-    const auto stage = [&](int u, int kt) {
+    const auto stage = [&](int u, int it) {
         pipe::wait_vm<(NS - 2) * LPW>();
         pipe::barrier();
-        const float *const ss = sS + (kt & (SR - 1)) * (PM + PN);
+        const float *const ss = sS + (it & (SR - 1)) * (PM + PN);
         const int ua = u * PM * kBlk, ub = u * PN * kBlk;
         Frag fa[2], fb[2];
         Frag16 ga, gb[2];
@@ -396,7 +403,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, CFG::WM * CFG::WN / 4) void
 #pragma unroll
         for (int i = 0; i < TI; i++) sa[i] = ss[wm * TI * 32 + i * 32 + l32];
         const float sbt = BT ? ss[scol] : 1.0f;
-        issue((u + NS - 1) & (NS - 1), kt + NS - 1);
+        issue((u + NS - 1) & (NS - 1), it + NS - 1);
         if constexpr (!BF16OUT) {
             ga = to_bf16<FA>(fa[0]);
 #pragma unroll
@@ -423,15 +430,15 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, CFG::WM * CFG::WN / 4) void
 
 #pragma unroll
     for (int u = 0; u < NS - 1; u++) issue(u, u);
+    const int nit = (nk + KG - 1) / KG;  // stages of a group; one past the end of K is all zeros
     if constexpr (NS == 2) {
-        // two stages at a time, so that their places are constants; with an odd number of them the
-        // last one is all zeros
-        for (int kt = 0; kt < nk; kt += 2) {
-            stage(0, kt);
-            stage(1, kt + 1);
+        // two at a time, so that their places are constants
+        for (int it = 0; it < nit; it += 2) {
+            stage(0, it);
+            stage(1, it + 1);
         }
     } else {
-        for (int kt = 0; kt < nk; kt++) stage(kt & (NS - 1), kt);
+        for (int it = 0; it < nit; it++) stage(it & (NS - 1), it);
     }
     {
         float4 sb[4];
@@ -441,16 +448,36 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, CFG::WM * CFG::WN / 4) void
     pipe::wait_vm<0>();
     pipe::barrier();  // every wave has left the loop: the stages' LDS is free
 
+    // two groups: each keeps one row of tiles of every wave's (its own number) and gives the other one
+    constexpr int TK = TI / KG;
+    if constexpr (KG == 2) {
+        float *const mine = reinterpret_cast<float *>(sCodes) + wave_all * 32 * 64;
+        const float *const other = reinterpret_cast<const float *>(sCodes) + (wave_all ^ NW) * 32 * 64;
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+#pragma unroll
+            for (int r = 0; r < 16; r++) {
+                mine[(j * 16 + r) * 64 + lane] = grp ? acc[0][j][r] : acc[1][j][r];
+                acc[0][j][r] = grp ? acc[1][j][r] : acc[0][j][r];
+            }
+        pipe::barrier();
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+#pragma unroll
+            for (int r = 0; r < 16; r++) acc[0][j][r] += other[(j * 16 + r) * 64 + lane];
+        pipe::barrier();
+    }
+
     // C through LDS, each wave its own part, TI2 x 32 rows at a time, so that rows leave as runs of 64
     // elements; 16-byte chunks are XOR-swizzled by the row
     constexpr int ESZ = BF16OUT ? 2 : 4, ROWB = 64 * ESZ, CPR = ROWB / 16, REG = NS * ST / NW;
-    constexpr int TI2 = TI * 32 * ROWB <= REG ? TI : TI / 2;
-    static_assert(TI2 >= 1 && TI % TI2 == 0 && TI2 * 32 * ROWB <= REG, "staging");
+    constexpr int TI2 = TK * 32 * ROWB <= REG ? TK : TK / 2;
+    static_assert(TI2 >= 1 && TK % TI2 == 0 && TI2 * 32 * ROWB <= REG, "staging");
     uint8_t *const reg = sC + wave * REG;
-    const int mbase = m0 + wm * TI * 32, nbase = n0 + wn * 64;
+    const int mbase = m0 + (wm * TI + grp) * 32, nbase = n0 + wn * 64;
     const bool vec = nbase + 64 <= g.N && g.ldc % (16 / ESZ) == 0 && ((uintptr_t)g.c & 15) == 0;
 #pragma unroll
-    for (int pass = 0; pass < TI / TI2; pass++) {
+    for (int pass = 0; pass < TK / TI2; pass++) {
 #pragma unroll
         for (int ii = 0; ii < TI2; ii++) {
             const int m = ii * 32 + l32;
@@ -491,35 +518,24 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, CFG::WM * CFG::WN / 4) void
 }
 
 // ---------------------------------------------------------------------------
-// Direct kernel, for few rows: 16 MT x 16 NT of C per workgroup, its eight
-// waves each taking every eighth block of K for the whole tile, fragments
-// straight from memory to registers, the waves' sums joined in LDS.  Any
-// alignment and K.
+// Kernel for few rows (up to 64): 16 columns of C per workgroup, its eight waves
+// each taking every eighth block of K for all of them, joined in LDS.
 //
-// With one row the product is bound by B's bytes; 16 rows of B per workgroup
-// give 256 workgroups from N = 4096 on, and eight waves each with the loads of
-// U blocks in flight (2 KiB of B per block and wave) cover the latency without
-// a split of K over workgroups, which would need memory to join them.
-constexpr int DW = 8;
+// With one row the product is bound by B's bytes.  16 rows of B per workgroup
+// make 256 workgroups from N = 4096 on, and the waves' blocks in flight cover
+// the latency without a split of K over workgroups, which would need memory to
+// join them.  Blocks come straight to LDS, a ring of S per wave and no barrier:
+// a fragment's lanes are rows, and loaded into registers its neighbouring lanes
+// read different lines, of which an L1 serves one per clock: 48 rows by 4096 x
+// 14336 took 28 us at 16 bytes per clock and CU, whatever was in flight.
+constexpr int DW = 8;  // waves
 
 struct Frag2 {
     uint4 c[2];
 };
-// bytes [32 h, 32 h + 32) of the block's 128 at p; without FULL, n bytes are left of the row there
-template <bool FULL>
-__device__ __forceinline__ Frag2 direct_frag(const uint8_t *p, int h, int n) {
-    Frag2 f;
-    if constexpr (FULL) {
-        __builtin_memcpy(&f, p + 32 * h, 32);
-    } else {
-        f.c[0] = load16(p + 32 * h, n - 32 * h);
-        f.c[1] = load16(p + 32 * h + 16, n - 32 * h - 16);
-    }
-    return f;
-}
 
 template <int FA, int FB, bool BF16OUT>
-__device__ __forceinline__ v4f direct_block(const Frag2 &a, const Frag2 &b) {
+__device__ __forceinline__ v4f few_block(const Frag2 &a, const Frag2 &b) {
     v4f p = {0.f, 0.f, 0.f, 0.f};
     const uint4 x = a.c[0], y = a.c[1], u = b.c[0], v = b.c[1];
     if constexpr (BF16OUT) {
@@ -535,111 +551,143 @@ __device__ __forceinline__ v4f direct_block(const Frag2 &a, const Frag2 &b) {
     return p;
 }
 
-template <int FA, int FB, bool BT, bool BF16OUT, int MT, int NT, int U>
-__global__ __launch_bounds__(64 * DW) void k_block_gemm_direct(BlockGemmArgs g) {
-    constexpr int DM = 16 * MT, DN = 16 * NT;
-    __shared__ __attribute__((aligned(16))) float sJ[DW][DM][DN + 4];
+// the first n bytes of v, the rest 0
+__device__ __forceinline__ uint4 keep_bytes(uint4 v, int n) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int d = 0; d < 4; d++) {
+        const int k = n - 4 * d;
+        w[d] = k >= 4 ? w[d] : k <= 0 ? 0u : w[d] & ((1u << (8 * k)) - 1u);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// AI: loads of 8 rows of A (M <= 8 AI); rows of the last tile beyond them are whatever LDS holds, and reach
+// only rows of C that do not exist
+template <int FA, int FB, bool BT, bool BF16OUT, int AI, int S>
+__global__ __launch_bounds__(64 * DW) void k_block_gemm_few(BlockGemmArgs g) {
+    constexpr int MT = (AI + 1) / 2, DM = 16 * MT;
+    constexpr int OB = MT * 2048, OS = OB + 2048, BLK = OS + 512;  // a block: A's rows, B's 16, scales of A, of B
+    constexpr int LPB = AI + 4;                                    // loads per block
+    constexpr int JOIN = DW * DM * 20 * 4;                         // the waves' sums, rows of 16 + 4 floats
+    __shared__ __attribute__((aligned(16))) uint8_t sR[DW * S * BLK > JOIN ? DW * S * BLK : JOIN];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, h = lane >> 4;
-    int tm, tn;
-    block_tile_of(g, tm, tn);
-    const int m0 = tm * DM, n0 = tn * DN;
-    const int nk = (g.K + kBlk - 1) / kBlk;
-    // rows past the edge repeat the last one; their results are not stored
-    const uint8_t *pa[MT], *pb[NT];
-    const float *qa[MT], *qb[NT];
+    const int n0 = blockIdx.x * 16;
+    const int nk = (g.K + kBlk - 1) / kBlk, ktail = g.K - (nk - 1) * kBlk;
+    const int lda = (int)g.lda, ldb = (int)g.ldb, nrows = min(16, g.N - n0);
+    // rows end at a multiple of 16 bytes: an aligned 16 bytes that hold a byte of the row
+    const int kend = (g.K + 15) & ~15;
+    const pipe::v4i rA = pipe::rsrc(g.a, (uint32_t)((g.M - 1) * lda + kend));
+    const pipe::v4i rB = pipe::rsrc(g.b + (int64_t)n0 * ldb, (uint32_t)((nrows - 1) * ldb + kend));
+    const pipe::v4i rSA = pipe::rsrc(g.as, (uint32_t)(((int64_t)(nk - 1) * g.ldsa + g.M) * 4));
+    const pipe::v4i rSB = pipe::rsrc(g.bs + (BT ? n0 / kBlk : n0), (uint32_t)(((int64_t)(nk - 1) * g.ldsb + (BT ? 1 : nrows)) * 4));
+    // lane l of a load: 16-byte slot l % 8 of row l / 8, logical chunk (l % 8) ^ key
+    const int lr = lane / 8;
+    int vA[AI], vB[2], cA[2];
 #pragma unroll
-    for (int i = 0; i < MT; i++) {
-        const int m = min(m0 + 16 * i + l16, g.M - 1);
-        pa[i] = g.a + (int64_t)m * g.lda;
-        qa[i] = g.as + m;
+    for (int o = 0; o < 2; o++) {
+        cA[o] = ((lane & 7) ^ swz_key<128>(lr + 8 * o)) << 4;
+        vB[o] = lr + 8 * o < nrows ? (lr + 8 * o) * ldb + cA[o] : kDead;
     }
 #pragma unroll
-    for (int j = 0; j < NT; j++) {
-        pb[j] = g.b + (int64_t)min(n0 + 16 * j + l16, g.N - 1) * g.ldb;
-        // a tiled B: 16 columns lie in one tile; else the scales of this lane's four columns
-        qb[j] = g.bs + (BT ? min(n0 + 16 * j, g.N - 1) / kBlk : n0 + 16 * j + 4 * h);
-    }
-    float acc[MT][NT][4];
+    for (int o = 0; o < AI; o++) vA[o] = lr + 8 * o < g.M ? (lr + 8 * o) * lda + cA[o & 1] : kDead;
+    const int vSA = lane < g.M ? lane * 4 : kDead, vSB = BT ? 0 : lane < nrows ? lane * 4 : kDead;
+    uint8_t *const ring = sR + wave * S * BLK;
+
+    const auto issue = [&](int slot, int i) {  // block number i of this wave
+        const int kt = wave + i * DW;
+        const bool live = kt < nk, last = kt == nk - 1;
+        uint8_t *const d = ring + slot * BLK;
+        const int so = live ? kt * kBlk : 0;
+        const bool in[2] = {live && (!last || cA[0] < ktail), live && (!last || cA[1] < ktail)};
+#pragma unroll
+        for (int o = 0; o < AI; o++) pipe::dma16(rA, d + o * 1024, in[o & 1] ? vA[o] : kDead, so);
+#pragma unroll
+        for (int o = 0; o < 2; o++) pipe::dma16(rB, d + OB + o * 1024, in[o] ? vB[o] : kDead, so);
+        dma4(rSA, d + OS, live ? vSA : kDead, live ? kt * (int)g.ldsa * 4 : 0);
+        dma4(rSB, d + OS + 256, live ? vSB : kDead, live ? kt * (int)g.ldsb * 4 : 0);
+    };
+
+    float acc[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; i++)
 #pragma unroll
-        for (int j = 0; j < NT; j++)
-#pragma unroll
-            for (int r = 0; r < 4; r++) acc[i][j][r] = 0.f;
+        for (int r = 0; r < 4; r++) acc[i][r] = 0.f;
+    const int count = nk > wave ? (nk - wave + DW - 1) / DW : 0;
+    const int ch[2] = {(h ^ swz_key<128>(l16)) << 4, ((4 + h) ^ swz_key<128>(l16)) << 4};  // this lane's chunks: h and 4 + h
 
-    // NB blocks from k0 on, DW apart; FULL: all of them whole, so that their loads go out together
-    const auto run = [&](int k0, auto nb, auto full) {
-        constexpr int NB = decltype(nb)::value;
-        constexpr bool FULL = decltype(full)::value;
-        Frag2 fa[NB][MT], fb[NB][NT];
-        float sa[NB][MT], sb[NB][NT][BT ? 1 : 4];
 #pragma unroll
-        for (int u = 0; u < NB; u++) {
-            const int kt = k0 + u * DW;
-            const int64_t k = (int64_t)kt * kBlk;
-            const int n = FULL ? kBlk : g.K - kt * kBlk;
+    for (int i = 0; i < S; i++) issue(i, i);
+    int slot = 0;
+    for (int i = 0; i < count; i++) {
+        pipe::wait_vm<(S - 1) * LPB>();
+        __builtin_amdgcn_sched_barrier(0);
+        const uint8_t *const d = ring + slot * BLK;
+        Frag2 fa[MT], fb;
+        float sa[MT];
+        float4 sb;
 #pragma unroll
-            for (int j = 0; j < NT; j++) {
-                fb[u][j] = direct_frag<FULL>(pb[j] + k, h, n);
+        for (int q = 0; q < 2; q++) fb.c[q] = *reinterpret_cast<const uint4 *>(d + OB + l16 * kBlk + ch[q]);
 #pragma unroll
-                for (int r = 0; r < (BT ? 1 : 4); r++)
-                    sb[u][j][r] = BT || n0 + 16 * j + 4 * h + r < g.N ? qb[j][kt * g.ldsb + r] : 0.f;
-            }
+        for (int t = 0; t < MT; t++) {
 #pragma unroll
-            for (int i = 0; i < MT; i++) {
-                fa[u][i] = direct_frag<FULL>(pa[i] + k, h, n);
-                sa[u][i] = qa[i][kt * g.ldsa];
+            for (int q = 0; q < 2; q++) fa[t].c[q] = *reinterpret_cast<const uint4 *>(d + (16 * t + l16) * kBlk + ch[q]);
+            sa[t] = *reinterpret_cast<const float *>(d + OS + (16 * t + l16) * 4);
+        }
+        if constexpr (BT) sb.x = *reinterpret_cast<const float *>(d + OS + 256);
+        else sb = *reinterpret_cast<const float4 *>(d + OS + 256 + 16 * h);
+        // the slot's values are in registers before its next block may land
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        issue(slot, i + S);
+        slot = slot + 1 == S ? 0 : slot + 1;
+        if (wave + i * DW == nk - 1 && ktail % 16 != 0) {  // the row's end inside a chunk
+#pragma unroll
+            for (int q = 0; q < 2; q++) {
+                const int n = ktail - (4 * q + h) * 16;
+                fb.c[q] = keep_bytes(fb.c[q], n);
+#pragma unroll
+                for (int t = 0; t < MT; t++) fa[t].c[q] = keep_bytes(fa[t].c[q], n);
             }
         }
 #pragma unroll
-        for (int u = 0; u < NB; u++)
+        for (int t = 0; t < MT; t++) {
+            const v4f p = few_block<FA, FB, BF16OUT>(fa[t], fb);
+            const float s4[4] = {sb.x, BT ? sb.x : sb.y, BT ? sb.x : sb.z, BT ? sb.x : sb.w};
 #pragma unroll
-            for (int i = 0; i < MT; i++)
-#pragma unroll
-                for (int j = 0; j < NT; j++) {
-                    const v4f p = direct_block<FA, FB, BF16OUT>(fa[u][i], fb[u][j]);
-#pragma unroll
-                    for (int r = 0; r < 4; r++)
-                        acc[i][j][r] = __builtin_fmaf(p[r], sa[u][i] * sb[u][j][BT ? 0 : r], acc[i][j][r]);
-                }
-    };
-    using I1 = std::integral_constant<int, 1>;
-    const int nfull = g.K / kBlk;
-    int k0 = wave;
-    for (; k0 + (U - 1) * DW < nfull; k0 += DW * U) run(k0, std::integral_constant<int, U>{}, std::true_type{});
-    for (; k0 < nfull; k0 += DW) run(k0, I1{}, std::true_type{});
-    if (k0 < nk) run(k0, I1{}, std::false_type{});
+            for (int r = 0; r < 4; r++) acc[t][r] = __builtin_fmaf(p[r], sa[t] * s4[r], acc[t][r]);
+        }
+    }
+    pipe::wait_vm<0>();
+    pipe::barrier();  // every wave's blocks are done with: the join may use their LDS
 
-    // lane: row m = l16 of tile i, columns 4 h .. 4 h + 3 of tile j
+    // lane: row m = l16 of tile t, columns 4 h .. 4 h + 3
+    float *const sJ = reinterpret_cast<float *>(sR);
 #pragma unroll
-    for (int i = 0; i < MT; i++)
-#pragma unroll
-        for (int j = 0; j < NT; j++)
-            *reinterpret_cast<float4 *>(&sJ[wave][16 * i + l16][16 * j + 4 * h]) =
-                make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+    for (int t = 0; t < MT; t++)
+        *reinterpret_cast<float4 *>(&sJ[(wave * DM + 16 * t + l16) * 20 + 4 * h]) =
+            make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
     __syncthreads();
-    for (int t = tid; t < DM * DN / 4; t += 64 * DW) {
-        const int m = t / (DN / 4), n = t % (DN / 4) * 4;
+    if (tid < DM * 4) {
+        const int m = tid / 4, n = tid % 4 * 4;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < DW; w++) {
-            const float4 x = *reinterpret_cast<const float4 *>(&sJ[w][m][n]);
+            const float4 x = *reinterpret_cast<const float4 *>(&sJ[(w * DM + m) * 20 + n]);
             v[0] += x.x;
             v[1] += x.y;
             v[2] += x.z;
             v[3] += x.w;
         }
-        block_store4<BF16OUT>(g, m0 + m, n0 + n, v);
+        block_store4<BF16OUT>(g, m, n0 + n, v);
     }
 }
 
-template <int FA, int FB, bool BT, bool BF16OUT, int MT, int NT, int U>
-hipError_t launch_block_gemm_direct(BlockGemmArgs g, hipStream_t s) {
-    g.tiles_m = (g.M + 16 * MT - 1) / (16 * MT);
-    g.tiles_n = (g.N + 16 * NT - 1) / (16 * NT);
-    hipLaunchKernelGGL((k_block_gemm_direct<FA, FB, BT, BF16OUT, MT, NT, U>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
-                       dim3(64 * DW), 0, s, g);
+template <int FA, int FB, bool BT, bool BF16OUT, int AI, int S>
+hipError_t launch_block_gemm_few(const BlockGemmArgs &g, hipStream_t s) {
+    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, BT, BF16OUT, AI, S>), dim3((unsigned)((g.N + 15) / 16)), dim3(64 * DW), 0,
+                       s, g);
     return hipGetLastError();
 }
 
@@ -649,21 +697,26 @@ hipError_t launch_block_gemm_pipe(BlockGemmArgs g, hipStream_t s) {
     g.tiles_m = (g.M + PM - 1) / PM;
     g.tiles_n = (g.N + PN - 1) / PN;
     hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, BF16OUT, CFG>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
-                       dim3(64 * CFG::WM * CFG::WN), 0, s, g);
+                       dim3(64 * CFG::WM * CFG::WN * CFG::KG), 0, s, g);
     return hipGetLastError();
 }
 
 template <int FA, int FB, bool BT, bool BF16OUT>
 hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
-    if (g.M <= 16) return launch_block_gemm_direct<FA, FB, BT, BF16OUT, 1, 1, 4>(g, s);
-    if (g.M <= 32) return launch_block_gemm_direct<FA, FB, BT, BF16OUT, 2, 1, 4>(g, s);
-    if (g.M <= 48) return launch_block_gemm_direct<FA, FB, BT, BF16OUT, 3, 1, 2>(g, s);
-    if (g.M <= 64) return launch_block_gemm_direct<FA, FB, BT, BF16OUT, 4, 1, 2>(g, s);
-    // the pipelined kernel: whole 16-byte chunks of K, aligned rows, offsets in 31 bits
+    // straight to LDS: aligned rows, offsets in 31 bits
     const int64_t nk = (g.K + kBlk - 1) / kBlk, lim = (int64_t)1 << 31;
-    const bool pipelined = g.K % 16 == 0 && g.lda % 16 == 0 && g.ldb % 16 == 0 && (uintptr_t)g.a % 16 == 0 &&
-                           (uintptr_t)g.b % 16 == 0 && 256 * g.lda < lim && 256 * g.ldb < lim &&
-                           (nk * g.ldsa + 256) * 4 < lim && (nk * g.ldsb + 256) * 4 < lim;
+    const bool aligned = g.lda % 16 == 0 && g.ldb % 16 == 0 && (uintptr_t)g.a % 16 == 0 && (uintptr_t)g.b % 16 == 0 &&
+                         256 * g.lda < lim && 256 * g.ldb < lim && (nk * g.ldsa + 256) * 4 < lim &&
+                         (nk * g.ldsb + 256) * 4 < lim;
+    if (aligned && g.M <= 64) {
+        if (g.M <= 8) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 1, 2>(g, s);
+        if (g.M <= 16) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 2, 2>(g, s);
+        if (g.M <= 32) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 4, 3>(g, s);
+        if (g.M <= 48) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 6, 2>(g, s);
+        return launch_block_gemm_few<FA, FB, BT, BF16OUT, 8, 1>(g, s);
+    }
+    // the pipelined kernels: whole 16-byte chunks of K
+    const bool pipelined = aligned && g.K % 16 == 0;
     if (pipelined) {
         const int64_t t256 = (int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256);
         if (t256 < 256) return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg128x128>(g, s);
