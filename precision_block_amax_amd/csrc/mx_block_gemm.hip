@@ -11,8 +11,7 @@ MX_PAIR(0, 0) MX_PAIR(0, 1) MX_PAIR(1, 0) MX_PAIR(1, 1)
 
 hipError_t launch_block_gemm(const BlockGemmArgs &g, int fa, int fb, bool bt, bool bf16_out, hipStream_t s) {
     if (g.K == 0) {
-        // at most 2^22 tiles of 2^14 elements: up to 2^28 workgroups of 256, below 2^32 threads
-        // only up to 2^24 of them; the rows beyond go in further launches
+        // 256 elements per workgroup, at most 2^31 of them per launch
         const int64_t rows = ((int64_t)1 << 31) / g.N > 0 ? ((int64_t)1 << 31) / g.N : 1;
         for (int64_t m = 0; m < g.M; m += rows) {
             const int mr = (int)min(rows, (int64_t)g.M - m);

@@ -10,8 +10,8 @@
 // holds one row m of C and 16 columns: sa is one value per lane, and with a
 // tiled B so is sa * sb.
 //
-// fp32 output: FP8 codes are converted to bf16 (exact) and multiplied by
-// V_MFMA_F32_32X32X16_BF16, whose products are exact and whose sums lose no
+// fp32 output: FP8 codes are converted to fp16 (exact) and multiplied by
+// V_MFMA_F32_32X32X16_F16, whose products are exact and whose sums lose no
 // more than fp32 does.  bf16 output: V_MFMA_F32_32X32X64_F8F6F4 on the
 // codes themselves, twice the rate.  Measured on gfx950, that instruction adds
 // the products of 32 K in a window ending 2^-13 below the largest (the
@@ -91,24 +91,56 @@ __device__ __forceinline__ v16f block_fp8(const Frag &a, const Frag &b) {
 }
 
 typedef float v4f __attribute__((ext_vector_type(4)));
+// 8 codes (lo: 0 .. 3, hi: 4 .. 7) as fp16, exact: E5M2 is the upper byte of an fp16 (one byte permute for
+// two codes, half the time of a conversion instruction), E4M3 lies within fp16's range, subnormals too
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+template <int F>
+__device__ __forceinline__ v8h to_f16x8(uint32_t lo, uint32_t hi) {
+    uint32_t w[4];
+    if constexpr (F == E5M2) {
+        w[0] = __builtin_amdgcn_perm(0u, lo, 0x010C000Cu);
+        w[1] = __builtin_amdgcn_perm(0u, lo, 0x030C020Cu);
+        w[2] = __builtin_amdgcn_perm(0u, hi, 0x010C000Cu);
+        w[3] = __builtin_amdgcn_perm(0u, hi, 0x030C020Cu);
+    } else {
+        w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
+        w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
+        w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false));
+        w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true));
+    }
+    return __builtin_bit_cast(v8h, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
 struct Frag16 {
-    v8bf v[8];
+    v8h v[8];
 };
 template <int F>
-__device__ __forceinline__ Frag16 to_bf16(const Frag &f) {
+__device__ __forceinline__ Frag16 to_f16(const Frag &f) {
     Frag16 o;
 #pragma unroll
     for (int q = 0; q < 4; q++) {
-        o.v[2 * q] = to_bf16x8<F>(f.c[q].x, f.c[q].y, 1.0f);
-        o.v[2 * q + 1] = to_bf16x8<F>(f.c[q].z, f.c[q].w, 1.0f);
+        o.v[2 * q] = to_f16x8<F>(f.c[q].x, f.c[q].y);
+        o.v[2 * q + 1] = to_f16x8<F>(f.c[q].z, f.c[q].w);
     }
     return o;
 }
-__device__ __forceinline__ v16f block_bf16(const Frag16 &a, const Frag16 &b) {
+__device__ __forceinline__ v16f block_f16(const Frag16 &a, const Frag16 &b) {
     v16f p = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int s = 0; s < 8; s++) p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b.v[s], a.v[s], p, 0, 0, 0);
+    for (int s = 0; s < 8; s++) p = __builtin_amdgcn_mfma_f32_32x32x16_f16(b.v[s], a.v[s], p, 0, 0, 0);
     return p;
+}
+
+// the first n bytes of v, the rest 0
+__device__ __forceinline__ uint4 keep_bytes(uint4 v, int n) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int d = 0; d < 4; d++) {
+        const int k = n - 4 * d;
+        w[d] = k >= 4 ? w[d] : k <= 0 ? 0u : w[d] & ((1u << (8 * k)) - 1u);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -132,7 +164,7 @@ __device__ __forceinline__ uint4 load16(const uint8_t *p, int n) {
 }
 
 template <int FA, int FB, bool BT, bool BF16OUT>
-__global__ __launch_bounds__(GNT, 2) void k_block_gemm(BlockGemmArgs g) {
+__global__ __launch_bounds__(GNT, BF16OUT ? 2 : 1) void k_block_gemm(BlockGemmArgs g) {
     __shared__ __attribute__((aligned(16))) uint8_t sA[2][GB * kBlk], sB[2][GB * kBlk];
     __shared__ __attribute__((aligned(16))) float sS[2][2 * GB];  // A's rows, B's rows
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -189,19 +221,19 @@ __global__ __launch_bounds__(GNT, 2) void k_block_gemm(BlockGemmArgs g) {
 #pragma unroll
         for (int j = 0; j < 2; j++) {
             fb[j] = read_frag(sB[b], wn * 64 + j * 32 + l32, h);
-            if constexpr (!BF16OUT) gb[j] = to_bf16<FB>(fb[j]);
+            if constexpr (!BF16OUT) gb[j] = to_f16<FB>(fb[j]);
         }
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             const Frag fa = read_frag(sA[b], wm * 64 + i * 32 + l32, h);
             Frag16 ga;
-            if constexpr (!BF16OUT) ga = to_bf16<FA>(fa);
+            if constexpr (!BF16OUT) ga = to_f16<FA>(fa);
             const float sa = ss[wm * 64 + i * 32 + l32];
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 v16f p;
                 if constexpr (BF16OUT) p = block_fp8<FA, FB>(fa, fb[j]);
-                else p = block_bf16(ga, gb[j]);
+                else p = block_f16(ga, gb[j]);
                 if constexpr (BT) {
                     const float s = sa * ss[GB + wn * 64];
 #pragma unroll
@@ -254,11 +286,14 @@ constexpr int kDead = (int)0x80000000u;  // a lane offset beyond every buffer: t
 // Configurations: tiles per wave, waves, ring.  KG groups of waves take every KG-th stage each, with
 // rings of their own, and their sums meet at the end: a 128 x 128 tile has work for four waves of 64 x 64
 // only, and a SIMD with one wave neither multiplies while it reads LDS nor the other way round.
-struct Cfg256x256 { static constexpr int TI = 4, WM = 2, WN = 4, NS = 2, KG = 1; };
-struct Cfg256x128 { static constexpr int TI = 2, WM = 4, WN = 2, NS = 2, KG = 1; };
-struct Cfg128x128 { static constexpr int TI = 2, WM = 2, WN = 2, NS = 2, KG = 2; };
+// PF: prefetch into L2 (below).
+struct Cfg256x256 { static constexpr int TI = 4, WM = 2, WN = 4, NS = 2, KG = 1; static constexpr bool PF = false; };
+struct Cfg256x128 { static constexpr int TI = 2, WM = 4, WN = 2, NS = 2, KG = 1; static constexpr bool PF = false; };
+struct Cfg128x128 { static constexpr int TI = 2, WM = 2, WN = 2, NS = 2, KG = 2; static constexpr bool PF = false; };
+struct Cfg128x128Far : Cfg128x128 { static constexpr bool PF = true; };
 
-template <int FA, int FB, bool BT, bool BF16OUT, class CFG>
+// RAG: K ends inside a chunk of 16 bytes
+template <int FA, int FB, bool BT, bool BF16OUT, class CFG, bool RAG>
 __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN * CFG::KG / 4) void k_block_gemm_pipe(BlockGemmArgs g) {
     constexpr int TI = CFG::TI, WM = CFG::WM, WN = CFG::WN, NS = CFG::NS, KG = CFG::KG;
     static_assert(KG == 1 || (KG == 2 && TI == 2), "the join swaps two rows of tiles");
@@ -267,7 +302,8 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     static_assert(NIA >= 1 && NIB >= 1 && PM % (8 * NW) == 0 && PN % (8 * NW) == 0, "load split");
     static_assert((PM + PN) / 64 <= NW, "one scale load per wave");
     static_assert((NS & (NS - 1)) == 0, "ring");
-    constexpr int LPW = NIA + NIB + 1;                   // loads of a wave per stage
+    constexpr bool PF = CFG::PF;
+    constexpr int LPW = NIA + NIB + 1 + PF;              // loads of a wave per stage
     constexpr int ST = (PM + PN) * kBlk, SR = 2 * NS;
     // A's stages of codes, then B's: a fragment read is one of eight lane offsets (four 32-byte
     // steps of K, two operands), the stage's place and a constant
@@ -276,6 +312,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     // scales, in a ring of their own: the last tile of a stage is scaled in the next one, while the
     // loads that reuse the stage's codes are under way
     __shared__ __attribute__((aligned(16))) float sScales[KG * SR * (PM + PN)];
+    __shared__ uint32_t sDump[PF ? 64 : 1];  // where the prefetches' words go
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave_all = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int grp = KG == 1 ? 0 : wave_all / NW, wave = wave_all % NW;
@@ -285,7 +322,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     int tm, tn;
     block_tile_of(g, tm, tn);
     const int m0 = tm * PM, n0 = tn * PN;
-    const int nk = (g.K + kBlk - 1) / kBlk, ktail = g.K - (nk - 1) * kBlk;  // ktail a multiple of 16
+    const int nk = (g.K + kBlk - 1) / kBlk, ktail = g.K - (nk - 1) * kBlk;
     const int mrows = min(PM, g.M - m0), nrows = min(PN, g.N - n0);
     const int lda = (int)g.lda, ldb = (int)g.ldb;
     const pipe::v4i rA = pipe::rsrc(g.a + (int64_t)m0 * lda, (uint32_t)mrows * lda);
@@ -318,6 +355,20 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     const int vS = (isA || !BT ? srow : srow / kBlk) * 4;
     float *const sdst = sS + (isA ? 0 : PM) + 64 * sw;
 
+    // Prefetch into L2.  A stage takes 128 bytes of each row, rows far apart; operands that come from beyond
+    // the last-level cache then open a DRAM page for every one of them, and a stage's loads wait for its
+    // slowest.  One wave of either group fetches a word of every line of whole KiB of rows, the next KiB of
+    // K, a few rows per stage: the first group A's rows, the second B's.  The 32 tiles that an XCD works on
+    // are 8 x 4 (block_tile_of), so a workgroup takes a quarter of its A rows and an eighth of its B rows.
+    // 1000 x 4096 x 28672: 184 us without, 157 with; two or four KiB ahead 166, 168; a line per row and
+    // stage, three stages ahead, 168.
+    static_assert(!PF || KG == 2, "a group for each operand");
+    constexpr int PW = 8 / KG;  // stages of a group per KiB
+    const bool pw = PF && wave == 0;
+    const int pper = (grp ? PN / 8 : PM / 4) / PW, pbase = grp ? (tm & 7) * (PN / 8) : (tn & 3) * (PM / 4);
+    const int prow0 = pbase + lane / 8, plim = lane / 8 < pper ? (grp ? nrows : mrows) : 0, pld = grp ? ldb : lda;
+    const pipe::v4i rP = grp ? rB : rA;
+
     const auto issue = [&](int u, int it) {  // the group's stage number `it` into place u
         const int kt = it * KG + grp;
         const bool live = kt < nk, last = kt == nk - 1;
@@ -334,6 +385,10 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
 #pragma unroll
         for (int q = 0; q < NIB; q++) pipe::dma16(rB, dB + q * 1024, b[q & 1], so + q * 8 * ldb);
         dma4(rS, sdst + (it & (SR - 1)) * (PM + PN), live ? vS : kDead, live ? kt * (int)lds_ * 4 : 0);
+        if constexpr (PF) {
+            const int pr = prow0 + it % PW * pper, pk = (it / PW + 1) * 1024 + (lane & 7) * 128;
+            dma4(rP, sDump, pw && pr < plim && pk < g.K ? pr * pld + pk : kDead, 0);
+        }
     };
 
     float acc[TI][2][16];
@@ -390,8 +445,20 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     };
 
     const auto stage = [&](int u, int it) {
-        pipe::wait_vm<(NS - 2) * LPW>();
+        pipe::wait_vm<(NS - 2) * LPW + PF>();  // the youngest load is a prefetch
         pipe::barrier();
+        if constexpr (RAG) {
+            if (it == (nk - 1) / KG) {  // the last stage: the bytes past K in the rows' last chunks become 0
+                static_assert(PM + PN == 64 * NW, "a thread for each row");
+                if (it * KG + grp == nk - 1 && ktail % 16 != 0) {
+                    const int t = wave * 64 + lane, row = t < PM ? t : t - PM;
+                    uint8_t *const base = t < PM ? sC + u * PM * kBlk : sC + OB + u * PN * kBlk;
+                    uint4 *const q = reinterpret_cast<uint4 *>(base + swz<128>(row, ktail / 16));
+                    *q = keep_bytes(*q, ktail % 16);
+                }
+                pipe::barrier();
+            }
+        }
         const float *const ss = sS + (it & (SR - 1)) * (PM + PN);
         const int ua = u * PM * kBlk, ub = u * PN * kBlk;
         Frag fa[2], fb[2];
@@ -405,9 +472,9 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
         const float sbt = BT ? ss[scol] : 1.0f;
         issue((u + NS - 1) & (NS - 1), it + NS - 1);
         if constexpr (!BF16OUT) {
-            ga = to_bf16<FA>(fa[0]);
+            ga = to_f16<FA>(fa[0]);
 #pragma unroll
-            for (int j = 0; j < 2; j++) gb[j] = to_bf16<FB>(fb[j]);
+            for (int j = 0; j < 2; j++) gb[j] = to_f16<FB>(fb[j]);
         }
         static_for<0, 2 * TI>([&](auto tt) {
             constexpr int t = decltype(tt)::value, i = t / 2, j = t % 2;
@@ -417,10 +484,10 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
             read_sb(sb);
             v16f p;
             if constexpr (BF16OUT) p = block_fp8<FA, FB>(fa[i & 1], fb[j]);
-            else p = block_bf16(ga, gb[j]);
+            else p = block_f16(ga, gb[j]);
             __builtin_amdgcn_sched_barrier(0);
             promote(acc[pi][pj], sb);
-            if constexpr (!BF16OUT && j == 1 && i + 1 < TI) ga = to_bf16<FA>(fa[(i + 1) & 1]);
+            if constexpr (!BF16OUT && j == 1 && i + 1 < TI) ga = to_f16<FA>(fa[(i + 1) & 1]);
             pp = p;
             ps = BT ? sa[i] * sbt : sa[i];
             psb = ss + scol + j * 32;
@@ -518,8 +585,8 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
 }
 
 // ---------------------------------------------------------------------------
-// Kernel for few rows (up to 64): 16 columns of C per workgroup, its eight waves
-// each taking every eighth block of K for all of them, joined in LDS.
+// Kernel for few rows: tiles of 8 AI x 16 NT of C, a workgroup's eight waves each
+// taking every eighth block of K for the whole tile, joined in LDS.
 //
 // With one row the product is bound by B's bytes.  16 rows of B per workgroup
 // make 256 workgroups from N = 4096 on, and the waves' blocks in flight cover
@@ -543,56 +610,46 @@ __device__ __forceinline__ v4f few_block(const Frag2 &a, const Frag2 &b) {
             v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)v.x, (int)v.y, (int)v.z, (int)v.w},
             v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w}, p, FB, FA, 0, 0, 0, 0);
     } else {
-        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(u.x, u.y, 1.f), to_bf16x8<FA>(x.x, x.y, 1.f), p, 0, 0, 0);
-        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(u.z, u.w, 1.f), to_bf16x8<FA>(x.z, x.w, 1.f), p, 0, 0, 0);
-        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(v.x, v.y, 1.f), to_bf16x8<FA>(y.x, y.y, 1.f), p, 0, 0, 0);
-        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(v.z, v.w, 1.f), to_bf16x8<FA>(y.z, y.w, 1.f), p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_f16x8<FB>(u.x, u.y), to_f16x8<FA>(x.x, x.y), p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_f16x8<FB>(u.z, u.w), to_f16x8<FA>(x.z, x.w), p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_f16x8<FB>(v.x, v.y), to_f16x8<FA>(y.x, y.y), p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_f16x8<FB>(v.z, v.w), to_f16x8<FA>(y.z, y.w), p, 0, 0, 0);
     }
     return p;
 }
 
-// the first n bytes of v, the rest 0
-__device__ __forceinline__ uint4 keep_bytes(uint4 v, int n) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int d = 0; d < 4; d++) {
-        const int k = n - 4 * d;
-        w[d] = k >= 4 ? w[d] : k <= 0 ? 0u : w[d] & ((1u << (8 * k)) - 1u);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// AI: loads of 8 rows of A (M <= 8 AI); rows of the last tile beyond them are whatever LDS holds, and reach
-// only rows of C that do not exist
-template <int FA, int FB, bool BT, bool BF16OUT, int AI, int S>
+// AI: loads of 8 rows of A; with an odd AI the rest of the matrix instruction's 16 rows is whatever LDS
+// holds, and reaches only rows of C that do not exist
+template <int FA, int FB, bool BT, bool BF16OUT, int AI, int NT, int S>
 __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(BlockGemmArgs g) {
-    constexpr int MT = (AI + 1) / 2, DM = 16 * MT;
-    constexpr int OB = MT * 2048, OS = OB + 2048, BLK = OS + 512;  // a block: A's rows, B's 16, scales of A, of B
-    constexpr int LPB = AI + 4;                                    // loads per block
-    constexpr int JOIN = DW * DM * 20 * 4;                         // the waves' sums, rows of 16 + 4 floats
+    constexpr int MT = (AI + 1) / 2, DM = 16 * MT, DN = 16 * NT, JP = DN + 4;
+    constexpr int OB = MT * 2048, OS = OB + NT * 2048, BLK = OS + 512;  // a block: A's rows, B's, scales of A, of B
+    constexpr int LPB = AI + 2 * NT + 2;                                // loads per block
+    constexpr int JOIN = DW * DM * JP * 4;                              // the waves' sums
     __shared__ __attribute__((aligned(16))) uint8_t sR[DW * S * BLK > JOIN ? DW * S * BLK : JOIN];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, h = lane >> 4;
-    const int n0 = blockIdx.x * 16;
+    int tm, tn;
+    block_tile_of(g, tm, tn);
+    const int m0 = tm * 8 * AI, n0 = tn * DN;
     const int nk = (g.K + kBlk - 1) / kBlk, ktail = g.K - (nk - 1) * kBlk;
-    const int lda = (int)g.lda, ldb = (int)g.ldb, nrows = min(16, g.N - n0);
+    const int lda = (int)g.lda, ldb = (int)g.ldb, mrows = min(8 * AI, g.M - m0), nrows = min(DN, g.N - n0);
     // rows end at a multiple of 16 bytes: an aligned 16 bytes that hold a byte of the row
     const int kend = (g.K + 15) & ~15;
-    const pipe::v4i rA = pipe::rsrc(g.a, (uint32_t)((g.M - 1) * lda + kend));
+    const pipe::v4i rA = pipe::rsrc(g.a + (int64_t)m0 * lda, (uint32_t)((mrows - 1) * lda + kend));
     const pipe::v4i rB = pipe::rsrc(g.b + (int64_t)n0 * ldb, (uint32_t)((nrows - 1) * ldb + kend));
-    const pipe::v4i rSA = pipe::rsrc(g.as, (uint32_t)(((int64_t)(nk - 1) * g.ldsa + g.M) * 4));
+    const pipe::v4i rSA = pipe::rsrc(g.as + m0, (uint32_t)(((int64_t)(nk - 1) * g.ldsa + mrows) * 4));
     const pipe::v4i rSB = pipe::rsrc(g.bs + (BT ? n0 / kBlk : n0), (uint32_t)(((int64_t)(nk - 1) * g.ldsb + (BT ? 1 : nrows)) * 4));
     // lane l of a load: 16-byte slot l % 8 of row l / 8, logical chunk (l % 8) ^ key
     const int lr = lane / 8;
-    int vA[AI], vB[2], cA[2];
+    int vA[AI], vB[2 * NT], cA[2];
 #pragma unroll
-    for (int o = 0; o < 2; o++) {
-        cA[o] = ((lane & 7) ^ swz_key<128>(lr + 8 * o)) << 4;
-        vB[o] = lr + 8 * o < nrows ? (lr + 8 * o) * ldb + cA[o] : kDead;
-    }
+    for (int o = 0; o < 2; o++) cA[o] = ((lane & 7) ^ swz_key<128>(lr + 8 * o)) << 4;
 #pragma unroll
-    for (int o = 0; o < AI; o++) vA[o] = lr + 8 * o < g.M ? (lr + 8 * o) * lda + cA[o & 1] : kDead;
-    const int vSA = lane < g.M ? lane * 4 : kDead, vSB = BT ? 0 : lane < nrows ? lane * 4 : kDead;
+    for (int o = 0; o < 2 * NT; o++) vB[o] = lr + 8 * o < nrows ? (lr + 8 * o) * ldb + cA[o & 1] : kDead;
+#pragma unroll
+    for (int o = 0; o < AI; o++) vA[o] = lr + 8 * o < mrows ? (lr + 8 * o) * lda + cA[o & 1] : kDead;
+    const int vSA = lane < mrows ? lane * 4 : kDead, vSB = BT ? 0 : lane < nrows ? lane * 4 : kDead;
     uint8_t *const ring = sR + wave * S * BLK;
 
     const auto issue = [&](int slot, int i) {  // block number i of this wave
@@ -604,16 +661,18 @@ __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(BlockGemmArgs g) {
 #pragma unroll
         for (int o = 0; o < AI; o++) pipe::dma16(rA, d + o * 1024, in[o & 1] ? vA[o] : kDead, so);
 #pragma unroll
-        for (int o = 0; o < 2; o++) pipe::dma16(rB, d + OB + o * 1024, in[o] ? vB[o] : kDead, so);
+        for (int o = 0; o < 2 * NT; o++) pipe::dma16(rB, d + OB + o * 1024, in[o & 1] ? vB[o] : kDead, so);
         dma4(rSA, d + OS, live ? vSA : kDead, live ? kt * (int)g.ldsa * 4 : 0);
         dma4(rSB, d + OS + 256, live ? vSB : kDead, live ? kt * (int)g.ldsb * 4 : 0);
     };
 
-    float acc[MT][4];
+    float acc[MT][NT][4];
 #pragma unroll
     for (int i = 0; i < MT; i++)
 #pragma unroll
-        for (int r = 0; r < 4; r++) acc[i][r] = 0.f;
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) acc[i][j][r] = 0.f;
     const int count = nk > wave ? (nk - wave + DW - 1) / DW : 0;
     const int ch[2] = {(h ^ swz_key<128>(l16)) << 4, ((4 + h) ^ swz_key<128>(l16)) << 4};  // this lane's chunks: h and 4 + h
 
@@ -624,19 +683,28 @@ __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(BlockGemmArgs g) {
         pipe::wait_vm<(S - 1) * LPB>();
         __builtin_amdgcn_sched_barrier(0);
         const uint8_t *const d = ring + slot * BLK;
-        Frag2 fa[MT], fb;
-        float sa[MT];
-        float4 sb;
+        Frag2 fa[MT], fb[NT];
+        float sa[MT], sb[NT][BT ? 1 : 4];
 #pragma unroll
-        for (int q = 0; q < 2; q++) fb.c[q] = *reinterpret_cast<const uint4 *>(d + OB + l16 * kBlk + ch[q]);
+        for (int j = 0; j < NT; j++) {
+#pragma unroll
+            for (int q = 0; q < 2; q++) fb[j].c[q] = *reinterpret_cast<const uint4 *>(d + OB + (16 * j + l16) * kBlk + ch[q]);
+            if constexpr (BT) {
+                sb[j][0] = *reinterpret_cast<const float *>(d + OS + 256);
+            } else {
+                const float4 t = *reinterpret_cast<const float4 *>(d + OS + 256 + 64 * j + 16 * h);
+                sb[j][0] = t.x;
+                sb[j][1] = t.y;
+                sb[j][2] = t.z;
+                sb[j][3] = t.w;
+            }
+        }
 #pragma unroll
         for (int t = 0; t < MT; t++) {
 #pragma unroll
             for (int q = 0; q < 2; q++) fa[t].c[q] = *reinterpret_cast<const uint4 *>(d + (16 * t + l16) * kBlk + ch[q]);
             sa[t] = *reinterpret_cast<const float *>(d + OS + (16 * t + l16) * 4);
         }
-        if constexpr (BT) sb.x = *reinterpret_cast<const float *>(d + OS + 256);
-        else sb = *reinterpret_cast<const float4 *>(d + OS + 256 + 16 * h);
         // the slot's values are in registers before its next block may land
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
@@ -646,87 +714,110 @@ __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(BlockGemmArgs g) {
 #pragma unroll
             for (int q = 0; q < 2; q++) {
                 const int n = ktail - (4 * q + h) * 16;
-                fb.c[q] = keep_bytes(fb.c[q], n);
+#pragma unroll
+                for (int j = 0; j < NT; j++) fb[j].c[q] = keep_bytes(fb[j].c[q], n);
 #pragma unroll
                 for (int t = 0; t < MT; t++) fa[t].c[q] = keep_bytes(fa[t].c[q], n);
             }
         }
 #pragma unroll
-        for (int t = 0; t < MT; t++) {
-            const v4f p = few_block<FA, FB, BF16OUT>(fa[t], fb);
-            const float s4[4] = {sb.x, BT ? sb.x : sb.y, BT ? sb.x : sb.z, BT ? sb.x : sb.w};
+        for (int t = 0; t < MT; t++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) acc[t][r] = __builtin_fmaf(p[r], sa[t] * s4[r], acc[t][r]);
-        }
+            for (int j = 0; j < NT; j++) {
+                const v4f p = few_block<FA, FB, BF16OUT>(fa[t], fb[j]);
+#pragma unroll
+                for (int r = 0; r < 4; r++) acc[t][j][r] = __builtin_fmaf(p[r], sa[t] * sb[j][BT ? 0 : r], acc[t][j][r]);
+            }
     }
     pipe::wait_vm<0>();
     pipe::barrier();  // every wave's blocks are done with: the join may use their LDS
 
-    // lane: row m = l16 of tile t, columns 4 h .. 4 h + 3
+    // lane: row m = l16 of tile (t, j), columns 4 h .. 4 h + 3
     float *const sJ = reinterpret_cast<float *>(sR);
 #pragma unroll
     for (int t = 0; t < MT; t++)
-        *reinterpret_cast<float4 *>(&sJ[(wave * DM + 16 * t + l16) * 20 + 4 * h]) =
-            make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+            *reinterpret_cast<float4 *>(&sJ[(wave * DM + 16 * t + l16) * JP + 16 * j + 4 * h]) =
+                make_float4(acc[t][j][0], acc[t][j][1], acc[t][j][2], acc[t][j][3]);
     __syncthreads();
-    if (tid < DM * 4) {
-        const int m = tid / 4, n = tid % 4 * 4;
+    for (int i = tid; i < DM * DN / 4; i += 64 * DW) {
+        const int m = i / (DN / 4), n = i % (DN / 4) * 4;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < DW; w++) {
-            const float4 x = *reinterpret_cast<const float4 *>(&sJ[(w * DM + m) * 20 + n]);
+            const float4 x = *reinterpret_cast<const float4 *>(&sJ[(w * DM + m) * JP + n]);
             v[0] += x.x;
             v[1] += x.y;
             v[2] += x.z;
             v[3] += x.w;
         }
-        block_store4<BF16OUT>(g, m, n0 + n, v);
+        if (m < 8 * AI) block_store4<BF16OUT>(g, m0 + m, n0 + n, v);
     }
 }
 
-template <int FA, int FB, bool BT, bool BF16OUT, int AI, int S>
-hipError_t launch_block_gemm_few(const BlockGemmArgs &g, hipStream_t s) {
-    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, BT, BF16OUT, AI, S>), dim3((unsigned)((g.N + 15) / 16)), dim3(64 * DW), 0,
-                       s, g);
+template <int FA, int FB, bool BT, bool BF16OUT, int AI, int NT, int S>
+hipError_t launch_block_gemm_few(BlockGemmArgs g, hipStream_t s) {
+    g.tiles_m = (g.M + 8 * AI - 1) / (8 * AI);
+    g.tiles_n = (g.N + 16 * NT - 1) / (16 * NT);
+    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, BT, BF16OUT, AI, NT, S>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
+                       dim3(64 * DW), 0, s, g);
     return hipGetLastError();
 }
 
-template <int FA, int FB, bool BT, bool BF16OUT, class CFG>
+template <int FA, int FB, bool BT, bool BF16OUT, class CFG, bool RAG = false>
 hipError_t launch_block_gemm_pipe(BlockGemmArgs g, hipStream_t s) {
     constexpr int PM = CFG::WM * CFG::TI * 32, PN = CFG::WN * 64;
     g.tiles_m = (g.M + PM - 1) / PM;
     g.tiles_n = (g.N + PN - 1) / PN;
-    hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, BF16OUT, CFG>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
+    hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, BF16OUT, CFG, RAG>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
                        dim3(64 * CFG::WM * CFG::WN * CFG::KG), 0, s, g);
     return hipGetLastError();
 }
 
+// The kernel for a product.  us measured on an MI355X, N = 4096 and bf16 output where not said otherwise.
 template <int FA, int FB, bool BT, bool BF16OUT>
 hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
-    // straight to LDS: aligned rows, offsets in 31 bits
+    // All but the general kernel load straight to LDS: rows of whole aligned 16 bytes, offsets in 31 bits.
     const int64_t nk = (g.K + kBlk - 1) / kBlk, lim = (int64_t)1 << 31;
     const bool aligned = g.lda % 16 == 0 && g.ldb % 16 == 0 && (uintptr_t)g.a % 16 == 0 && (uintptr_t)g.b % 16 == 0 &&
                          256 * g.lda < lim && 256 * g.ldb < lim && (nk * g.ldsa + 256) * 4 < lim &&
                          (nk * g.ldsb + 256) * 4 < lim;
-    if (aligned && g.M <= 64) {
-        if (g.M <= 8) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 1, 2>(g, s);
-        if (g.M <= 16) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 2, 2>(g, s);
-        if (g.M <= 32) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 4, 3>(g, s);
-        if (g.M <= 48) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 6, 2>(g, s);
-        return launch_block_gemm_few<FA, FB, BT, BF16OUT, 8, 1>(g, s);
+    if (!aligned) {
+        g.tiles_m = (g.M + GB - 1) / GB;
+        g.tiles_n = (g.N + GB - 1) / GB;
+        hipLaunchKernelGGL((k_block_gemm<FA, FB, BT, BF16OUT>), dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(GNT), 0, s, g);
+        return hipGetLastError();
     }
-    // the pipelined kernels: whole 16-byte chunks of K
-    const bool pipelined = aligned && g.K % 16 == 0;
-    if (pipelined) {
-        const int64_t t256 = (int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256);
-        if (t256 < 256) return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg128x128>(g, s);
-        if constexpr (BF16OUT && BT) return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg256x256>(g, s);
-        else return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg256x128>(g, s);
+    const auto tiles = [&](int64_t m, int64_t n) { return (g.M + m - 1) / m * ((g.N + n - 1) / n); };
+    if (g.M <= 8) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 1, 1, 2>(g, s);
+    if (g.M <= 16) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 2, 1, 2>(g, s);
+    if (g.M <= 32) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 4, 1, 3>(g, s);
+    if (g.M <= 48) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 6, 1, 2>(g, s);
+    // 64 rows: 32 columns per workgroup read A half as often, 16 make twice the workgroups: 42 against 55 at
+    // N = 28672, K = 4096 (896 workgroups), 20 against 18 at K = 14336 (128)
+    if (g.M <= 64 && tiles(64, 32) < 256) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 8, 1, 1>(g, s);
+    // Up to two rounds of 64 x 32 tiles on the 256 CUs (the 128 x 128 tiles are then 64 at most): K = 14336, one
+    // round (M = 128) 21 against 64, two (256) 38 against 63; K = 4096, two 15 against 21, four (512) 27
+    // against 21.  float32: one 24 against 36, two 32 against 36, four 48 against 38.
+    if (g.M <= 64 || tiles(64, 32) <= 512) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 8, 2, 1>(g, s);
+    if (g.K % 16 != 0) return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg128x128, true>(g, s);
+    const int64_t r128 = (tiles(128, 128) + 255) / 256;
+    if constexpr (BF16OUT && BT) {
+        // a round of 256 x 256 tiles takes 1.75 us per 128 K, one of 128 x 128 tiles 0.70
+        const int64_t r256 = (tiles(256, 256) + 255) / 256;
+        if (5 * r256 <= 2 * r128) return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg256x256>(g, s);
+        // long rows, every CU busy: 1000 rows, K = 28672 184 without and 157 with the prefetch; 14336 79 and 75;
+        // 8192 43 and 45
+        if (g.K >= 12288 && tiles(128, 128) >= 256)
+            return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg128x128Far>(g, s);
+    } else {
+        // (with fp32 output or B's scales by column 256 x 256 tiles need more registers than there are)
+        // a round of 256 x 128 tiles takes 2.0 us per 128 K (fp32), one of 128 x 128 tiles 1.05
+        const int64_t r256 = (tiles(256, 128) + 255) / 256;
+        if (2 * r256 <= r128) return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg256x128>(g, s);
     }
-    g.tiles_m = (g.M + GB - 1) / GB;
-    g.tiles_n = (g.N + GB - 1) / GB;
-    hipLaunchKernelGGL((k_block_gemm<FA, FB, BT, BF16OUT>), dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(GNT), 0, s, g);
-    return hipGetLastError();
+    return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg128x128>(g, s);
 }
 
 template <int FA, int FB>

@@ -183,7 +183,25 @@ def test_gemm(mx, M, N, K, tile, bf16):
         check_product(c, a, fa, b, fb, tile, bf16)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 200, 256), (40, 200, 300), (300, 520, 640), (520, 300, 272)])
+# sizes beyond the small tiles: 128 x 128 (whole and ragged K, long rows), 256 x 256 and 256 x 128 tiles, odd edges
+LARGE = [(1100, 1100, 384), (1111, 1301, 4001), (1100, 1100, 130), (2048, 2048, 12352), (2051, 2177, 12304), (4096, 4096, 272),
+         (4100, 4250, 400), (4096, 2048, 144), (2300, 4100, 1000), (8200, 4099, 16)]
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+@pytest.mark.parametrize("tile", [True, False])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_gemm_large(mx, M, N, K, tile, bf16):
+    import torch
+    print("case", M, N, K, tile, bf16, flush=True)
+    for fa, fb in (("e4m3", "e4m3"), ("e5m2", "e4m3")):
+        a, b = operand(mx, M, K, fa, False, M + K, 3), operand(mx, N, K, fb, tile, N + K + 1, 3)
+        c = mx.block_gemm(*a, fa, *b, fb, out_dtype=torch.bfloat16 if bf16 else torch.float32)
+        check_product(c, a, fa, b, fb, tile, bf16)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 200, 256), (40, 200, 300), (300, 520, 640), (520, 300, 272), (1200, 1160, 272), (1201, 1160, 301),
+                                   (4200, 4100, 272)])
 @pytest.mark.parametrize("bf16", [True, False])
 def test_gemm_strides_and_guards(mx, M, N, K, bf16):
     """operands inside larger buffers whose other bytes are NaN codes and NaN scales, unaligned too; C inside a larger
@@ -219,13 +237,13 @@ def test_gemm_empty_k_and_sizes(mx, M):
     assert mx.block_gemm(*b, "e4m3", *a, "e4m3").shape == (0, M)
 
 
-@pytest.mark.parametrize("M", [1, 24, 60, 200, 600])
+@pytest.mark.parametrize("M,N", [(1, 300), (24, 300), (60, 300), (200, 300), (600, 300), (1200, 1200), (4200, 4100)])
 @pytest.mark.parametrize("bf16", [True, False])
-def test_gemm_nan_scales(mx, M, bf16):
+def test_gemm_nan_scales(mx, M, N, bf16):
     """a NaN scale of A's row m makes row m NaN, one of B's row n column n, and nothing else"""
     import torch
     dt = torch.bfloat16 if bf16 else torch.float32
-    N, K = 300, 640
+    K = 640
     x, w = data(M, K, 5), data(N, K, 6)
     x[M - 1, 200] = float("inf")
     w[37, 5] = float("nan")
@@ -240,7 +258,7 @@ def test_gemm_nan_scales(mx, M, bf16):
     want[:, 0:128] = True
     assert torch.equal(c.isnan(), want)
     # every row and column in turn at the edges of the kernels' tiles, in the first and in the last block
-    for m in {0, 4, 31, 63, 130} & set(range(M)):
+    for m in {0, 4, 31, 63, 130, 140} & set(range(M)):
         for blk in (0, 4):
             a, b = mx.block_quantize(data(M, K, 5), "e4m3"), mx.block_quantize(data(N, K, 6), "e4m3")
             a[1][blk, m], b[1][blk, 299 - m] = float("nan"), float("inf")
@@ -251,7 +269,7 @@ def test_gemm_nan_scales(mx, M, bf16):
             assert c[rest].isfinite().all()
 
 
-@pytest.mark.parametrize("M,N", [(1, 64), (40, 64), (300, 256)])
+@pytest.mark.parametrize("M,N", [(1, 64), (40, 64), (300, 256), (1200, 1200), (4200, 4100)])
 def test_gemm_small_terms_kept_in_fp32(mx, M, N):
     """float32 output: 1 + 2^-18 in one block, the small term 2^-9 * 2^-9, is exact.  Beside a large pair that cancels,
     fp32 holds the small terms to a step of the running sum only: the terms 448 * 448 = 200704 and their negative add
@@ -269,6 +287,28 @@ def test_gemm_small_terms_kept_in_fp32(mx, M, N):
     a[:, 41], b[:, 41] = big, big | 0x80
     c = mx.block_gemm(a, s[0], "e4m3", b, s[1], "e4m3", out_dtype=torch.float32)
     assert ((c - (1 + 2.0 ** -18)).abs() <= 2 * 2.0 ** -7).all()
+
+
+@pytest.mark.parametrize("M", [1, 40, 300, 1200, 4200])
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e5m2")])
+def test_gemm_smallest_and_largest_codes(mx, M, fa, fb):
+    """subnormal codes are numbers: their products, all multiples of one power of two and their sums below 2^24 of it,
+    are exact in float32; so are the largest codes' (128 of one product per block, an integer of 24 bits times a power of two)"""
+    import torch
+    N, K = 300 if M < 1000 else 1160 if M < 4000 else 4096, 256
+    g = torch.Generator(device="cuda").manual_seed(7)
+    top = {"e4m3": 8, "e5m2": 4}
+    rnd = lambda n, f: (torch.randint(0, top[f], (n, K), device="cuda", generator=g) +
+                        128 * torch.randint(0, 2, (n, K), device="cuda", generator=g)).to(torch.uint8)
+    one = lambda n: torch.ones(2, n, device="cuda")
+    a, b = rnd(M, fa), rnd(N, fb)
+    c = mx.block_gemm(a, one(M), fa, b, one(N), fb, out_dtype=torch.float32)
+    want = a.view(ref.F8[fa]).double() @ b.view(ref.F8[fb]).double().t().contiguous()
+    assert torch.equal(c.double(), want) and bool((want != 0).any())
+    big = {"e4m3": 0x7E, "e5m2": 0x7B}
+    a, b = torch.full_like(a, big[fa]), torch.full_like(b, big[fb])
+    c = mx.block_gemm(a, one(M), fa, b, one(N), fb, out_dtype=torch.float32)
+    assert (c.double() == 256 * ref.FMAX[fa] * ref.FMAX[fb]).all()
 
 
 @pytest.mark.parametrize("bf16", [True, False])
@@ -296,7 +336,9 @@ def test_gemm_repeats_bits_on_streams_and_in_graphs(mx):
     eager calls"""
     import torch
     for M, N, K, dt, tile in ((1, 1024, 2048, torch.bfloat16, True), (40, 512, 4096, torch.float32, False),
-                              (300, 512, 1024, torch.bfloat16, True), (600, 512, 1024, torch.float32, False)):
+                              (300, 512, 1024, torch.bfloat16, True), (1300, 1200, 1024, torch.float32, False),
+                              (1300, 1200, 1001, torch.bfloat16, True), (4200, 4200, 640, torch.bfloat16, True),
+                              (4200, 4200, 640, torch.float32, False)):
         a, b = operand(mx, M, K, "e4m3", False, 1), operand(mx, N, K, "e4m3", tile, 2)
         a2 = operand(mx, M, K, "e4m3", False, 9)
         want, want2 = (mx.block_gemm(*t, "e4m3", *b, "e4m3", out_dtype=dt) for t in (a, a2))
