@@ -263,8 +263,8 @@ __global__ __launch_bounds__(GNT, BF16OUT ? 2 : 1) void k_block_gemm(BlockGemmAr
 }
 
 // ---------------------------------------------------------------------------
-// Pipelined kernel: codes and scales straight to LDS, a ring of NS stages of
-// 128 K, of which NS - 1 are in flight.
+// Pipelined kernel: codes and scales straight to LDS, two stages of 128 K, one
+// of them in flight.
 //
 // WM x WN waves, each TI x 2 tiles of 32 x 32.  Within a stage the tiles follow
 // one another so that the matrix pipe never waits for the vector one: tile t's
@@ -283,27 +283,25 @@ __device__ __forceinline__ void dma4(pipe::v4i r, void *lds, int voff, int soff)
 
 constexpr int kDead = (int)0x80000000u;  // a lane offset beyond every buffer: the load writes zeros
 
-// Configurations: tiles per wave, waves, ring.  KG groups of waves take every KG-th stage each, with
+// Configurations: tiles per wave, waves.  KG groups of waves take every KG-th stage each, with
 // rings of their own, and their sums meet at the end: a 128 x 128 tile has work for four waves of 64 x 64
 // only, and a SIMD with one wave neither multiplies while it reads LDS nor the other way round.
 // PF: prefetch into L2 (below).
-struct Cfg256x256 { static constexpr int TI = 4, WM = 2, WN = 4, NS = 2, KG = 1; static constexpr bool PF = false; };
-struct Cfg256x128 { static constexpr int TI = 2, WM = 4, WN = 2, NS = 2, KG = 1; static constexpr bool PF = false; };
-struct Cfg128x128 { static constexpr int TI = 2, WM = 2, WN = 2, NS = 2, KG = 2; static constexpr bool PF = false; };
+struct Cfg256x256 { static constexpr int TI = 4, WM = 2, WN = 4, KG = 1; static constexpr bool PF = false; };
+struct Cfg256x128 { static constexpr int TI = 2, WM = 4, WN = 2, KG = 1; static constexpr bool PF = false; };
+struct Cfg128x128 { static constexpr int TI = 2, WM = 2, WN = 2, KG = 2; static constexpr bool PF = false; };
 struct Cfg128x128Far : Cfg128x128 { static constexpr bool PF = true; };
 
 // RAG: K ends inside a chunk of 16 bytes
 template <int FA, int FB, bool BT, bool BF16OUT, class CFG, bool RAG>
 __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN * CFG::KG / 4) void k_block_gemm_pipe(BlockGemmArgs g) {
-    constexpr int TI = CFG::TI, WM = CFG::WM, WN = CFG::WN, NS = CFG::NS, KG = CFG::KG;
+    constexpr int TI = CFG::TI, WM = CFG::WM, WN = CFG::WN, NS = 2, KG = CFG::KG;
     static_assert(KG == 1 || (KG == 2 && TI == 2), "the join swaps two rows of tiles");
     constexpr int NW = WM * WN, PM = WM * TI * 32, PN = WN * 64;
     constexpr int NIA = PM / 8 / NW, NIB = PN / 8 / NW;  // 1 KiB loads (8 rows) per wave and stage
     static_assert(NIA >= 1 && NIB >= 1 && PM % (8 * NW) == 0 && PN % (8 * NW) == 0, "load split");
     static_assert((PM + PN) / 64 <= NW, "one scale load per wave");
-    static_assert((NS & (NS - 1)) == 0, "ring");
     constexpr bool PF = CFG::PF;
-    constexpr int LPW = NIA + NIB + 1 + PF;              // loads of a wave per stage
     constexpr int ST = (PM + PN) * kBlk, SR = 2 * NS;
     // A's stages of codes, then B's: a fragment read is one of eight lane offsets (four 32-byte
     // steps of K, two operands), the stage's place and a constant
@@ -444,9 +442,12 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
         return f;
     };
 
-    const auto stage = [&](int u, int it) {
-        pipe::wait_vm<(NS - 2) * LPW + PF>();  // the youngest load is a prefetch
+    // Stage `it` of the group, in place u, has landed for every wave, and every wave is done with the reads of
+    // the stage before it, whose place takes the stage after it.
+    const auto arrive = [&](int u, int it) {
+        pipe::wait_vm<PF>();  // the youngest load is a prefetch
         pipe::barrier();
+        issue(u ^ 1, it + 1);
         if constexpr (RAG) {
             if (it == (nk - 1) / KG) {  // the last stage: the bytes past K in the rows' last chunks become 0
                 static_assert(PM + PN == 64 * NW, "a thread for each row");
@@ -459,18 +460,29 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
                 pipe::barrier();
             }
         }
+    };
+
+    // EARLY: a stage begins with its first fragments in registers.  All its LDS reads are out before its
+    // last two tiles, so the next stage arrives there: the barrier, the loads' issue and the next stage's
+    // first reads fall into those tiles' matrix work instead of standing between two stages.  fp32 output,
+    // 6144 x 4096 x 8192: 400 -> 381 us.  bf16 output has no registers left for it in 256 x 256 tiles (13
+    // spilled: 187 -> 210 us) and gains nothing in 128 x 128 (47.7, 48.9 us).
+    constexpr bool EARLY = !BF16OUT && !RAG;
+    Frag fa[2], fb[2];
+    const auto stage = [&](int u, int it) {
         const float *const ss = sS + (it & (SR - 1)) * (PM + PN);
         const int ua = u * PM * kBlk, ub = u * PN * kBlk;
-        Frag fa[2], fb[2];
         Frag16 ga, gb[2];
-        fa[0] = frag(pa, ua);
-#pragma unroll
-        for (int j = 0; j < 2; j++) fb[j] = frag(pb, ub + j * 32 * kBlk);
+        if constexpr (!EARLY) {
+            arrive(u, it);
+            fa[0] = frag(pa, ua);
+            fb[0] = frag(pb, ub);
+        }
+        fb[1] = frag(pb, ub + 32 * kBlk);
         float sa[TI];
 #pragma unroll
         for (int i = 0; i < TI; i++) sa[i] = ss[wm * TI * 32 + i * 32 + l32];
         const float sbt = BT ? ss[scol] : 1.0f;
-        issue((u + NS - 1) & (NS - 1), it + NS - 1);
         if constexpr (!BF16OUT) {
             ga = to_f16<FA>(fa[0]);
 #pragma unroll
@@ -479,7 +491,13 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
         static_for<0, 2 * TI>([&](auto tt) {
             constexpr int t = decltype(tt)::value, i = t / 2, j = t % 2;
             constexpr int pi = t ? (t - 1) / 2 : TI - 1, pj = t ? (t - 1) % 2 : 1;  // the tile before
+            if constexpr (EARLY && t == 2 * TI - 2) arrive(u ^ 1, it + 1);
             if constexpr (j == 0 && i + 1 < TI) fa[(i + 1) & 1] = frag(pa, ua + (i + 1) * 32 * kBlk);
+            if constexpr (EARLY && t == 2 * TI - 1) {
+                static_assert(TI % 2 == 0, "the last row's fragments are in fa[1]");
+                fa[0] = frag(pa, (u ^ 1) * PM * kBlk);
+                fb[0] = frag(pb, (u ^ 1) * PN * kBlk);
+            }
             float4 sb[4];
             read_sb(sb);
             v16f p;
@@ -495,17 +513,17 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
         });
     };
 
-#pragma unroll
-    for (int u = 0; u < NS - 1; u++) issue(u, u);
-    const int nit = (nk + KG - 1) / KG;  // stages of a group; one past the end of K is all zeros
-    if constexpr (NS == 2) {
-        // two at a time, so that their places are constants
-        for (int it = 0; it < nit; it += 2) {
-            stage(0, it);
-            stage(1, it + 1);
-        }
-    } else {
-        for (int it = 0; it < nit; it++) stage(it & (NS - 1), it);
+    // two stages at a time, so that their places are constants; past the end of K they are all zeros
+    const int nit = (nk + KG - 1) / KG;
+    issue(0, 0);
+    if constexpr (EARLY) {
+        arrive(0, 0);
+        fa[0] = frag(pa, 0);
+        fb[0] = frag(pb, 0);
+    }
+    for (int it = 0; it < nit; it += 2) {
+        stage(0, it);
+        stage(1, it + 1);
     }
     {
         float4 sb[4];
