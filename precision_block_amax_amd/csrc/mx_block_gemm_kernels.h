@@ -797,6 +797,8 @@ hipError_t launch_block_gemm_pipe(BlockGemmArgs g, hipStream_t s) {
 template <int FA, int FB, bool BT, bool BF16OUT>
 hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
     // All but the general kernel load straight to LDS: rows of whole aligned 16 bytes, offsets in 31 bits.
+    if (g.M == 1) g.lda = (g.K + 15) / 16 * 16;  // a single row has no stride
+    if (g.N == 1) g.ldb = (g.K + 15) / 16 * 16;
     const int64_t nk = (g.K + kBlk - 1) / kBlk, lim = (int64_t)1 << 31;
     const bool aligned = g.lda % 16 == 0 && g.ldb % 16 == 0 && (uintptr_t)g.a % 16 == 0 && (uintptr_t)g.b % 16 == 0 &&
                          256 * g.lda < lim && 256 * g.ldb < lim && (nk * g.ldsa + 256) * 4 < lim &&
@@ -808,17 +810,18 @@ hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
         return hipGetLastError();
     }
     const auto tiles = [&](int64_t m, int64_t n) { return (g.M + m - 1) / m * ((g.N + n - 1) / n); };
-    if (g.M <= 8) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 1, 1, 2>(g, s);
-    if (g.M <= 16) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 2, 1, 2>(g, s);
-    if (g.M <= 32) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 4, 1, 3>(g, s);
-    if (g.M <= 48) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 6, 1, 2>(g, s);
+    const int64_t wide = (int64_t)1 << 26;  // columns from which 16 of them per workgroup would be 2^31 threads
+    if (g.M <= 8 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 1, 1, 2>(g, s);
+    if (g.M <= 16 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 2, 1, 2>(g, s);
+    if (g.M <= 32 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 4, 1, 3>(g, s);
+    if (g.M <= 48 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 6, 1, 2>(g, s);
     // 64 rows: 32 columns per workgroup read A half as often, 16 make twice the workgroups: 42 against 55 at
     // N = 28672, K = 4096 (896 workgroups), 20 against 18 at K = 14336 (128)
     if (g.M <= 64 && tiles(64, 32) < 256) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 8, 1, 1>(g, s);
     // Up to two rounds of 64 x 32 tiles on the 256 CUs (the 128 x 128 tiles are then 64 at most): K = 14336, one
     // round (M = 128) 21 against 64, two (256) 38 against 63; K = 4096, two 15 against 21, four (512) 27
     // against 21.  float32: one 24 against 36, two 32 against 36, four 48 against 38.
-    if (g.M <= 64 || tiles(64, 32) <= 512) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 8, 2, 1>(g, s);
+    if ((g.M <= 64 && g.N < wide) || tiles(64, 32) <= 512) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 8, 2, 1>(g, s);
     if (g.K % 16 != 0) return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg128x128, true>(g, s);
     const int64_t r128 = (tiles(128, 128) + 255) / 256;
     if constexpr (BF16OUT && BT) {

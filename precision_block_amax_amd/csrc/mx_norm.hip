@@ -492,15 +492,26 @@ hipError_t launch_bwd(const NormBwdArgs &a, int64_t chunks, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_norm(const NormArgs &a, int to, int fmt, hipStream_t s) {
-    if (to == TO_BF16) return launch_norm_to<TO_BF16, E4M3>(a, s);
-    if (to == TO_BLOCK)
-        return fmt == E4M3 ? launch_norm_to<TO_BLOCK, E4M3>(a, s) : launch_norm_to<TO_BLOCK, E5M2>(a, s);
-    switch (fmt) {
-    case E4M3: return launch_norm_to<TO_MX, E4M3>(a, s);
-    case E5M2: return launch_norm_to<TO_MX, E5M2>(a, s);
-    default: return launch_norm_to<TO_MX, E2M1>(a, s);
+hipError_t launch_norm(const NormArgs &all, int to, int fmt, hipStream_t s) {
+    constexpr int64_t most = (int64_t)1 << 25;  // rows per launch: below 2^32 threads at 1024 for 16 rows
+    for (int64_t r = 0; r < all.rows; r += most) {
+        NormArgs a = all;
+        a.rows = all.rows - r < most ? all.rows - r : most;
+        a.x += r * a.ldx;
+        a.out = (uint8_t *)a.out + r * a.ld_out * (to == TO_BF16 ? 2 : 1);
+        if (to == TO_BLOCK) a.scales = (float *)a.scales + r;
+        if (to == TO_MX) a.scales = (uint8_t *)a.scales + r * a.ld_scales;
+        if (a.mean) a.mean += r;
+        if (a.rstd) a.rstd += r;
+        hipError_t e;
+        if (to == TO_BF16) e = launch_norm_to<TO_BF16, E4M3>(a, s);
+        else if (to == TO_BLOCK) e = fmt == E4M3 ? launch_norm_to<TO_BLOCK, E4M3>(a, s) : launch_norm_to<TO_BLOCK, E5M2>(a, s);
+        else if (fmt == E4M3) e = launch_norm_to<TO_MX, E4M3>(a, s);
+        else if (fmt == E5M2) e = launch_norm_to<TO_MX, E5M2>(a, s);
+        else e = launch_norm_to<TO_MX, E2M1>(a, s);
+        if (e != hipSuccess) return e;
     }
+    return hipSuccess;
 }
 
 int64_t norm_backward_workspace(int64_t rows, int64_t cols) { return dparam_chunks(rows, cols) * 2 * cols; }

@@ -166,7 +166,7 @@ def check_product(c, a, fa, b, fb, tile, bf16):
         assert err.norm() <= (2.0 ** -8 / 3 ** 0.5 + 2.0 ** -11) * C.norm(), (err.norm() / C.norm()).item()
 
 
-GEMM_SIZES = [(1, 1, 1), (1, 128, 128), (1, 6144, 512), (2, 300, 64), (5, 77, 333), (16, 256, 1024), (17, 130, 4097), (31, 515, 640),
+GEMM_SIZES = [(1, 1, 1), (1, 128, 128), (1, 300, 4001), (70, 1, 1001), (300, 1, 250), (1, 6144, 512), (2, 300, 64), (5, 77, 333), (16, 256, 1024), (17, 130, 4097), (31, 515, 640),
               (33, 96, 128), (48, 512, 2048), (64, 640, 1152), (65, 128, 260), (100, 1000, 144), (128, 128, 128), (129, 257, 384),
               (256, 512, 512), (300, 301, 302), (333, 640, 1000), (512, 768, 1280), (513, 1025, 272), (1024, 512, 896)]
 

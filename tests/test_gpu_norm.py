@@ -203,8 +203,8 @@ def test_layer_norm_strides_empty_and_many_rows(mx):
     assert mx.layer_norm_quantize(e)[1].shape == (5, 0)
     dx, dw, db = mx.layer_norm_backward(e, e, None, mean, rstd)
     assert dx.shape == (0, 640) and (dw == 0).all() and (db == 0).all()
-    # more rows than a launch has workgroups, two kinds of kernels
-    for rows, cols in ((4500001, 8), (1048600, 1032)):
+    # more rows than a launch takes, and than it has workgroups, two kinds of kernels
+    for rows, cols in ((2 ** 25 + 4000, 8), (4500001, 8), (1048600, 1032)):
         g = torch.Generator(device="cuda").manual_seed(1)
         x = torch.randn(rows, cols, device="cuda", generator=g).bfloat16()
         for rms in (False, True):
@@ -214,6 +214,10 @@ def test_layer_norm_strides_empty_and_many_rows(mx):
             tol = 2.0 ** -8 * want.abs() + y_error(x[at], None, rms, want, wm, wr)
             assert ((y[at].double() - want).abs() <= tol).all()
             assert bool(y.isfinite().all())
+            if cols == 8:
+                c, sc, _, _ = mx.layer_norm_quantize(x, fmt="e5m2", rms=rms)
+                d = (ref.values(c[at], sc[:, at], "e5m2") - want).abs()
+                assert (d <= 2.0 ** -3 * want.abs() * (1 + 2.0 ** -9) + 2.0 ** -17 * sc[:, at].double().t()).all()
             dx = mx.layer_norm_backward(y, x, None, mean, rstd, rms=rms, weight_grad=False, bias_grad=False)[0]
             want = ref.norm_backward(y[at], x[at], None, None if rms else mean[at], rstd[at], rms)[0]
             err = (dx[at].double() - want).abs()
