@@ -26,6 +26,11 @@
 namespace mx {
 namespace {
 
+// bf16 input larger than half of the 256 MB last-level cache is read past it: less of it would be found there
+// than it pushes out.  32768 x 4096: to bf16 117 us through the cache, 90 past it, backward 168 and 145; but
+// 8192 x 4096 (67 MB, partly still cached) 27 and 32.
+bool past_cache(int64_t rows, int64_t cols) { return rows * cols > (int64_t)1 << 26; }
+
 // sum over the wave, in every lane: within rows of 16 lanes by DPP (neighbours, pairs, mirrored halves,
 // mirrored row), then row against row and half against half (one swap gives each side both values)
 __device__ __forceinline__ float wave_sum(float v) {
@@ -86,7 +91,7 @@ __device__ __forceinline__ void store_vec(uint16_t *p, const float (&y)[8], int 
 // written as runs of the workgroup's rows (8192 x 4096: row by row 34 us, where the bf16 output with a
 // third more bytes took 27).
 constexpr int kNormRows = 16;  // most rows per workgroup
-template <int T, int U, int TO, int F, bool WHOLE>
+template <int T, int U, int TO, int F, bool WHOLE, bool PAST>
 __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a, int per) {
     constexpr int NT = T < 256 ? 256 : T, RPW = NT / T, W = T / 64;
     constexpr bool KEEP = U <= 2;  // the parameters fit in registers beside a row
@@ -109,7 +114,7 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a, int pe
         const bool live = row < count;
         const uint16_t *p = a.x + (r0 + (live ? row : 0)) * a.ldx;
 #pragma unroll
-        for (int u = 0; u < U; u++) load_vec<WHOLE>(w[u], p, 8 * (u * T + t), a.cols, live);
+        for (int u = 0; u < U; u++) load_vec<WHOLE, PAST>(w[u], p, 8 * (u * T + t), a.cols, live);
     };
     // sum over the row's threads; `s` is written again only after another barrier
     const auto row_sum = [&](float v, float (&s)[RPW][W]) {
@@ -233,8 +238,9 @@ hipError_t launch_norm_tu(const NormArgs &a, hipStream_t s) {
     int64_t per = a.rows / fill / RPW * RPW;
     per = per < RPW ? RPW : per > kNormRows ? kNormRows : per;
     const dim3 grid((unsigned)((a.rows + per - 1) / per)), block(NT);
-    if (a.cols % 8 == 0) hipLaunchKernelGGL((k_norm<T, U, TO, F, true>), grid, block, 0, s, a, (int)per);
-    else hipLaunchKernelGGL((k_norm<T, U, TO, F, false>), grid, block, 0, s, a, (int)per);
+    if (a.cols % 8 != 0) hipLaunchKernelGGL((k_norm<T, U, TO, F, false, false>), grid, block, 0, s, a, (int)per);
+    else if (past_cache(a.rows, a.cols)) hipLaunchKernelGGL((k_norm<T, U, TO, F, true, true>), grid, block, 0, s, a, (int)per);
+    else hipLaunchKernelGGL((k_norm<T, U, TO, F, true, false>), grid, block, 0, s, a, (int)per);
     return hipGetLastError();
 }
 
@@ -253,7 +259,7 @@ hipError_t launch_norm_to(const NormArgs &a, hipStream_t s) {
 // T threads and 8 T U >= cols elements per row, R rows at a time; workgroup b takes rows
 // [b, b + 1) * per.  PARAMS: the sums of dy * xh and dy over those rows go to ws[b][0 and 1][cols].
 // Without, R is 1 and rows are read where the loop meets them.
-template <int T, int U, int R, bool PARAMS, bool WHOLE>
+template <int T, int U, int R, bool PARAMS, bool WHOLE, bool PAST>
 __global__ __launch_bounds__(T *R) void k_norm_bwd(NormBwdArgs a, int per) {
     constexpr int W = T / 64;
     __shared__ float s0[R][W], s1[R][W];
@@ -282,8 +288,8 @@ __global__ __launch_bounds__(T *R) void k_norm_bwd(NormBwdArgs a, int per) {
         const int64_t r = r0 + (live ? row : 0);
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            load_vec<WHOLE>(wx[u], a.x + r * a.ldx, 8 * (u * T + t), a.cols, live);
-            load_vec<WHOLE>(wd[u], a.dy + r * a.lddy, 8 * (u * T + t), a.cols, live);
+            load_vec<WHOLE, PAST>(wx[u], a.x + r * a.ldx, 8 * (u * T + t), a.cols, live);
+            load_vec<WHOLE, PAST>(wd[u], a.dy + r * a.lddy, 8 * (u * T + t), a.cols, live);
         }
         rstd = a.rstd[r];
         mean = a.rms ? 0.f : a.mean[r];
@@ -476,8 +482,9 @@ template <int T, int U>
 hipError_t launch_dx(const NormBwdArgs &a, hipStream_t s) {
     const int per = (int)((a.rows + (1 << 20) - 1) >> 20);
     const dim3 grid((unsigned)((a.rows + per - 1) / per));
-    if (a.cols % 8 == 0) hipLaunchKernelGGL((k_norm_bwd<T, U, 1, false, true>), grid, dim3(T), 0, s, a, per);
-    else hipLaunchKernelGGL((k_norm_bwd<T, U, 1, false, false>), grid, dim3(T), 0, s, a, per);
+    if (a.cols % 8 != 0) hipLaunchKernelGGL((k_norm_bwd<T, U, 1, false, false, false>), grid, dim3(T), 0, s, a, per);
+    else if (past_cache(a.rows, a.cols)) hipLaunchKernelGGL((k_norm_bwd<T, U, 1, false, true, true>), grid, dim3(T), 0, s, a, per);
+    else hipLaunchKernelGGL((k_norm_bwd<T, U, 1, false, true, false>), grid, dim3(T), 0, s, a, per);
     return hipGetLastError();
 }
 
@@ -485,8 +492,10 @@ template <int T, int U, int R>
 hipError_t launch_bwd(const NormBwdArgs &a, int64_t chunks, hipStream_t s) {
     if (!a.dw && !a.db) return launch_dx<T, U>(a, s);
     const int per = (int)((a.rows + chunks - 1) / chunks);
-    if (a.cols % 8 == 0) hipLaunchKernelGGL((k_norm_bwd<T, U, R, true, true>), dim3((unsigned)chunks), dim3(T * R), 0, s, a, per);
-    else hipLaunchKernelGGL((k_norm_bwd<T, U, R, true, false>), dim3((unsigned)chunks), dim3(T * R), 0, s, a, per);
+    const dim3 grid((unsigned)chunks), block(T * R);
+    if (a.cols % 8 != 0) hipLaunchKernelGGL((k_norm_bwd<T, U, R, true, false, false>), grid, block, 0, s, a, per);
+    else if (past_cache(a.rows, a.cols)) hipLaunchKernelGGL((k_norm_bwd<T, U, R, true, true, true>), grid, block, 0, s, a, per);
+    else hipLaunchKernelGGL((k_norm_bwd<T, U, R, true, true, false>), grid, block, 0, s, a, per);
     return hipGetLastError();
 }
 

@@ -127,6 +127,22 @@ def test_quantize_empty(mx):
         assert len(mx.block_quantize_dual(x, "e4m3", "e5m2")) == 4
 
 
+def test_quantize_large_equals_its_parts(mx):
+    """input above the size from which it is read past the cache: every form equals that of its parts"""
+    import torch
+    rows, cols = 8320, 8200
+    x = data(rows, cols, 11, 3)
+    parts = [x[:4096], x[4096:]]
+    for fmt in ("e4m3", "e5m2"):
+        for mode in MODES:
+            c, s = mx.block_quantize(x, fmt, mode)
+            got = [mx.block_quantize(p, fmt, mode) for p in parts]
+            t = mode.endswith("transpose")
+            assert torch.equal(c, torch.cat([g[0] for g in got], 1 if t else 0)), (fmt, mode)
+            assert torch.equal(s, torch.cat([g[1] for g in got], 0 if t else 1)), (fmt, mode)
+    same_operand((c[:256, :4096], s[:32, :2]), ref.quantize(x[:4096, :256], "e5m2", "tile_transpose"))
+
+
 def test_quantize_beyond_31_bits(mx):
     """more than 2^31 elements: offsets of x and of both forms' codes need 64 bits"""
     import torch

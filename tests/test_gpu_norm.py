@@ -259,6 +259,35 @@ def test_layer_norm_backward(mx, rows, cols, rms):
     assert torch.equal(one[0], dx) and one[1] is None and torch.equal(one[2], db)
 
 
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("cols", [640, 1000, 2048, 4096, 8192, 16384])
+def test_norm_large_equals_its_parts(mx, cols, rms):
+    """input above the size from which it is read past the cache: rows equal those of smaller calls, the gradients of
+    the parameters are within the rounding of their sums"""
+    import torch
+    rows = 2 ** 26 // cols + 600
+    x, w, b, dy = make(rows, cols, 2)
+    cut = rows // 2
+    for call in (lambda t: mx.layer_norm(t, w, b, rms=rms), lambda t: mx.layer_norm_quantize(t, w, b, rms=rms),
+                 lambda t: mx.layer_norm_quantize(t[:, :cols // 32 * 32], fmt="e2m1", scaling="mx", rms=rms)):
+        all_, p, q = call(x), call(x[:cut]), call(x[cut:])
+        for a, u, v in zip(all_, p, q):
+            if a is not None:
+                d = 1 if a.dim() == 2 and a.shape[0] != rows else 0
+                assert torch.equal(a, torch.cat([u, v], d))
+    _, mean, rstd = mx.layer_norm(x, w, b, rms=rms)
+    dx, dw, db = mx.layer_norm_backward(dy, x, w, mean, rstd, rms=rms)
+    m = lambda a, c: None if rms else mean[a:c]
+    dx1 = mx.layer_norm_backward(dy[:cut], x[:cut], w, m(0, cut), rstd[:cut], rms=rms)[0]
+    dx2 = mx.layer_norm_backward(dy[cut:], x[cut:], w, m(cut, rows), rstd[cut:], rms=rms, weight_grad=False, bias_grad=False)[0]
+    assert torch.equal(dx, torch.cat([dx1, dx2]))
+    wx, ww, wb = ref.norm_backward(dy, x, w, mean, rstd, rms)
+    d = dy.double().abs()
+    xh = (x.double().abs() + (0 if rms else mean.double().abs()[:, None])) * rstd.double()[:, None]
+    n = (rows / 256 + 16 + 256 + 8) * 2.0 ** -24   # rows of a chunk, then at most 256 chunks, one after another
+    assert ((dw.double() - ww).abs() <= n * (d * xh).sum(0)).all() and ((db.double() - wb).abs() <= n * d.sum(0)).all()
+
+
 def test_norm_repeats_bits_on_streams_and_in_graphs(mx):
     """the same bits from other streams at once (each call has its own workspace), and replayed from two graphs
     between eager calls"""
