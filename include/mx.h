@@ -43,7 +43,9 @@
  *     element codes 0.  An all-zero block gets scale 0x00.  The sign of zero
  *     is kept (-0 -> 0x80 for FP8, 0x8 for E2M1).
  *   - A size of 0 is a valid empty call: nothing is read or written (except
- *     mx_gemm with K == 0, which writes C = 0), and pointers may be NULL.
+ *     mx_gemm and mx_block_gemm with K == 0, which write C = 0, and
+ *     mx_layer_norm_backward with rows == 0, which writes zero gradients of the
+ *     parameters), and pointers may be NULL.
  *
  * Errors (no call throws, no call aborts):
  *   MX_ERR_INVALID_ARG  bad argument, detected on the host before any HIP
@@ -413,8 +415,8 @@ mx_status_t mx_block_quantize_dual(const void *x_bf16, int64_t rows, int64_t col
  * `out`, ldc >= N.  Every block's sum is multiplied by its scales and added to
  * an fp32 accumulator.
  *   MX_OUT_F32   every product is exact and sums are fp32: |C - sum| <=
- *                1e-5 * sum |terms|.  The codes travel as bf16 (exact) through
- *                the bf16 matrix instruction.
+ *                1e-5 * sum |terms|.  The codes travel as fp16 (exact) through
+ *                the fp16 matrix instruction.
  *   MX_OUT_BF16  the FP8 matrix instruction, at twice that rate.  It adds the
  *                32 products of a step in a window that ends 2^-13 below the
  *                largest, so a block's sum may be off by 2^-8 of its sum of
@@ -422,7 +424,11 @@ mx_status_t mx_block_quantize_dual(const void *x_bf16, int64_t rows, int64_t col
  *                below the result's own rounding to bf16 unless the sum cancels
  *                far.  Call with MX_OUT_F32 where that matters.
  * Products of two scales outside fp32's range are Inf or 0.  A NaN scale makes
- * every element of C that it contributes to NaN.
+ * every element of C that it contributes to NaN; NaN and Inf codes behave as
+ * these values.  Fast are operands whose rows are aligned to 16 bytes (any K;
+ * as the quantizers' callers lay them out); others take a general kernel,
+ * about half as fast.  A row's last 16 aligned bytes are read whole, its bytes
+ * past K not used.
  */
 mx_status_t mx_block_gemm(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa, mx_format_t fa,
                           const void *b_codes, int64_t ldb, const float *b_scales, int64_t ldsb, mx_format_t fb,
@@ -440,7 +446,10 @@ mx_status_t mx_block_gemm(const void *a_codes, int64_t lda, const float *a_scale
  * mean before the squares are summed.  weight and bias: `cols` values of
  * `param` type each, either may be NULL (1 and 0).  mean and rstd: fp32, one
  * per row, for the backward pass; mean is not written for MX_NORM_RMS, either
- * may be NULL.  eps >= 0, finite.
+ * may be NULL.  eps >= 0, finite.  Rows are held whole by a workgroup: cols
+ * above 32768 are MX_ERR_UNSUPPORTED.  Sums and squares are fp32 numbers, so
+ * values whose squares leave its range (about 1e19 / sqrt(cols)) are not
+ * normalised; a constant row with eps = 0 gives NaN.
  */
 typedef enum {
     MX_NORM_LAYER = 0, /* mean and variance                        */

@@ -83,7 +83,7 @@ mx_status_t check_norm(const void *x, int64_t rows, int64_t cols, int64_t ldx, i
     if (rows < 0 || cols < 0 || ldx < cols || !type_ok(param) || (kind != MX_NORM_LAYER && kind != MX_NORM_RMS))
         return MX_ERR_INVALID_ARG;
     if (rows > 0 && cols > 0 && !x) return MX_ERR_INVALID_ARG;
-    if (cols > kNormMaxCols || rows > kMaxDim) return MX_ERR_UNSUPPORTED;
+    if (rows > 0 && (cols > kNormMaxCols || rows > kMaxDim)) return MX_ERR_UNSUPPORTED;
     return MX_OK;
 }
 
@@ -205,6 +205,7 @@ mx_status_t mx_layer_norm_backward(const void *dy_bf16, int64_t lddy, const void
     if (st != MX_OK) return st;
     if (lddy < cols || lddx < cols) return MX_ERR_INVALID_ARG;
     if (cols == 0 || (rows == 0 && !dweight && !dbias)) return MX_OK;
+    if (cols > kMaxDim) return MX_ERR_UNSUPPORTED;  // (no rows)
     if (rows > 0 && (!dy_bf16 || !rstd || !dx_bf16 || (k == MX_NORM_LAYER && !mean))) return MX_ERR_INVALID_ARG;
     const int64_t need = dweight || dbias ? mx_layer_norm_backward_workspace(rows, cols) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 16 != 0)) return MX_ERR_INVALID_ARG;

@@ -285,6 +285,26 @@ def test_gemm_nan_scales(mx, M, N, bf16):
             assert c[rest].isfinite().all()
 
 
+@pytest.mark.parametrize("M,N", [(1, 300), (40, 300), (300, 300), (1200, 1200), (4200, 4100)])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_gemm_special_codes(mx, M, N, bf16):
+    """NaN codes, and E5M2's infinities, make the elements that they enter NaN and Inf, and no others"""
+    import torch
+    dt = torch.bfloat16 if bf16 else torch.float32
+    K = 400
+    a, b = operand(mx, M, K, "e5m2", False, 1), operand(mx, N, K, "e4m3", True, 2)
+    b[0][:, 7] = 0x38                                    # 1
+    a[0][M - 1, 399], a[0][0, 7] = 0x7F, 0x7C           # NaN, Inf
+    b[0][5, 130] = 0xFF                                  # NaN
+    c = mx.block_gemm(*a, "e5m2", *b, "e4m3", out_dtype=dt)
+    want = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    want[M - 1], want[:, 5] = True, True
+    assert torch.equal(c.isnan(), want)
+    inf = torch.zeros_like(want)
+    inf[0] = True
+    assert torch.equal(c == float("inf"), inf & ~want)
+
+
 @pytest.mark.parametrize("M,N", [(1, 64), (40, 64), (300, 256), (1200, 1200), (4200, 4100)])
 def test_gemm_small_terms_kept_in_fp32(mx, M, N):
     """float32 output: 1 + 2^-18 in one block, the small term 2^-9 * 2^-9, is exact.  Beside a large pair that cancels,
