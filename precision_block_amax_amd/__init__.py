@@ -361,7 +361,12 @@ def gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_codes: torch.Tenso
 
 BLOCK = 128
 _BLOCK_MODES = {"row": 0, "transpose": 1, "tile": 2, "tile_transpose": 3}
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
 _NO_SCOPE = contextlib.nullcontext()
+# the current device and stream without the checks and the Stream object of torch.cuda's functions (0.1 us each
+# instead of 0.3 and 2; these calls are short), where torch has them
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _scope(device: torch.device, stream):
@@ -369,14 +374,12 @@ def _scope(device: torch.device, stream):
     stream (so that the memory of the outputs and the workspace belongs to the stream that
     writes it)."""
     if stream is None:
-        return _NO_SCOPE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        return _NO_SCOPE if _get_device() == device.index else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+    elif stream.device != device:
+        raise ValueError("the stream belongs to %s, the operands to %s" % (stream.device, device))
     return torch.cuda.stream(stream)
-
-
-# the current stream's handle without building a Stream object (0.1 us instead of 2), where torch has it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _current(device: torch.device) -> int:
@@ -396,30 +399,38 @@ def _cdiv(a: int, b: int) -> int:
     return -(-a // b)
 
 
-def _ld(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _input(x: torch.Tensor) -> Tuple[int, int, int]:
+    """rows, columns and row stride of a bf16 matrix on a GPU"""
+    if x.dtype is not _BF16 or x.dim() != 2 or not x.is_cuda:
+        raise ValueError("expected a 2-D bf16 tensor on a GPU")
+    (rows, cols), (ld, step) = x.shape, x.stride()
+    if step != 1 and rows and cols:
+        raise ValueError("the last dimension must be contiguous")
+    return rows, cols, ld if rows > 1 else cols
 
 
-def _rows_of(t: torch.Tensor, dtype: torch.dtype, shape, device, what: str) -> int:
+def _rows_of(t: torch.Tensor, dtype: torch.dtype, rows: int, width: int, device, what: str) -> int:
     """the row stride (elements) of a [rows x width] tensor with contiguous rows"""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
-        raise ValueError("%s must be %s of shape %s on %s" % (what, dtype, tuple(shape), device))
-    if t.shape[1] > 1 and t.shape[0] > 0 and t.stride(1) != 1:
+    if t.dtype is not dtype or t.shape != (rows, width) or t.device != device:
+        raise ValueError("%s must be %s of shape (%d, %d) on %s" % (what, dtype, rows, width, device))
+    ld, step = t.stride()
+    if step != 1 and width > 1 and rows:
         raise ValueError("the rows of %s must be contiguous" % what)
-    return _ld(t)
+    return ld if rows > 1 else width
 
 
 def _block_outputs(device, n: int, k: int, tile: bool, out):
-    """codes [n x k] (rows padded to a multiple of 16 bytes) and scales [blocks of k x n or tiles of n]"""
-    ns = _cdiv(n, BLOCK) if tile else n
+    """codes [n x k] (rows padded to a multiple of 16 bytes), their row stride, scales [blocks of k x n or
+    tiles of n] and their row stride"""
+    ns, kb = _cdiv(n, BLOCK) if tile else n, _cdiv(k, BLOCK)
     if out is None:
         pitch = _cdiv(k, 16) * 16
-        codes = torch.empty((n, pitch), dtype=torch.uint8, device=device)
-        return (codes if pitch == k else codes[:, :k]), torch.empty((_cdiv(k, BLOCK), ns), dtype=torch.float32, device=device)
+        codes = torch.empty((n, pitch), dtype=_U8, device=device)
+        scales = torch.empty((kb, ns), dtype=_F32, device=device)
+        return codes if pitch == k else codes[:, :k], pitch, scales, ns
     codes, scales = out
-    _rows_of(codes, torch.uint8, (n, k), device, "codes")
-    _rows_of(scales, torch.float32, (_cdiv(k, BLOCK), ns), device, "scales")
-    return codes, scales
+    return (codes, _rows_of(codes, _U8, n, k, device, "codes"), scales,
+            _rows_of(scales, _F32, kb, ns, device, "scales"))
 
 
 def block_quantize(x: torch.Tensor, fmt, mode: str = "row", out=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -428,16 +439,15 @@ def block_quantize(x: torch.Tensor, fmt, mode: str = "row", out=None, stream=Non
     "transpose": blocks along dim 0, codes [C x R], scales [ceil(R/128) x C]; "tile" and
     "tile_transpose": 128 x 128 tiles, scales [ceil(C/128) x ceil(R/128)] or its transpose.
     `out` = (codes, scales) may have strided rows."""
-    _check_bf16_2d(x)
-    f = _fp8(fmt)
-    if mode not in _BLOCK_MODES:
+    rows, cols, ldx = _input(x)
+    f, m, dev = _fp8(fmt), _BLOCK_MODES.get(mode), x.device
+    if m is None:
         raise ValueError("mode must be one of %s" % sorted(_BLOCK_MODES))
-    rows, cols = x.shape
-    n, k = (cols, rows) if mode.endswith("transpose") else (rows, cols)
-    with _scope(x.device, stream):
-        codes, scales = _block_outputs(x.device, n, k, mode.startswith("tile"), out)
-        _check(lib().mx_block_quantize(_ptr(x), rows, cols, _ldx(x), f, _BLOCK_MODES[mode], _ptr(codes), _ld(codes),
-                                       _ptr(scales), _ld(scales), _current(x.device)))
+    n, k = (cols, rows) if m & 1 else (rows, cols)
+    with _scope(dev, stream):
+        codes, ldc, scales, lds = _block_outputs(dev, n, k, m >= 2, out)
+        _check(lib().mx_block_quantize(x.data_ptr(), rows, cols, ldx, f, m, codes.data_ptr(), ldc, scales.data_ptr(), lds,
+                                       _current(dev)))
     return codes, scales
 
 
@@ -446,15 +456,14 @@ def block_quantize_dual(x: torch.Tensor, fmt_row, fmt_t, tile: bool = False, out
     """mx_block_quantize_dual: (codes, scales, codes_t, scales_t) from one read of x, as
     block_quantize(x, fmt_row, "row") and (x, fmt_t, "transpose") give them, or with tile as
     "tile" and "tile_transpose" do.  `out` is a 4-tuple of output tensors."""
-    _check_bf16_2d(x)
-    fr, ft = _fp8(fmt_row), _fp8(fmt_t)
-    rows, cols = x.shape
-    with _scope(x.device, stream):
-        cr, sr = _block_outputs(x.device, rows, cols, tile, None if out is None else out[:2])
-        ct, st = _block_outputs(x.device, cols, rows, tile, None if out is None else out[2:])
-        _check(lib().mx_block_quantize_dual(_ptr(x), rows, cols, _ldx(x), 1 if tile else 0, fr, _ptr(cr), _ld(cr),
-                                            _ptr(sr), _ld(sr), ft, _ptr(ct), _ld(ct), _ptr(st), _ld(st),
-                                            _current(x.device)))
+    rows, cols, ldx = _input(x)
+    fr, ft, dev = _fp8(fmt_row), _fp8(fmt_t), x.device
+    with _scope(dev, stream):
+        cr, ldcr, sr, ldsr = _block_outputs(dev, rows, cols, tile, None if out is None else out[:2])
+        ct, ldct, st, ldst = _block_outputs(dev, cols, rows, tile, None if out is None else out[2:])
+        _check(lib().mx_block_quantize_dual(x.data_ptr(), rows, cols, ldx, 1 if tile else 0, fr, cr.data_ptr(), ldcr,
+                                            sr.data_ptr(), ldsr, ft, ct.data_ptr(), ldct, st.data_ptr(), ldst,
+                                            _current(dev)))
     return cr, sr, ct, st
 
 
@@ -469,47 +478,43 @@ def block_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_codes: torch
     if a_codes.dim() != 2 or b_codes.dim() != 2 or a_scales.dim() != 2 or b_scales.dim() != 2 or not a_codes.is_cuda:
         raise ValueError("expected 2-D operands on a GPU")
     dev = a_codes.device
-    (M, K), N = a_codes.shape, b_codes.shape[0]
-    if b_codes.shape[1] != K:
+    (M, K), (N, kb) = a_codes.shape, b_codes.shape
+    if kb != K:
         raise ValueError("A and B disagree on K")
-    if out_dtype not in (torch.float32, torch.bfloat16):
+    if out_dtype is not _BF16 and out_dtype is not _F32:
         raise ValueError("out_dtype must be float32 or bfloat16")
     kb, tiles = _cdiv(K, BLOCK), _cdiv(N, BLOCK)
-    tile = b_scales.shape[1] == tiles and tiles != N
-    lda = _rows_of(a_codes, torch.uint8, (M, K), dev, "A's codes")
-    ldb = _rows_of(b_codes, torch.uint8, (N, K), dev, "B's codes")
-    ldsa = _rows_of(a_scales, torch.float32, (kb, M), dev, "A's scales")
-    ldsb = _rows_of(b_scales, torch.float32, (kb, tiles if tile else N), dev, "B's scales")
-    if out is not None:
-        _rows_of(out, out_dtype, (M, N), dev, "out")
+    tile = tiles != N and b_scales.shape[1] == tiles
+    lda = _rows_of(a_codes, _U8, M, K, dev, "A's codes")
+    ldb = _rows_of(b_codes, _U8, N, K, dev, "B's codes")
+    ldsa = _rows_of(a_scales, _F32, kb, M, dev, "A's scales")
+    ldsb = _rows_of(b_scales, _F32, kb, tiles if tile else N, dev, "B's scales")
+    ldc = N if out is None else _rows_of(out, out_dtype, M, N, dev, "out")
     with _scope(dev, stream):
         if out is None:
             out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        _check(lib().mx_block_gemm(_ptr(a_codes), lda, _ptr(a_scales), ldsa, f_a, _ptr(b_codes), ldb, _ptr(b_scales),
-                                   ldsb, f_b, 1 if tile else 0, M, N, K, _ptr(out),
-                                   OUT_BF16 if out_dtype == torch.bfloat16 else OUT_F32, _ld(out), _current(dev)))
+        _check(lib().mx_block_gemm(a_codes.data_ptr(), lda, a_scales.data_ptr(), ldsa, f_a, b_codes.data_ptr(), ldb,
+                                   b_scales.data_ptr(), ldsb, f_b, 1 if tile else 0, M, N, K, out.data_ptr(),
+                                   OUT_BF16 if out_dtype is _BF16 else OUT_F32, ldc, _current(dev)))
     return out
 
 
-def _params(x: torch.Tensor, weight, bias) -> int:
-    """checks weight and bias against x; their type as the library's enum"""
-    for t, what in ((weight, "weight"), (bias, "bias")):
-        if t is None:
-            continue
-        if t.dtype not in (torch.float32, torch.bfloat16) or tuple(t.shape) != (x.shape[1],) or t.device != x.device:
-            raise ValueError("%s must be float32 or bfloat16 of shape (%d,) on %s" % (what, x.shape[1], x.device))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % what)
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+def _param(t: Optional[torch.Tensor], cols: int, device, what: str) -> int:
+    """the address of weight or bias (0: none) after its checks"""
+    if t is None:
+        return 0
+    if (t.dtype is not _BF16 and t.dtype is not _F32) or t.shape != (cols,) or t.device != device:
+        raise ValueError("%s must be float32 or bfloat16 of shape (%d,) on %s" % (what, cols, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return t.data_ptr()
+
+
+def _param_type(weight: Optional[torch.Tensor], bias: Optional[torch.Tensor]) -> int:
+    if weight is not None and bias is not None and weight.dtype is not bias.dtype:
         raise ValueError("weight and bias must have the same type")
     p = weight if weight is not None else bias
-    return OUT_F32 if p is not None and p.dtype == torch.float32 else OUT_BF16
-
-
-def _stats(x: torch.Tensor, rms: bool):
-    rows = x.shape[0]
-    mean = None if rms else torch.empty((rows,), dtype=torch.float32, device=x.device)
-    return mean, torch.empty((rows,), dtype=torch.float32, device=x.device)
+    return OUT_F32 if p is not None and p.dtype is _F32 else OUT_BF16
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -518,17 +523,17 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     """mx_layer_norm: (y, mean, rstd) of the rows of x (bf16); y is bf16, mean and rstd float32 for
     layer_norm_backward.  rms: RMS norm, the mean taken as 0 (mean is then None).  weight and
     bias: float32 or bfloat16, or None."""
-    _check_bf16_2d(x)
-    p = _params(x, weight, bias)
-    rows, cols = x.shape
-    if out is not None:
-        _rows_of(out, torch.bfloat16, (rows, cols), x.device, "out")
-    with _scope(x.device, stream):
+    rows, cols, ldx = _input(x)
+    dev = x.device
+    w, b, p = _param(weight, cols, dev, "weight"), _param(bias, cols, dev, "bias"), _param_type(weight, bias)
+    ldy = cols if out is None else _rows_of(out, _BF16, rows, cols, dev, "out")
+    with _scope(dev, stream):
         if out is None:
-            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
-        mean, rstd = _stats(x, rms)
-        _check(lib().mx_layer_norm(_ptr(x), rows, cols, _ldx(x), _ptr(weight), _ptr(bias), p, 1 if rms else 0, eps,
-                                   _ptr(out), _ld(out), _ptr(mean), _ptr(rstd), _current(x.device)))
+            out = torch.empty((rows, cols), dtype=_BF16, device=dev)
+        mean = None if rms else torch.empty((rows,), dtype=_F32, device=dev)
+        rstd = torch.empty((rows,), dtype=_F32, device=dev)
+        _check(lib().mx_layer_norm(x.data_ptr(), rows, cols, ldx, w, b, p, 1 if rms else 0, eps, out.data_ptr(), ldy,
+                                   _ptr(mean), rstd.data_ptr(), _current(dev)))
     return out, mean, rstd
 
 
@@ -538,26 +543,34 @@ def layer_norm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None, 
     """The norm written as a quantized operand: (codes, scales, mean, rstd).  scaling "block"
     (mx_layer_norm_block_quantize): codes and scales as block_quantize(y, fmt, "row") lays them out;
     "mx" (mx_layer_norm_quantize): as quantize(y, fmt).  y is not rounded to bf16 in between."""
-    _check_bf16_2d(x)
-    p = _params(x, weight, bias)
-    rows, cols = x.shape
+    rows, cols, ldx = _input(x)
+    dev = x.device
+    w, b, p = _param(weight, cols, dev, "weight"), _param(bias, cols, dev, "bias"), _param_type(weight, bias)
     if scaling not in ("block", "mx"):
         raise ValueError("scaling must be 'block' or 'mx'")
     f = _fp8(fmt) if scaling == "block" else _fmt(fmt)
-    with _scope(x.device, stream):
+    with _scope(dev, stream):
         if scaling == "block":
-            codes, scales = _block_outputs(x.device, rows, cols, False, out)
+            codes, ldc, scales, lds = _block_outputs(dev, rows, cols, False, out)
         else:
-            codes, scales = _outputs(x.device, rows, cols, f, out)
-        mean, rstd = _stats(x, rms)
-        head = (_ptr(x), rows, cols, _ldx(x), _ptr(weight), _ptr(bias), p, 1 if rms else 0, eps, f)
+            codes, scales = _outputs(dev, rows, cols, f, out)
+        mean = None if rms else torch.empty((rows,), dtype=_F32, device=dev)
+        rstd = torch.empty((rows,), dtype=_F32, device=dev)
         if scaling == "block":
-            _check(lib().mx_layer_norm_block_quantize(*head, _ptr(codes), _ld(codes), _ptr(scales), _ld(scales),
-                                                      _ptr(mean), _ptr(rstd), _current(x.device)))
+            _check(lib().mx_layer_norm_block_quantize(x.data_ptr(), rows, cols, ldx, w, b, p, 1 if rms else 0, eps, f,
+                                                      codes.data_ptr(), ldc, scales.data_ptr(), lds, _ptr(mean),
+                                                      rstd.data_ptr(), _current(dev)))
         else:
-            _check(lib().mx_layer_norm_quantize(*head, _ptr(codes), _ptr(scales), _ptr(mean), _ptr(rstd),
-                                                _current(x.device)))
+            _check(lib().mx_layer_norm_quantize(x.data_ptr(), rows, cols, ldx, w, b, p, 1 if rms else 0, eps, f,
+                                                codes.data_ptr(), scales.data_ptr(), _ptr(mean), rstd.data_ptr(),
+                                                _current(dev)))
     return codes, scales, mean, rstd
+
+
+def _stat(t: Optional[torch.Tensor], rows: int, device, what: str) -> int:
+    if t is None or t.dtype is not _F32 or t.shape != (rows,) or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be contiguous float32 of shape (%d,) on %s" % (what, rows, device))
+    return t.data_ptr()
 
 
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: Optional[torch.Tensor],
@@ -566,27 +579,21 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     """mx_layer_norm_backward: (dx, dweight, dbias) for the output gradient dy (bf16) of
     layer_norm or layer_norm_quantize, with the mean and rstd they returned; dx is bf16,
     dweight and dbias float32, None where not asked for."""
-    _check_bf16_2d(dy)
-    _check_bf16_2d(x)
-    if dy.shape != x.shape or dy.device != x.device:
+    _, _, lddy = _input(dy)
+    rows, cols, ldx = _input(x)
+    dev = x.device
+    if dy.shape != x.shape or dy.device != dev:
         raise ValueError("dy and x must agree in shape and device")
-    p = _params(x, weight, None)
-    rows, cols = x.shape
-    for t, what in ((None if rms else mean, "mean"), (rstd, "rstd")):
-        if what == "mean" and rms:
-            continue
-        if t is None or t.dtype != torch.float32 or tuple(t.shape) != (rows,) or t.device != x.device or not t.is_contiguous():
-            raise ValueError("%s must be contiguous float32 of shape (%d,) on %s" % (what, rows, x.device))
-    if out is not None:
-        _rows_of(out, torch.bfloat16, (rows, cols), x.device, "out")
-    with _scope(x.device, stream):
+    w, p = _param(weight, cols, dev, "weight"), _param_type(weight, None)
+    m, r = 0 if rms else _stat(mean, rows, dev, "mean"), _stat(rstd, rows, dev, "rstd")
+    lddx = cols if out is None else _rows_of(out, _BF16, rows, cols, dev, "out")
+    with _scope(dev, stream):
         if out is None:
-            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
-        dw = torch.empty((cols,), dtype=torch.float32, device=x.device) if weight_grad else None
-        db = torch.empty((cols,), dtype=torch.float32, device=x.device) if bias_grad else None
+            out = torch.empty((rows, cols), dtype=_BF16, device=dev)
+        dw = torch.empty((cols,), dtype=_F32, device=dev) if weight_grad else None
+        db = torch.empty((cols,), dtype=_F32, device=dev) if bias_grad else None
         need = lib().mx_layer_norm_backward_workspace(rows, cols) if weight_grad or bias_grad else 0
-        ws = torch.empty((need,), dtype=torch.uint8, device=x.device) if need else None
-        _check(lib().mx_layer_norm_backward(_ptr(dy), _ldx(dy), _ptr(x), _ldx(x), rows, cols, _ptr(weight), p,
-                                            1 if rms else 0, None if rms else _ptr(mean), _ptr(rstd), _ptr(out), _ld(out),
-                                            _ptr(dw), _ptr(db), _ptr(ws), need, _current(x.device)))
+        ws = torch.empty((need,), dtype=_U8, device=dev) if need else None
+        _check(lib().mx_layer_norm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, rows, cols, w, p, 1 if rms else 0, m, r,
+                                            out.data_ptr(), lddx, _ptr(dw), _ptr(db), _ptr(ws), need, _current(dev)))
     return out, dw, db
