@@ -323,6 +323,8 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     const int nk = (g.K + kBlk - 1) / kBlk, ktail = g.K - (nk - 1) * kBlk;
     const int mrows = min(PM, g.M - m0), nrows = min(PN, g.N - n0);
     const int lda = (int)g.lda, ldb = (int)g.ldb;
+    // rows past the operand lie past its records, whichever part of the offset is the scalar one (the range check
+    // counts both: measured), and read as zeros
     const pipe::v4i rA = pipe::rsrc(g.a + (int64_t)m0 * lda, (uint32_t)mrows * lda);
     const pipe::v4i rB = pipe::rsrc(g.b + (int64_t)n0 * ldb, (uint32_t)nrows * ldb);
 

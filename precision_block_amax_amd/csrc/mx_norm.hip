@@ -469,13 +469,16 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_norm_dparam_sum(NormBwdArgs 
     }
 }
 
-// rows of a workgroup at a time (R), and the chunks that the rows are cut into: one workgroup per CU
+// rows of a workgroup at a time (R), and the chunks that the rows are cut into: about one workgroup per CU, and
+// none without a row (300 rows: 2 for each of 150 workgroups, not of 256)
 int norm_rows_at_once(int64_t cols) {
-    return cols <= 1024 ? 8 : cols <= 2048 ? 8 : cols <= 4096 ? 4 : cols <= 8192 ? 2 : 1;
+    return cols <= 2048 ? 8 : cols <= 4096 ? 4 : cols <= 8192 ? 2 : 1;
 }
 int64_t dparam_chunks(int64_t rows, int64_t cols) {
+    if (rows == 0) return 0;
     const int64_t r = cols <= 16384 ? norm_rows_at_once(cols) : 16, n = (rows + r - 1) / r;
-    return n < 256 ? n : 256;
+    const int64_t most = n < 256 ? n : 256, per = (rows + most - 1) / most;
+    return (rows + per - 1) / per;
 }
 
 template <int T, int U>
@@ -527,7 +530,7 @@ int64_t norm_backward_workspace(int64_t rows, int64_t cols) { return dparam_chun
 
 hipError_t launch_norm_backward(const NormBwdArgs &a, hipStream_t s) {
     const bool params = a.dw || a.db;
-    const int64_t chunks = a.rows > 0 ? dparam_chunks(a.rows, a.cols) : 0;
+    const int64_t chunks = dparam_chunks(a.rows, a.cols);
     hipError_t e = hipSuccess;
     if (a.rows > 0) {
         if (a.cols <= 512) e = launch_bwd<64, 1, 8>(a, chunks, s);

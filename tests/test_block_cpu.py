@@ -146,6 +146,20 @@ def test_binding_refuses():
         mx._fp8("e2m1")
 
 
+@pytest.mark.parametrize("cols", [8, 1024, 2048, 4096, 8192, 16384, 16392, 32768])
+def test_norm_backward_workgroups_all_have_rows(cols):
+    """Workgroup b of the backward pass takes rows b * per .. with per = ceil(rows / workgroups), and reads its
+    first row before it looks at its count: the last one must have a row.  The workspace (two fp32 sums of
+    cols for each workgroup) tells how many there are."""
+    import precision_block_amax_amd as mx
+    size = mx.lib().mx_layer_norm_backward_workspace
+    assert size(0, cols) == 0
+    for rows in [*range(1, 1200), 2049, 4095, 5000, 65537, (1 << 20) + 1, (1 << 31) - 1]:
+        chunks, rest = divmod(size(rows, cols), 2 * 4 * cols)
+        assert rest == 0 and 1 <= chunks <= 256
+        assert (chunks - 1) * -(-rows // chunks) < rows
+
+
 def test_reference_norm_gradient_against_differences():
     """The formula the kernels are held to, against central differences of the definition in float64:
     with step h the difference is off by h^2 times third derivatives of order 1 and by 2^-53 / h."""
