@@ -47,26 +47,37 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
-// parameters c .. c + 7 as fp32; `other` where there are none, anything past cols
-template <bool WHOLE>
-__device__ __forceinline__ void load_param8(float (&w)[8], const void *p, bool bf16, int c, int cols, float other) {
-    if (!p) {
+// Parameters of vectors c0 + 8 T u (u < U) as fp32: `other` where there are none, 0 past cols.  Without WHOLE a
+// vector that the row's end cuts is taken element by element.  All loads go out before the first is used.
+template <bool WHOLE, int T, int U>
+__device__ __forceinline__ void load_params(float (&w)[U][8], const void *p, bool bf16, int c0, int cols, float other) {
+    if (p && bf16) {
+        uint32_t t[U][4];
 #pragma unroll
-        for (int i = 0; i < 8; i++) w[i] = other;
-    } else if (bf16) {
-        uint32_t t[4];
-        load_vec<WHOLE>(t, reinterpret_cast<const uint16_t *>(p), c, cols, true);
+        for (int u = 0; u < U; u++) load_vec<WHOLE>(t[u], reinterpret_cast<const uint16_t *>(p), c0 + 8 * T * u, cols, true);
 #pragma unroll
-        for (int i = 0; i < 8; i++) w[i] = (i & 1) ? bf16_hi(t[i >> 1]) : bf16_lo(t[i >> 1]);
-    } else {
+        for (int u = 0; u < U; u++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) w[u][i] = (i & 1) ? bf16_hi(t[u][i >> 1]) : bf16_lo(t[u][i >> 1]);
+        return;
+    }
+    if (p) {
         const float *q = reinterpret_cast<const float *>(p);
-        if (WHOLE || c + 8 <= cols) {
-            __builtin_memcpy(w, q + min(c, cols - 8), 32);
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; i++) w[i] = q[min(c + i, cols - 1)];
+        for (int u = 0; u < U; u++) {
+            const int c = c0 + 8 * T * u;
+            if (WHOLE || c + 8 <= cols) {
+                __builtin_memcpy(w[u], q + min(c, cols - 8), 32);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) w[u][i] = q[min(c + i, cols - 1)];
+            }
         }
     }
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[u][i] = c0 + 8 * T * u + (WHOLE ? 0 : i) < cols ? (p ? w[u][i] : other) : 0.f;
 }
 
 // y as bf16 to columns c .. c + 7 of the row at p, those before cols; WHOLE as in load_vec
@@ -101,14 +112,6 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a, int pe
     const float rn = 1.0f / (float)a.cols;
     const int64_t r0 = (int64_t)blockIdx.x * per;
     const int count = (int)min((int64_t)per, a.rows - r0);
-    float wt[KEEP ? U : 1][8], bs[KEEP ? U : 1][8];
-    if constexpr (KEEP) {
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            load_param8<WHOLE>(wt[u], a.weight, a.param_bf16, 8 * (u * T + t), a.cols, 1.f);
-            load_param8<WHOLE>(bs[u], a.bias, a.param_bf16, 8 * (u * T + t), a.cols, 0.f);
-        }
-    }
     uint32_t w[U][4];
     const auto load = [&](int row) {
         const bool live = row < count;
@@ -128,7 +131,13 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a, int pe
         }
         return v;
     };
-    load(grp);
+    load(grp);  // under way while the parameters come
+    // past the row's end x, weight and bias are 0, and with them every term of the sums and y
+    float wt[KEEP ? U : 1][8], bs[KEEP ? U : 1][8];
+    if constexpr (KEEP) {
+        load_params<WHOLE, T>(wt, a.weight, a.param_bf16, 8 * t, a.cols, 1.f);
+        load_params<WHOLE, T>(bs, a.bias, a.param_bf16, 8 * t, a.cols, 0.f);
+    }
     for (int rb = 0; rb < count; rb += RPW) {
         const bool live = rb + grp < count;
         const int64_t row = r0 + rb + grp;
@@ -148,8 +157,9 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a, int pe
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 const int n = a.cols - 8 * (u * T + t);
+                const float mu = n > 0 ? mean : 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; i++) y[u][i] = (WHOLE ? 0 : i) < n ? y[u][i] - mean : 0.f;
+                for (int i = 0; i < 8; i++) y[u][i] = WHOLE || i < n ? y[u][i] - mu : 0.f;
             }
         } else if (T > 64) {
             __syncthreads();  // the other barrier between two uses of s1
@@ -169,19 +179,19 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a, int pe
         for (int u = 0; u < U; u++) {
             const int c = 8 * (u * T + t), n = a.cols - c;
             if constexpr (!KEEP) {
-                load_param8<WHOLE>(wt[0], a.weight, a.param_bf16, c, a.cols, 1.f);
-                load_param8<WHOLE>(bs[0], a.bias, a.param_bf16, c, a.cols, 0.f);
+                load_params<WHOLE, T>(wt, a.weight, a.param_bf16, c, a.cols, 1.f);
+                load_params<WHOLE, T>(bs, a.bias, a.param_bf16, c, a.cols, 0.f);
             }
             const int k = KEEP ? u : 0;
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                y[u][i] = (WHOLE ? 0 : i) < n ? __builtin_fmaf(y[u][i] * rstd, wt[k][i], bs[k][i]) : 0.f;
+            for (int i = 0; i < 8; i++) y[u][i] = __builtin_fmaf(y[u][i] * rstd, wt[k][i], bs[k][i]);
             if constexpr (TO == TO_BF16) {
                 if (live) store_vec<WHOLE>(reinterpret_cast<uint16_t *>(a.out) + row * a.ld_out, y[u], c, a.cols);
             } else {
-                uint32_t m = 0;
+                float am = __builtin_fabsf(y[u][0]);  // NaN if an element is: one instruction for two elements
 #pragma unroll
-                for (int i = 0; i < 8; i++) m = umax(m, __float_as_uint(y[u][i]) & 0x7FFFFFFFu);
+                for (int i = 1; i < 8; i++) am = __builtin_elementwise_maximum(am, __builtin_fabsf(y[u][i]));
+                uint32_t m = __float_as_uint(am) & 0x7FFFFFFFu;
                 m = TO == TO_BLOCK ? row16_max(m) : quad_max(m);
                 uint8_t *q = reinterpret_cast<uint8_t *>(a.out) + row * a.ld_out;
                 if constexpr (TO == TO_BLOCK) {
@@ -269,18 +279,6 @@ __global__ __launch_bounds__(T *R) void k_norm_bwd(NormBwdArgs a, int per) {
     const float rn = 1.0f / (float)a.cols;
     const int64_t r0 = (int64_t)blockIdx.x * per;
     const int count = (int)min((int64_t)per, a.rows - r0);  // rows of this workgroup, numbered from 0 below
-    float wt[U][8];
-    float dw[PARAMS ? U : 1][8], db[PARAMS ? U : 1][8];
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-        const int c = 8 * (u * T + t), n = a.cols - c;
-        load_param8<WHOLE>(wt[u], a.weight, a.param_bf16, c, a.cols, 1.f);
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            wt[u][i] = i < n ? wt[u][i] : 0.f;
-            if constexpr (PARAMS) dw[u][i] = db[u][i] = 0.f;
-        }
-    }
     uint32_t wx[U][4], wd[U][4];
     float rstd = 0.f, mean = 0.f;
     const auto load = [&](int row) {
@@ -295,7 +293,16 @@ __global__ __launch_bounds__(T *R) void k_norm_bwd(NormBwdArgs a, int per) {
         mean = a.rms ? 0.f : a.mean[r];
     };
     const auto get = [](const uint32_t(&w)[4], int i) { return (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); };
-    load(grp);
+    load(grp);  // under way while the weight comes
+    float wt[U][8];
+    load_params<WHOLE, T>(wt, a.weight, a.param_bf16, 8 * t, a.cols, 1.f);
+    float dw[PARAMS ? U : 1][8], db[PARAMS ? U : 1][8];
+    if constexpr (PARAMS) {
+#pragma unroll
+        for (int u = 0; u < U; u++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) dw[u][i] = db[u][i] = 0.f;
+    }
     for (int rb = 0; rb < count; rb += R) {
         const int row = rb + grp;
         uint32_t cx[U][4], cd[U][4];
