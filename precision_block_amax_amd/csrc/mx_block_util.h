@@ -60,19 +60,25 @@ __device__ __forceinline__ void store8(uint8_t *p, uint32_t lo, uint32_t hi, int
     }
 }
 
+// v from another lane of its row of 16.  Every lane has a source in the patterns below; said so (the last
+// argument), the compiler folds the move into the operation that takes it.
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
 // max over the 16 lanes of a DPP row, in every one of them: neighbours, pairs, halves mirrored, whole row mirrored
 __device__ __forceinline__ uint32_t row16_max_pk(uint32_t v) {
-    v = pk_max_u16(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false));
-    v = pk_max_u16(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false));
-    v = pk_max_u16(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));
-    v = pk_max_u16(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));
-    return v;
+    v = pk_max_u16(v, dpp<kDppXor1>(v));
+    v = pk_max_u16(v, dpp<kDppXor2>(v));
+    v = pk_max_u16(v, dpp<kDppHalfMirror>(v));
+    return pk_max_u16(v, dpp<kDppMirror>(v));
 }
 __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
-    v = quad_max(v);
-    v = umax(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));
-    v = umax(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));
-    return v;
+    v = umax(v, dpp<kDppXor1>(v));
+    v = umax(v, dpp<kDppXor2>(v));
+    v = umax(v, dpp<kDppHalfMirror>(v));
+    return umax(v, dpp<kDppMirror>(v));
 }
 
 // scale and inverse of a block from its amax bits (fp32 magnitude).  A block
@@ -97,11 +103,19 @@ __device__ __forceinline__ void block_scale(uint32_t amax_bits, float &scale, fl
     inv = __builtin_fmaf(__builtin_fmaf(-a, q0, fmax), y1, q0) * 0x1p-12f;
 }
 
-// four codes of v * inv, clamped to the format's largest value
+// Four codes of v * inv.  No clamp: where ok, |v| <= amax and inv <= (1 + 2^-23) fmax / amax, so that |v * inv|
+// exceeds the largest code by 2^-22 of it at most and rounds to it.
 template <int F>
 __device__ __forceinline__ uint32_t block_cvt4(float a, float b, float c, float d, float inv, bool ok) {
-    const uint32_t q = cvt4_fp8<F>(a * inv, b * inv, c * inv, d * inv, 1.0f, block_fmax<F>());
-    return ok ? q : 0u;
+    v2s w = {0, 0};
+    if constexpr (F == E4M3) {
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a * inv, b * inv, 1.0f, false);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c * inv, d * inv, 1.0f, true);
+    } else {
+        w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w, a * inv, b * inv, 1.0f, false);
+        w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w, c * inv, d * inv, 1.0f, true);
+    }
+    return ok ? __builtin_bit_cast(uint32_t, w) : 0u;
 }
 
 }  // namespace
