@@ -460,7 +460,7 @@ __global__ __launch_bounds__(256) void k_norm_dparam(NormBwdArgs a, int64_t per)
 
 // the chunks' sums: 64 columns of one of the two gradients per workgroup, sixteen waves taking every
 // sixteenth chunk
-constexpr int kSumWaves = 16;
+constexpr int kSumWaves = 16, kSumLoads = 8;
 __global__ __launch_bounds__(64 * kSumWaves) void k_norm_dparam_sum(NormBwdArgs a, int chunks) {
     __shared__ float s[kSumWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -469,8 +469,14 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_norm_dparam_sum(NormBwdArgs 
     if (!out) return;  // uniform
     float v = 0.f;
     if (c < a.cols) {
-#pragma unroll 8
-        for (int k = wave; k < chunks; k += kSumWaves) v += a.ws[((int64_t)k * 2 + blockIdx.y) * a.cols + c];
+        const float *p = a.ws + (int64_t)blockIdx.y * a.cols + c;
+        for (int k = wave; k < chunks; k += kSumLoads * kSumWaves) {
+            float t[kSumLoads];  // all under way together, also where they are not of a whole number
+#pragma unroll
+            for (int i = 0; i < kSumLoads; i++) t[i] = p[(int64_t)min(k + i * kSumWaves, chunks - 1) * 2 * a.cols];
+#pragma unroll
+            for (int i = 0; i < kSumLoads; i++) v += k + i * kSumWaves < chunks ? t[i] : 0.f;
+        }
     }
     s[wave][lane] = v;
     __syncthreads();
