@@ -52,14 +52,18 @@ __device__ __forceinline__ void block_store4(const BlockGemmArgs &g, int m, int 
         if (left >= 4) {
             __builtin_memcpy(p, t, 8);
         } else {
-            for (int e = 0; e < left; e++) p[e] = (uint16_t)(t[e >> 1] >> (16 * (e & 1)));
+#pragma unroll
+            for (int e = 0; e < 3; e++)
+                if (e < left) p[e] = (uint16_t)(t[e >> 1] >> (16 * (e & 1)));
         }
     } else {
         float *p = reinterpret_cast<float *>(g.c) + (int64_t)m * g.ldc + n;
         if (left >= 4) {
             __builtin_memcpy(p, v, 16);
         } else {
-            for (int e = 0; e < left; e++) p[e] = v[e];
+#pragma unroll
+            for (int e = 0; e < 3; e++)  // constant indices: v is in registers
+                if (e < left) p[e] = v[e];
         }
     }
 }
@@ -218,38 +222,33 @@ __global__ __launch_bounds__(GNT, BF16OUT ? 2 : 1) void k_block_gemm(BlockGemmAr
         const float *ss = sS[b];
         Frag fb[2];
         Frag16 gb[2];
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
+        static_for<0, 2>([&](auto jj) {
+            constexpr int j = decltype(jj)::value;
             fb[j] = read_frag(sB[b], wn * 64 + j * 32 + l32, h);
             if constexpr (!BF16OUT) gb[j] = to_f16<FB>(fb[j]);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
+        });
+        static_for<0, 4>([&](auto tt) {
+            constexpr int i = decltype(tt)::value / 2, j = decltype(tt)::value % 2;
             const Frag fa = read_frag(sA[b], wm * 64 + i * 32 + l32, h);
-            Frag16 ga;
-            if constexpr (!BF16OUT) ga = to_f16<FA>(fa);
             const float sa = ss[wm * 64 + i * 32 + l32];
+            v16f p;
+            if constexpr (BF16OUT) p = block_fp8<FA, FB>(fa, fb[j]);
+            else p = block_f16(to_f16<FA>(fa), gb[j]);
+            if constexpr (BT) {
+                const float s = sa * ss[GB + wn * 64];
 #pragma unroll
-            for (int j = 0; j < 2; j++) {
-                v16f p;
-                if constexpr (BF16OUT) p = block_fp8<FA, FB>(fa, fb[j]);
-                else p = block_f16(ga, gb[j]);
-                if constexpr (BT) {
-                    const float s = sa * ss[GB + wn * 64];
+                for (int r = 0; r < 16; r++) acc[i][j][r] = __builtin_fmaf(p[r], s, acc[i][j][r]);
+            } else {
 #pragma unroll
-                    for (int r = 0; r < 16; r++) acc[i][j][r] = __builtin_fmaf(p[r], s, acc[i][j][r]);
-                } else {
+                for (int q = 0; q < 4; q++) {
+                    const float4 sb = *reinterpret_cast<const float4 *>(&ss[GB + wn * 64 + j * 32 + 8 * q + 4 * h]);
+                    const float s4[4] = {sb.x, sb.y, sb.z, sb.w};
 #pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        const float4 sb = *reinterpret_cast<const float4 *>(&ss[GB + wn * 64 + j * 32 + 8 * q + 4 * h]);
-                        const float s4[4] = {sb.x, sb.y, sb.z, sb.w};
-#pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            acc[i][j][4 * q + e] = __builtin_fmaf(p[4 * q + e], sa * s4[e], acc[i][j][4 * q + e]);
-                    }
+                    for (int e = 0; e < 4; e++)
+                        acc[i][j][4 * q + e] = __builtin_fmaf(p[4 * q + e], sa * s4[e], acc[i][j][4 * q + e]);
                 }
             }
-        }
+        });
         if (kt + 1 < nk) store(b ^ 1);
         __syncthreads();
     }
