@@ -426,9 +426,9 @@ mx_status_t mx_block_quantize_dual(const void *x_bf16, int64_t rows, int64_t col
  * Products of two scales outside fp32's range are Inf or 0.  A NaN scale makes
  * every element of C that it contributes to NaN; NaN and Inf codes behave as
  * these values.  Fast are operands whose rows are aligned to 16 bytes (any K;
- * as the quantizers' callers lay them out); others take a general kernel,
- * about half as fast.  A row's last 16 aligned bytes are read whole, its bytes
- * past K not used.
+ * as the quantizers' callers lay them out); others take a general kernel, at
+ * about two thirds of the speed.  A row's last 16 aligned bytes are read whole,
+ * its bytes past K not used.
  */
 mx_status_t mx_block_gemm(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa, mx_format_t fa,
                           const void *b_codes, int64_t ldb, const float *b_scales, int64_t ldsb, mx_format_t fb,

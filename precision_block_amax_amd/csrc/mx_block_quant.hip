@@ -14,7 +14,10 @@
 // reduction dimension's blocks are their outer dimension.
 //
 // Bound by memory: 2 bytes read and 1 byte (and 1/32) written per element and
-// form.
+// form.  Measured over inputs that take turns: 28672 x 4096 in tiles, both forms
+// (470 MB) 74 us, 6.4 TB/s; 8192 x 4096 by rows (102 MB) 18 us, 5.6 TB/s; 1000 x
+// 6144, both forms (25 MB, 384 workgroups) 10.3 us, of which launch, one read's
+// latency, two barriers and the stores, one after the other, are the most.
 #include "mx_block_util.h"
 
 namespace mx {

@@ -17,8 +17,14 @@
 // workspace to a second kernel.  All sums are in a fixed order, so the same
 // inputs give the same bits.
 //
-// All of it is bound by memory: 2 bytes read and 2 (1 for FP8) written per
-// element forward, 4 read and 2 written backward.
+// Bound by memory: 2 bytes read and 2 (1 for FP8) written per element forward,
+// 4 read and 2 written backward; next by the vector units, 4 clocks per
+// instruction and wave (250 of them for a wave's 1024 elements to FP8).
+// Measured: 8192 x 4096 to bf16 (134 MB) 25.8 us, 5.2 TB/s, to FP8 (102 MB) 22.8
+// us, 4.5 TB/s; backward (201 MB) 47.4 us, 43 of them the first kernel's; 1001 x
+// 8192 backward (49 MB) 18.8 us: 2 rows at a time in a workgroup leave two or
+// three latencies in a row, and the chunks' sums are a third of the bytes again.
+// One row of 4096: 4 us, launch and latency.
 #include <type_traits>
 
 #include "mx_block_util.h"
@@ -103,7 +109,9 @@ __device__ __forceinline__ void store_vec(uint16_t *p, const float (&y)[8], int 
 }
 
 // T threads and 8 T U >= cols elements per row, NT / T rows at a time; a workgroup takes the `per` rows from
-// blockIdx.x * per on, the next rows' loads under way while it works on these.  Block scales lie
+// blockIdx.x * per on, the next rows' loads under way while it works on these.  T: 4096 columns to FP8, 8192
+// rows, took 27 us with 256 threads a row, 28 with 512, 35 with 128 and 39 with a wave (no barriers, but the
+// parameters are then read again for every row).  Block scales lie
 // rows-innermost, so those of one row are 4-byte stores to as many lines: they are collected in LDS and
 // written as runs of the workgroup's rows (8192 x 4096: row by row 34 us, where the bf16 output with a
 // third more bytes took 27).
