@@ -18,8 +18,8 @@
 // inputs give the same bits.
 //
 // Bound by memory: 2 bytes read and 2 (1 for FP8) written per element forward,
-// 4 read and 2 written backward; next by the vector units, 4 clocks per
-// instruction and wave (250 of them for a wave's 1024 elements to FP8).
+// 4 read and 2 written backward; to FP8 the vector units, busy half of the time,
+// and the two barriers per row come next.
 // Measured: 8192 x 4096 to bf16 (134 MB) 25.8 us, 5.2 TB/s, to FP8 (102 MB) 22.8
 // us, 4.5 TB/s; backward (201 MB) 47.4 us, 43 of them the first kernel's; 1001 x
 // 8192 backward (49 MB) 18.8 us: 2 rows at a time in a workgroup leave two or
@@ -119,7 +119,9 @@ constexpr int kNormRows = 16;  // most rows per workgroup
 template <int T, int U, int TO, int F, bool WHOLE, bool PAST>
 __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a, int per) {
     constexpr int NT = T < 256 ? 256 : T, RPW = NT / T, W = T / 64;
-    constexpr bool KEEP = U <= 2;  // the parameters fit in registers beside a row
+    // the parameters and the next row fit in registers beside a row (with four vectors per thread they would be
+    // spilled: 2048 x 32768 to FP8 97 us with the next row, 68 without)
+    constexpr bool KEEP = U <= 2;
     __shared__ float s0[RPW][W], s1[RPW][W];
     __shared__ float sSc[TO == TO_BLOCK ? T * U / 16 * kNormRows : 1];  // [block][row]
     const int t = threadIdx.x % T, grp = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
@@ -145,7 +147,7 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a, int pe
         }
         return v;
     };
-    load(grp);  // under way while the parameters come
+    if constexpr (KEEP) load(grp);  // under way while the parameters come
     // past the row's end x, weight and bias are 0, and with them every term of the sums and y
     float wt[KEEP ? U : 1][8], bs[KEEP ? U : 1][8];
     if constexpr (KEEP) {
@@ -155,6 +157,7 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a, int pe
     for (int rb = 0; rb < count; rb += RPW) {
         const bool live = rb + grp < count;
         const int64_t row = r0 + rb + grp;
+        if constexpr (!KEEP) load(rb + grp);
         float y[U][8];
         float sum = 0.f;
 #pragma unroll
@@ -164,7 +167,7 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a, int pe
                 y[u][i] = (i & 1) ? bf16_hi(w[u][i >> 1]) : bf16_lo(w[u][i >> 1]);
                 sum += y[u][i];
             }
-        load(rb + grp + RPW);
+        if constexpr (KEEP) load(rb + grp + RPW);
         float mean = 0.f;
         if (!a.rms) {
             mean = row_sum(sum, s0) * rn;
