@@ -302,7 +302,8 @@ struct Cfg256x128 { static constexpr int TI = 2, WM = 4, WN = 2, KG = 1; static 
 struct Cfg128x128 { static constexpr int TI = 2, WM = 2, WN = 2, KG = 2; static constexpr bool PF = false; };
 struct Cfg128x128Far : Cfg128x128 { static constexpr bool PF = true; };
 
-// RAG: K ends inside a chunk of 16 bytes
+// RAG: K ends inside a chunk of 16 bytes.  The stages leave that chunk out, and its products are added after them
+// from registers (a branch for it in the loop made the compiler spill: up to 200 registers).
 template <int FA, int FB, bool BT, bool BF16OUT, class CFG, bool RAG>
 __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN * CFG::KG / 4) void k_block_gemm_pipe(BlockGemmArgs g) {
     constexpr int TI = CFG::TI, WM = CFG::WM, WN = CFG::WN, NS = 2, KG = CFG::KG;
@@ -330,7 +331,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     int tm, tn;
     block_tile_of(g, tm, tn);
     const int m0 = tm * PM, n0 = tn * PN;
-    const int nk = (g.K + kBlk - 1) / kBlk, ktail = g.K - (nk - 1) * kBlk;
+    const int K = RAG ? g.K & ~15 : g.K, nk = (K + kBlk - 1) / kBlk, ktail = K - (nk - 1) * kBlk;
     const int mrows = min(PM, g.M - m0), nrows = min(PN, g.N - n0);
     const int lda = (int)g.lda, ldb = (int)g.ldb;
     // rows past the operand lie past its records, whichever part of the offset is the scalar one (the range check
@@ -397,7 +398,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
         dma4(rS, sdst + (it & (SR - 1)) * (PM + PN), live ? vS : kDead, live ? kt * (int)lds_ * 4 : 0);
         if constexpr (PF) {
             const int pr = prow0 + it % PW * pper, pk = (it / PW + 1) * 1024 + (lane & 7) * 128;
-            dma4(rP, sDump, pw && pr < plim && pk < g.K ? pr * pld + pk : kDead, 0);
+            dma4(rP, sDump, pw && pr < plim && pk < K ? pr * pld + pk : kDead, 0);
         }
     };
 
@@ -460,18 +461,6 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
         pipe::wait_vm<PF>();  // the youngest load is a prefetch
         pipe::barrier();
         issue(u ^ 1, it + 1);
-        if constexpr (RAG) {
-            if (it == (nk - 1) / KG) {  // the last stage: the bytes past K in the rows' last chunks become 0
-                static_assert(PM + PN == 64 * NW, "a thread for each row");
-                if (it * KG + grp == nk - 1 && ktail % 16 != 0) {
-                    const int t = wave * 64 + lane, row = t < PM ? t : t - PM;
-                    uint8_t *const base = t < PM ? sC + u * PM * kBlk : sC + OB + u * PN * kBlk;
-                    uint4 *const q = reinterpret_cast<uint4 *>(base + swz<128>(row, ktail / 16));
-                    *q = keep_bytes(*q, ktail % 16);
-                }
-                pipe::barrier();
-            }
-        }
     };
 
     // EARLY: a stage begins with its first fragments in registers.  All its LDS reads are out before its
@@ -479,7 +468,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     // first reads fall into those tiles' matrix work instead of standing between two stages.  fp32 output,
     // 6144 x 4096 x 8192: 400 -> 381 us.  bf16 output has no registers left for it in 256 x 256 tiles (13
     // spilled: 187 -> 210 us) and gains nothing in 128 x 128 (47.7, 48.9 us).
-    constexpr bool EARLY = !BF16OUT && !RAG;
+    constexpr bool EARLY = !BF16OUT;
     Frag fa[2], fb[2];
     const auto stage = [&](int u, int it) {
         const float *const ss = sS + (it & (SR - 1)) * (PM + PN);
@@ -541,6 +530,47 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
         float4 sb[4];
         read_sb(sb);
         promote(acc[TI - 1][1], sb);
+    }
+    if constexpr (RAG) {
+        if (grp == 0) {
+            const int kb = K / kBlk;
+            // the first half of the lanes holds the chunk, the other one zeros
+            const auto chunk = [&](const uint8_t *p) {
+                uint4 v;
+                __builtin_memcpy(&v, p + K, 16);
+                return keep_bytes(v, h ? 0 : g.K - K);
+            };
+            static_for<0, 2>([&](auto jj) {
+                constexpr int j = decltype(jj)::value;
+                const int n = wn * 64 + j * 32;
+                const uint4 b = chunk(g.b + (int64_t)(n0 + min(n + l32, nrows - 1)) * ldb);
+                float sb[16];
+                if constexpr (BT) {
+                    sb[0] = g.bs[kb * g.ldsb + (n0 + min(n, nrows - 1)) / kBlk];
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 16; r++) sb[r] = g.bs[kb * g.ldsb + n0 + min(n + 8 * (r / 4) + 4 * h + r % 4, nrows - 1)];
+                }
+                static_for<0, TI>([&](auto ii) {
+                    constexpr int i = decltype(ii)::value;
+                    __builtin_amdgcn_sched_barrier(0);  // one tile's operands at a time
+                    const int m = m0 + min((wm * TI + i) * 32 + l32, mrows - 1);
+                    const uint4 a = chunk(g.a + (int64_t)m * lda);
+                    const float sa = g.as[kb * g.ldsa + m];
+                    v16f p = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    if constexpr (BF16OUT) {
+                        p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                            v8i{(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0},
+                            v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0}, p, FB, FA, 0, 0, 0, 0);
+                    } else {
+                        p = __builtin_amdgcn_mfma_f32_32x32x16_f16(to_f16x8<FB>(b.x, b.y), to_f16x8<FA>(a.x, a.y), p, 0, 0, 0);
+                        p = __builtin_amdgcn_mfma_f32_32x32x16_f16(to_f16x8<FB>(b.z, b.w), to_f16x8<FA>(a.z, a.w), p, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 16; r++) acc[i][j][r] = __builtin_fmaf(p[r], sa * sb[BT ? 0 : r], acc[i][j][r]);
+                });
+            });
+        }
     }
     pipe::wait_vm<0>();
     pipe::barrier();  // every wave has left the loop: the stages' LDS is free
@@ -797,7 +827,7 @@ hipError_t launch_block_gemm_few(BlockGemmArgs g, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int FA, int FB, bool BT, bool BF16OUT, class CFG, bool RAG = false>
+template <int FA, int FB, bool BT, bool BF16OUT, class CFG, bool RAG>
 hipError_t launch_block_gemm_pipe(BlockGemmArgs g, hipStream_t s) {
     constexpr int PM = CFG::WM * CFG::TI * 32, PN = CFG::WN * 64;
     g.tiles_m = (g.M + PM - 1) / PM;
@@ -805,6 +835,12 @@ hipError_t launch_block_gemm_pipe(BlockGemmArgs g, hipStream_t s) {
     hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, BF16OUT, CFG, RAG>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
                        dim3(64 * CFG::WM * CFG::WN * CFG::KG), 0, s, g);
     return hipGetLastError();
+}
+
+template <int FA, int FB, bool BT, bool BF16OUT, class CFG>
+hipError_t launch_block_gemm_k(const BlockGemmArgs &g, hipStream_t s) {
+    return g.K % 16 ? launch_block_gemm_pipe<FA, FB, BT, BF16OUT, CFG, true>(g, s)
+                    : launch_block_gemm_pipe<FA, FB, BT, BF16OUT, CFG, false>(g, s);
 }
 
 // The kernel for a product.  us measured on an MI355X, N = 4096 and bf16 output where not said otherwise.
@@ -817,12 +853,13 @@ hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
     const bool aligned = g.lda % 16 == 0 && g.ldb % 16 == 0 && (uintptr_t)g.a % 16 == 0 && (uintptr_t)g.b % 16 == 0 &&
                          256 * g.lda < lim && 256 * g.ldb < lim && (nk * g.ldsa + 256) * 4 < lim &&
                          (nk * g.ldsb + 256) * 4 < lim;
-    if (!aligned) {
+    const auto general = [&]() {
         g.tiles_m = (g.M + GB - 1) / GB;
         g.tiles_n = (g.N + GB - 1) / GB;
         hipLaunchKernelGGL((k_block_gemm<FA, FB, BT, BF16OUT>), dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(GNT), 0, s, g);
         return hipGetLastError();
-    }
+    };
+    if (!aligned) return general();
     const auto tiles = [&](int64_t m, int64_t n) { return (g.M + m - 1) / m * ((g.N + n - 1) / n); };
     const int64_t wide = (int64_t)1 << 26;  // columns from which 16 of them per workgroup would be 2^31 threads
     if (g.M <= 8 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 1, 1, 2>(g, s);
@@ -836,23 +873,23 @@ hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
     // round (M = 128) 21 against 64, two (256) 38 against 63; K = 4096, two 15 against 21, four (512) 27
     // against 21.  float32: one 24 against 36, two 32 against 36, four 48 against 38.
     if ((g.M <= 64 && g.N < wide) || tiles(64, 32) <= 512) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 8, 2, 1>(g, s);
-    if (g.K % 16 != 0) return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg128x128, true>(g, s);
+    if (g.K < 16) return general();  // no whole chunk for a stage
     const int64_t r128 = (tiles(128, 128) + 255) / 256;
     if constexpr (BF16OUT && BT) {
         // a round of 256 x 256 tiles takes 1.75 us per 128 K, one of 128 x 128 tiles 0.70
         const int64_t r256 = (tiles(256, 256) + 255) / 256;
-        if (5 * r256 <= 2 * r128) return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg256x256>(g, s);
+        if (5 * r256 <= 2 * r128) return launch_block_gemm_k<FA, FB, BT, BF16OUT, Cfg256x256>(g, s);
         // long rows, every CU busy: 1000 rows, K = 28672 184 without and 157 with the prefetch; 14336 79 and 75;
         // 8192 43 and 45
         if (g.K >= 12288 && tiles(128, 128) >= 256)
-            return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg128x128Far>(g, s);
+            return launch_block_gemm_k<FA, FB, BT, BF16OUT, Cfg128x128Far>(g, s);
     } else {
         // (with fp32 output or B's scales by column 256 x 256 tiles need more registers than there are)
         // a round of 256 x 128 tiles takes 2.0 us per 128 K (fp32), one of 128 x 128 tiles 1.05
         const int64_t r256 = (tiles(256, 128) + 255) / 256;
-        if (2 * r256 <= r128) return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg256x128>(g, s);
+        if (2 * r256 <= r128) return launch_block_gemm_k<FA, FB, BT, BF16OUT, Cfg256x128>(g, s);
     }
-    return launch_block_gemm_pipe<FA, FB, BT, BF16OUT, Cfg128x128>(g, s);
+    return launch_block_gemm_k<FA, FB, BT, BF16OUT, Cfg128x128>(g, s);
 }
 
 template <int FA, int FB>

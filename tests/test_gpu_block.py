@@ -216,6 +216,31 @@ def test_gemm_large(mx, M, N, K, tile, bf16):
         check_product(c, a, fa, b, fb, tile, bf16)
 
 
+# K ends inside 16 bytes: every tile size, a reduction of less than 16, whole blocks and one element, long rows
+RAGGED_K = [(40, 300, 257), (100, 300, 15), (1100, 1100, 1), (1100, 1100, 15), (1100, 1100, 17), (1111, 1301, 129), (1100, 1100, 255),
+            (2048, 2048, 12353), (4096, 2048, 135), (4100, 4250, 401), (4096, 4096, 1037), (8200, 4099, 31)]
+
+
+@pytest.mark.parametrize("M,N,K", RAGGED_K)
+@pytest.mark.parametrize("tile", [True, False])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_gemm_ragged_k(mx, M, N, K, tile, bf16):
+    """rows of whole 16 bytes whose bytes past K are NaN codes, as those around the operands are"""
+    import torch
+    print("case", M, N, K, tile, bf16, flush=True)
+
+    def inside(t):
+        buf = torch.full((t.shape[0] + 2, (K + 15) // 16 * 16 + 32), 0x7F, dtype=torch.uint8, device="cuda")
+        v = buf[1:1 + t.shape[0], 16:16 + K]
+        v.copy_(t)
+        return v
+
+    for fa, fb in (("e4m3", "e4m3"), ("e5m2", "e4m3")):
+        a, b = operand(mx, M, K, fa, False, M + K, 3), operand(mx, N, K, fb, tile, N + K + 1, 3)
+        c = mx.block_gemm(inside(a[0]), a[1], fa, inside(b[0]), b[1], fb, out_dtype=torch.bfloat16 if bf16 else torch.float32)
+        check_product(c, a, fa, b, fb, tile, bf16)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 200, 256), (40, 200, 300), (300, 520, 640), (520, 300, 272), (1200, 1160, 272), (1201, 1160, 301),
                                    (4200, 4100, 272)])
 @pytest.mark.parametrize("bf16", [True, False])
