@@ -534,16 +534,24 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     if constexpr (RAG) {
         if (grp == 0) {
             const int kb = K / kBlk;
-            // the first half of the lanes holds the chunk, the other one zeros
             const auto chunk = [&](const uint8_t *p) {
                 uint4 v;
                 __builtin_memcpy(&v, p + K, 16);
-                return keep_bytes(v, h ? 0 : g.K - K);
+                return v;
             };
+            const int left = h ? 0 : g.K - K;  // the first half of the lanes holds the chunk, the other one zeros
+            uint4 ca[TI];
+            float sa[TI];
+#pragma unroll
+            for (int i = 0; i < TI; i++) {
+                const int m = m0 + min((wm * TI + i) * 32 + l32, mrows - 1);
+                ca[i] = chunk(g.a + (int64_t)m * lda);
+                sa[i] = g.as[kb * g.ldsa + m];
+            }
             static_for<0, 2>([&](auto jj) {
                 constexpr int j = decltype(jj)::value;
                 const int n = wn * 64 + j * 32;
-                const uint4 b = chunk(g.b + (int64_t)(n0 + min(n + l32, nrows - 1)) * ldb);
+                const uint4 b = keep_bytes(chunk(g.b + (int64_t)(n0 + min(n + l32, nrows - 1)) * ldb), left);
                 float sb[16];
                 if constexpr (BT) {
                     sb[0] = g.bs[kb * g.ldsb + (n0 + min(n, nrows - 1)) / kBlk];
@@ -553,10 +561,8 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
                 }
                 static_for<0, TI>([&](auto ii) {
                     constexpr int i = decltype(ii)::value;
-                    __builtin_amdgcn_sched_barrier(0);  // one tile's operands at a time
-                    const int m = m0 + min((wm * TI + i) * 32 + l32, mrows - 1);
-                    const uint4 a = chunk(g.a + (int64_t)m * lda);
-                    const float sa = g.as[kb * g.ldsa + m];
+                    __builtin_amdgcn_sched_barrier(0);  // one tile at a time
+                    const uint4 a = keep_bytes(ca[i], left);
                     v16f p = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                     if constexpr (BF16OUT) {
                         p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
@@ -567,7 +573,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
                         p = __builtin_amdgcn_mfma_f32_32x32x16_f16(to_f16x8<FB>(b.z, b.w), to_f16x8<FA>(a.z, a.w), p, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int r = 0; r < 16; r++) acc[i][j][r] = __builtin_fmaf(p[r], sa * sb[BT ? 0 : r], acc[i][j][r]);
+                    for (int r = 0; r < 16; r++) acc[i][j][r] = __builtin_fmaf(p[r], sa[i] * sb[BT ? 0 : r], acc[i][j][r]);
                 });
             });
         }
