@@ -155,8 +155,8 @@ mx_status_t mx_block_gemm(const void *a_codes, int64_t lda, const float *a_scale
                         {c, extent(M, ldc, N, o == MX_OUT_BF16 ? 2 : 4)}};
     mx_status_t st = check_ranges(r, 5, 4);
     if (st != MX_OK) return st;
-    // sizes in 31 bits; at most 2^22 workgroups of up to 512 threads
-    if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim || blocks(M) * blocks(N) >= ((int64_t)1 << 22))
+    // sizes in 31 bits, K rounded up to whole blocks too; at most 2^22 workgroups of up to 512 threads
+    if (M >= kMaxDim || N >= kMaxDim || K > kMaxDim - kBlk || blocks(M) * blocks(N) >= ((int64_t)1 << 22))
         return MX_ERR_UNSUPPORTED;
     if ((st = check_device()) != MX_OK) return st;
     BlockGemmArgs g{(const uint8_t *)a_codes, (const uint8_t *)b_codes, a_scales, b_scales, c, lda, ldb, ldsa, ldsb, ldc,

@@ -856,9 +856,9 @@ hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
     if (g.M == 1) g.lda = (g.K + 15) / 16 * 16;  // a single row has no stride
     if (g.N == 1) g.ldb = (g.K + 15) / 16 * 16;
     const int64_t nk = (g.K + kBlk - 1) / kBlk, lim = (int64_t)1 << 31;
+    const int64_t lim_code = lim / 256, lim_scale = (lim / 4 - 257) / nk;  // strides may be any 64-bit number: no products
     const bool aligned = g.lda % 16 == 0 && g.ldb % 16 == 0 && (uintptr_t)g.a % 16 == 0 && (uintptr_t)g.b % 16 == 0 &&
-                         256 * g.lda < lim && 256 * g.ldb < lim && (nk * g.ldsa + 256) * 4 < lim &&
-                         (nk * g.ldsb + 256) * 4 < lim;
+                         g.lda < lim_code && g.ldb < lim_code && g.ldsa <= lim_scale && g.ldsb <= lim_scale;
     const auto general = [&]() {
         g.tiles_m = (g.M + GB - 1) / GB;
         g.tiles_n = (g.N + GB - 1) / GB;
