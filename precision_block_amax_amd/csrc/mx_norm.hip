@@ -59,6 +59,16 @@ __device__ __forceinline__ float rsqrt1(float v) {
     return __builtin_fmaf(0.5f * y, __builtin_fmaf(-(v * y), y, 1.0f), y);
 }
 
+// sum / n, correctly rounded unless it is subnormal: an approximation and one correction by its exact remainder, as
+// block_scale (n: a whole number, rn its rounded reciprocal).  sum * rn alone gives constant rows of 896, 1000 or
+// 7168 columns a mean beside their value, and y then shows the difference times a very large rstd.  An infinite
+// quotient has no remainder.
+__device__ __forceinline__ float row_mean(float sum, float n, float rn) {
+    const float q = sum * rn;
+    const float m = __builtin_fmaf(__builtin_fmaf(-q, n, sum), rn, q);
+    return __builtin_fabsf(q) < INFINITY ? m : q;
+}
+
 // Parameters of vectors c0 + 8 T u (u < U) as fp32: `other` where there are none, 0 past cols.  Without WHOLE a
 // vector that the row's end cuts is taken element by element.  All loads go out before the first is used.
 template <bool WHOLE, int T, int U>
@@ -170,7 +180,7 @@ __global__ __launch_bounds__((T < 256 ? 256 : T)) void k_norm(NormArgs a, int pe
         if constexpr (KEEP) load(rb + grp + RPW);
         float mean = 0.f;
         if (!a.rms) {
-            mean = row_sum(sum, s0) * rn;
+            mean = row_mean(row_sum(sum, s0), (float)a.cols, rn);
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 const int n = a.cols - 8 * (u * T + t);

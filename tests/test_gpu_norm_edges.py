@@ -1,0 +1,59 @@
+"""The norm on rows that a rounding of the mean shows up in, and its backward pass beside large means."""
+import pytest
+
+import block_reference as ref
+
+pytestmark = pytest.mark.gpu
+E = 2.0 ** -18   # test_gpu_norm.py: fp32 sums of a row and the few roundings after them
+
+
+@pytest.fixture(scope="module")
+def mx():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import precision_block_amax_amd as m
+    m.lib()
+    return m
+
+
+@pytest.mark.parametrize("cols", [1, 100, 513, 896, 1000, 1792, 3584, 4096, 7168, 14336, 16392, 28672, 32768])
+def test_constant_rows(mx, cols):
+    """every bf16 significand, repeated: the fp32 sum of up to 2^15 equal numbers of 8 bits is exact in any order, so
+    the mean is the number itself, every x - mean is 0 and y is the bias, in every output form; with eps = 0 rstd is
+    Inf and y NaN"""
+    import torch
+    print("case", cols, flush=True)
+    sig = torch.arange(128, 256, device="cuda").double()
+    x = torch.cat([sig * 2.0 ** -7, -sig * 2.0 ** 6, sig * 2.0 ** -40]).bfloat16()[:, None].repeat(1, cols)
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    w, b = ((torch.randn(cols, device="cuda", generator=g)).bfloat16() for _ in range(2))
+    y, mean, rstd = mx.layer_norm(x, w, b, eps=1e-5)
+    assert torch.equal(mean, x[:, 0].float())
+    assert ((rstd.double() * 1e-5 ** 0.5 - 1).abs() <= 2.0 ** -22).all()
+    assert torch.equal(y, b.expand_as(y))
+    want = ref.quantize(b[None], "e4m3")
+    codes, scales, mean, _ = mx.layer_norm_quantize(x, w, b, "e4m3", eps=1e-5)
+    assert torch.equal(mean, x[:, 0].float())
+    assert torch.equal(codes, want[0].expand_as(codes)) and torch.equal(scales, want[1].expand_as(scales))
+    if cols % 32 == 0:
+        want = mx.quantize(b[None].contiguous(), "e2m1")
+        codes, scales, _, _ = mx.layer_norm_quantize(x, w, b, "e2m1", eps=1e-5, scaling="mx")
+        assert torch.equal(codes, want[0].expand_as(codes)) and torch.equal(scales, want[1].expand_as(scales))
+    y, mean, rstd = mx.layer_norm(x, w, b, eps=0.0)
+    assert torch.equal(mean, x[:, 0].float()) and (rstd == float("inf")).all() and y.isnan().all()
+
+
+@pytest.mark.parametrize("cols", [1, 7, 100, 513, 1000, 4096, 7168, 16392])
+def test_mean_is_the_rounded_quotient(mx, cols):
+    """rows of small whole numbers: the sum is exact in any order, and the mean is its quotient rounded to fp32 once;
+    a row with an Inf has that mean, and one whose sum leaves fp32 an infinite one"""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.randint(-255, 256, (300, cols), device="cuda", generator=g).bfloat16()
+    want = (x.double().sum(1) / cols).float()   # a quotient of 24 bits by 15 rounded to 53 first: no double rounding
+    x[7, cols // 2] = float("inf")
+    x[8, 0] = -float("inf")
+    x[9] = 3e38
+    want[7], want[8], want[9] = float("inf"), -float("inf"), float("inf") if cols > 1 else x[9, 0].float()
+    mean = mx.layer_norm(x)[1]
+    assert torch.equal(mean, want)
