@@ -333,7 +333,8 @@ __global__ __launch_bounds__(T *R) void k_norm_bwd(NormBwdArgs a, int per) {
     for (int rb = 0; rb < count; rb += R) {
         const int row = rb + grp;
         uint32_t cx[U][4], cd[U][4];
-        const float rs = rstd, mn = mean;
+        // a row that is not there has x, mean and rstd 0, and with them xh
+        const float rs = row < count ? rstd : 0.f, mn = row < count ? mean : 0.f;
         float sg = 0.f, sgx = 0.f;
 #pragma unroll
         for (int u = 0; u < U; u++) {
@@ -342,9 +343,20 @@ __global__ __launch_bounds__(T *R) void k_norm_bwd(NormBwdArgs a, int per) {
                 cx[u][k] = wx[u][k];
                 cd[u][k] = wd[u][k];
             }
+            // past the row's end x and dy are 0, and mu too: mean * rstd may be beyond fp32 where no xh is, and
+            // Inf times a dy of 0 is NaN
+            const int n = a.cols - 8 * (u * T + t);
+            const float mu = n > 0 ? mn : 0.f;
+            float xm[8];
 #pragma unroll
-            for (int i = 0; i < 8; i++) {  // past the row's end dy is 0, and so is every term
-                const float d = get(cd[u], i), xh = (get(cx[u], i) - mn) * rs, g = d * wt[u][i];
+            for (int i = 0; i < 8; i++) xm[i] = get(cx[u], i) - mu;
+            if (!WHOLE && n < 8) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) xm[i] = i < n ? xm[i] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float d = get(cd[u], i), xh = xm[i] * rs, g = d * wt[u][i];
                 sg += g;
                 sgx = __builtin_fmaf(g, xh, sgx);
                 if constexpr (PARAMS) {

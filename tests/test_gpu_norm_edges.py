@@ -57,3 +57,29 @@ def test_mean_is_the_rounded_quotient(mx, cols):
     want[7], want[8], want[9] = float("inf"), -float("inf"), float("inf") if cols > 1 else x[9, 0].float()
     mean = mx.layer_norm(x)[1]
     assert torch.equal(mean, want)
+
+
+@pytest.mark.parametrize("rows,cols", [(9, 100), (300, 513), (33, 1000), (300, 1024), (11, 2056), (65, 4096), (3, 8200), (5, 16392)])
+@pytest.mark.parametrize("params", [True, False])
+def test_backward_beside_a_large_mean(mx, rows, cols, params):
+    """constant rows of 1e33 between ordinary ones, eps = 1e-12: mean * rstd is beyond fp32, but x - mean is 0 in every
+    column, and nothing of it reaches dx, the parameters' sums or other rows.  Each term carries the roundings of
+    E's derivation, relative to itself; the sums over rows those of test_gpu_norm.py"""
+    import torch
+    print("case", rows, cols, params, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    x, w, dy = r(rows, cols).bfloat16(), (1 + 0.3 * r(cols)).bfloat16(), (1e-2 * r(rows, cols)).bfloat16()
+    x[0::4], x[2::4] = 1e33, -1e33
+    _, mean, rstd = mx.layer_norm(x, w, eps=1e-12)
+    assert torch.equal(mean[0::2], x[0::2, 0].float()) and bool((rstd * mean)[0::2].isinf().all())
+    dx, dw, db = mx.layer_norm_backward(dy, x, w, mean, rstd, weight_grad=params, bias_grad=params)
+    wx, ww, wb = ref.norm_backward(dy, x, w, mean, rstd, False)
+    d, k = dy.double().abs(), rstd.double()[:, None]
+    xh = (x.double() - mean.double()[:, None]).abs() * k
+    t = d * w.double().abs()
+    tol = 2.0 ** -8 * wx.abs() + 2.0 ** -134 + 2 * E * k * (t + t.mean(1, keepdim=True) + xh * (t * xh).mean(1, keepdim=True))
+    assert ((dx.double() - wx).abs() <= tol).all()
+    if params:
+        n = (rows / 128 + 16 + 128 + 8) * 2.0 ** -24
+        assert ((dw.double() - ww).abs() <= n * (d * xh).sum(0)).all() and ((db.double() - wb).abs() <= n * d.sum(0)).all()
