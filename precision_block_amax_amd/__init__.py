@@ -404,7 +404,7 @@ def _input(x: torch.Tensor) -> Tuple[int, int, int]:
     if x.dtype is not _BF16 or x.dim() != 2 or not x.is_cuda:
         raise ValueError("expected a 2-D bf16 tensor on a GPU")
     (rows, cols), (ld, step) = x.shape, x.stride()
-    if step != 1 and rows and cols:
+    if step != 1 and cols > 1 and rows:
         raise ValueError("the last dimension must be contiguous")
     return rows, cols, ld if rows > 1 else cols
 

@@ -83,3 +83,18 @@ def test_backward_beside_a_large_mean(mx, rows, cols, params):
     if params:
         n = (rows / 128 + 16 + 128 + 8) * 2.0 ** -24
         assert ((dw.double() - ww).abs() <= n * (d * xh).sum(0)).all() and ((db.double() - wb).abs() <= n * d.sum(0)).all()
+
+
+def test_single_column_of_any_stride(mx):
+    """rows of one element are contiguous whatever the stride of that dimension says"""
+    import torch
+    x = torch.randn(1, 300, device="cuda").bfloat16()
+    col = x.t()
+    assert col.shape == (300, 1) and col.stride(1) == 300
+    for mode in ("row", "transpose", "tile", "tile_transpose"):
+        got, want = mx.block_quantize(col, "e4m3", mode), ref.quantize(col, "e4m3", mode)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    y, mean, rstd = mx.layer_norm(col, eps=1.0)
+    assert (y == 0).all() and torch.equal(mean, x[0].float()) and (rstd == 1).all()
+    dx, dw, db = mx.layer_norm_backward(col, col, None, mean, rstd)
+    assert (dx == 0).all() and (dw == 0).all()
