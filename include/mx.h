@@ -374,6 +374,11 @@ mx_status_t mx_gemm_layout(const void *a_codes, mx_layout_t a_layout, const void
  * of rows (tile rows).  Bytes between the end of a row and the next row, and
  * floats between the last row's scale and the next block's, are neither read
  * as values nor written.
+ *
+ * Overlap, in these calls and the norm's below: no byte of an output may be
+ * one of another buffer of the call.  Whole extents that are disjoint always
+ * qualify; so do two buffers with one row stride in bytes whose rows lie in
+ * each other's gaps (a norm's x and y as the halves of wider rows, say).
  */
 typedef enum {
     MX_BLOCK_ROW = 0,            /* blocks of 128 along cols; codes [rows x cols]; scales [ceil(cols/128)][rows]  */

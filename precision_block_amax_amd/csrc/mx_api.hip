@@ -44,11 +44,7 @@ mx_status_t check_quant(const void *x, int64_t rows, int64_t cols, int64_t ldx, 
 bool strided_overlap(const void *p, int64_t lp, int64_t wp, const void *q, int64_t lq, int64_t wq, int64_t rows) {
     if (rows <= 0 || wp <= 0 || wq <= 0) return false;
     if (!overlap(p, (rows - 1) * lp + wp, q, (rows - 1) * lq + wq)) return false;
-    if (lp != lq) return true;
-    const int64_t L = lp;
-    int64_t d = (int64_t)((uintptr_t)q - (uintptr_t)p) % L;
-    if (d < 0) d += L;
-    return !(d >= wp && d + wq <= L);
+    return lp != lq || !interleaved(p, wp, q, wq, lp);
 }
 
 // checks of the GEMM's arguments, operand row strides in bytes

@@ -18,25 +18,32 @@ bool fp8(int f) { return f == MX_E4M3 || f == MX_E5M2; }
 bool type_ok(int t) { return t == MX_OUT_F32 || t == MX_OUT_BF16; }
 int64_t blocks(int64_t n) { return (n + kBlk - 1) / kBlk; }
 
-// bytes from the first of `rows` rows to the end of the last: row stride ld, `width` used, in units of
-// `size` bytes; -1 if that leaves 64 bits
-int64_t extent(int64_t rows, int64_t ld, int64_t width, int64_t size) {
-    if (rows <= 0 || width <= 0) return 0;
-    if (rows - 1 > (INT64_MAX / size - width) / ld) return -1;
-    return ((rows - 1) * ld + width) * size;
-}
-
+// `rows` rows of `width` used bytes, one every `stride` bytes (0: a single row); `n` bytes from the first of them to the
+// end of the last, -1 if that leaves 64 bits
 struct Range {
     const void *p;
-    int64_t n;
+    int64_t n, width, stride;
 };
+Range run(const void *p, int64_t n) { return {p, n, n, 0}; }
+// row stride ld, `width` used, in units of `size` bytes
+Range rows_at(const void *p, int64_t rows, int64_t ld, int64_t width, int64_t size) {
+    if (rows <= 0 || width <= 0) return run(p, 0);
+    if (rows == 1 && width <= INT64_MAX / size) return run(p, width * size);
+    if (rows - 1 > (INT64_MAX / size - width) / ld) return run(p, -1);
+    return {p, ((rows - 1) * ld + width) * size, width * size, ld * size};
+}
+// no byte belongs to both: their whole extents are disjoint, or the rows of one lie in the gaps of the other's
+bool disjoint(const Range &a, const Range &b) {
+    if (!overlap(a.p, a.n, b.p, b.n)) return true;
+    return a.stride > 0 && a.stride == b.stride && interleaved(a.p, a.width, b.p, b.width, a.stride);
+}
 // every range exists (n >= 0) and no range from `first_out` on overlaps another one
 mx_status_t check_ranges(const Range *r, int count, int first_out) {
     for (int i = 0; i < count; i++)
         if (r[i].n < 0) return MX_ERR_INVALID_ARG;
     for (int i = first_out; i < count; i++)
         for (int j = 0; j < i; j++)
-            if (overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return MX_ERR_INVALID_ARG;
+            if (!disjoint(r[i], r[j])) return MX_ERR_INVALID_ARG;
     return MX_OK;
 }
 
@@ -46,8 +53,8 @@ mx_status_t check_form(int64_t n, int64_t k, bool tile, int fmt, const void *cod
     if (!fp8(fmt) || ld_codes < k || ld_scales < (tile ? blocks(n) : n)) return MX_ERR_INVALID_ARG;
     if (n == 0 || k == 0) return MX_OK;
     if (!codes || !scales) return MX_ERR_INVALID_ARG;
-    r[0] = {codes, extent(n, ld_codes, k, 1)};
-    r[1] = {scales, extent(blocks(k), ld_scales, tile ? blocks(n) : n, 4)};
+    r[0] = rows_at(codes, n, ld_codes, k, 1);
+    r[1] = rows_at(scales, blocks(k), ld_scales, tile ? blocks(n) : n, 4);
     return MX_OK;
 }
 
@@ -69,7 +76,7 @@ mx_status_t block_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld
     }
     if (rows == 0 || cols == 0) return MX_OK;
     if (!x) return MX_ERR_INVALID_ARG;
-    r[0] = {x, extent(rows, ldx, cols, 2)};
+    r[0] = rows_at(x, rows, ldx, cols, 2);
     if ((st = check_ranges(r, n, 1)) != MX_OK) return st;
     // one workgroup of 256 threads per tile, counted in 32 bits
     if (rows > kMaxDim || cols > kMaxDim || blocks(rows) * blocks(cols) >= ((int64_t)1 << 24)) return MX_ERR_UNSUPPORTED;
@@ -89,7 +96,7 @@ mx_status_t check_norm(const void *x, int64_t rows, int64_t cols, int64_t ldx, i
 
 mx_status_t norm(const void *x, int64_t rows, int64_t cols, int64_t ldx, const void *weight, const void *bias,
                  int param, int kind, float eps, int to, int fmt, void *out, int64_t ld_out, int64_t out_width,
-                 int64_t out_size, void *scales, int64_t ld_scales, int64_t scale_bytes, float *mean, float *rstd,
+                 int64_t out_size, void *scales, int64_t ld_scales, const Range &scale_range, float *mean, float *rstd,
                  void *stream) {
     mx_status_t st = check_norm(x, rows, cols, ldx, param, kind);
     if (st != MX_OK) return st;
@@ -98,13 +105,13 @@ mx_status_t norm(const void *x, int64_t rows, int64_t cols, int64_t ldx, const v
     if (!out || (to != TO_BF16 && !scales)) return MX_ERR_INVALID_ARG;
     const int64_t ps = param == MX_OUT_BF16 ? 2 : 4;
     if (kind == MX_NORM_RMS) mean = nullptr;
-    const Range r[7] = {{x, extent(rows, ldx, cols, 2)},
-                        {weight, weight ? cols * ps : 0},
-                        {bias, bias ? cols * ps : 0},
-                        {out, extent(rows, ld_out, out_width, out_size)},
-                        {scales, scale_bytes},
-                        {mean, mean ? rows * 4 : 0},
-                        {rstd, rstd ? rows * 4 : 0}};
+    const Range r[7] = {rows_at(x, rows, ldx, cols, 2),
+                        run(weight, weight ? cols * ps : 0),
+                        run(bias, bias ? cols * ps : 0),
+                        rows_at(out, rows, ld_out, out_width, out_size),
+                        scale_range,
+                        run(mean, mean ? rows * 4 : 0),
+                        run(rstd, rstd ? rows * 4 : 0)};
     if ((st = check_ranges(r, 7, 3)) != MX_OK) return st;
     if ((st = check_device()) != MX_OK) return st;
     const NormArgs a{(const uint16_t *)x, rows,   ldx,    (int)cols, weight, bias,     param == MX_OUT_BF16,
@@ -148,11 +155,9 @@ mx_status_t mx_block_gemm(const void *a_codes, int64_t lda, const float *a_scale
     if (lda < K || ldb < K || ldsa < M || ldsb < nb || ldc < N) return MX_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return MX_OK;
     if (!c || (K > 0 && (!a_codes || !a_scales || !b_codes || !b_scales))) return MX_ERR_INVALID_ARG;
-    const Range r[5] = {{a_codes, extent(M, lda, K, 1)},
-                        {a_scales, extent(blocks(K), ldsa, M, 4)},
-                        {b_codes, extent(N, ldb, K, 1)},
-                        {b_scales, extent(blocks(K), ldsb, nb, 4)},
-                        {c, extent(M, ldc, N, o == MX_OUT_BF16 ? 2 : 4)}};
+    const Range r[5] = {rows_at(a_codes, M, lda, K, 1), rows_at(a_scales, blocks(K), ldsa, M, 4),
+                        rows_at(b_codes, N, ldb, K, 1), rows_at(b_scales, blocks(K), ldsb, nb, 4),
+                        rows_at(c, M, ldc, N, o == MX_OUT_BF16 ? 2 : 4)};
     mx_status_t st = check_ranges(r, 5, 4);
     if (st != MX_OK) return st;
     // sizes in 31 bits, K rounded up to whole blocks too; at most 2^22 workgroups of up to 512 threads
@@ -169,7 +174,7 @@ mx_status_t mx_layer_norm(const void *x_bf16, int64_t rows, int64_t cols, int64_
                           float *mean, float *rstd, void *stream) {
     if (ldy < cols) return MX_ERR_INVALID_ARG;
     return norm(x_bf16, rows, cols, ldx, weight, bias, raw(param), raw(kind), eps, TO_BF16, 0, y_bf16, ldy, cols, 2,
-                nullptr, 0, 0, mean, rstd, stream);
+                nullptr, 0, run(nullptr, 0), mean, rstd, stream);
 }
 
 mx_status_t mx_layer_norm_quantize(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx, const void *weight,
@@ -179,7 +184,7 @@ mx_status_t mx_layer_norm_quantize(const void *x_bf16, int64_t rows, int64_t col
     if (!fmt_ok(f) || cols < 0 || cols % 32 != 0 || rows < 0) return MX_ERR_INVALID_ARG;
     const int64_t cb = code_bytes(cols, f), sb = cols / 32;
     return norm(x_bf16, rows, cols, ldx, weight, bias, raw(param), raw(kind), eps, TO_MX, f, codes, cb, cb, 1, scales,
-                sb, extent(rows, sb, sb, 1), mean, rstd, stream);
+                sb, rows_at(scales, rows, sb, sb, 1), mean, rstd, stream);
 }
 
 mx_status_t mx_layer_norm_block_quantize(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx,
@@ -189,7 +194,7 @@ mx_status_t mx_layer_norm_block_quantize(const void *x_bf16, int64_t rows, int64
     const int f = raw(fmt);
     if (!fp8(f) || cols < 0 || rows < 0 || ld_codes < cols || ld_scales < rows) return MX_ERR_INVALID_ARG;
     return norm(x_bf16, rows, cols, ldx, weight, bias, raw(param), raw(kind), eps, TO_BLOCK, f, codes, ld_codes, cols,
-                1, scales, ld_scales, extent(blocks(cols), ld_scales, rows, 4), mean, rstd, stream);
+                1, scales, ld_scales, rows_at(scales, blocks(cols), ld_scales, rows, 4), mean, rstd, stream);
 }
 
 int64_t mx_layer_norm_backward_workspace(int64_t rows, int64_t cols) {
@@ -209,15 +214,15 @@ mx_status_t mx_layer_norm_backward(const void *dy_bf16, int64_t lddy, const void
     if (rows > 0 && (!dy_bf16 || !rstd || !dx_bf16 || (k == MX_NORM_LAYER && !mean))) return MX_ERR_INVALID_ARG;
     const int64_t need = dweight || dbias ? mx_layer_norm_backward_workspace(rows, cols) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 16 != 0)) return MX_ERR_INVALID_ARG;
-    const Range r[9] = {{dy_bf16, extent(rows, lddy, cols, 2)},
-                        {x_bf16, extent(rows, ldx, cols, 2)},
-                        {weight, weight ? cols * (p == MX_OUT_BF16 ? 2 : 4) : 0},
-                        {mean, k == MX_NORM_LAYER ? rows * 4 : 0},
-                        {rstd, rows * 4},
-                        {dx_bf16, extent(rows, lddx, cols, 2)},
-                        {dweight, dweight ? cols * 4 : 0},
-                        {dbias, dbias ? cols * 4 : 0},
-                        {workspace, need}};
+    const Range r[9] = {rows_at(dy_bf16, rows, lddy, cols, 2),
+                        rows_at(x_bf16, rows, ldx, cols, 2),
+                        run(weight, weight ? cols * (p == MX_OUT_BF16 ? 2 : 4) : 0),
+                        run(mean, k == MX_NORM_LAYER ? rows * 4 : 0),
+                        run(rstd, rows * 4),
+                        rows_at(dx_bf16, rows, lddx, cols, 2),
+                        run(dweight, dweight ? cols * 4 : 0),
+                        run(dbias, dbias ? cols * 4 : 0),
+                        run(workspace, need)};
     if ((st = check_ranges(r, 9, 5)) != MX_OK) return st;
     if ((st = check_device()) != MX_OK) return st;
     const NormBwdArgs a{(const uint16_t *)dy_bf16, (const uint16_t *)x_bf16, rows, lddy, ldx, lddx, (int)cols, weight,

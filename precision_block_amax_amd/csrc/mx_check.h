@@ -37,6 +37,14 @@ inline bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
     return a < b + (uintptr_t)m && b < a + (uintptr_t)n;
 }
 
+// Rows of wp bytes from p and of wq bytes from q, both one row every `stride` bytes, any number of them: every row
+// of the second lies in the gap after a row of the first.
+inline bool interleaved(const void *p, int64_t wp, const void *q, int64_t wq, int64_t stride) {
+    int64_t d = (int64_t)((uintptr_t)q - (uintptr_t)p) % stride;
+    if (d < 0) d += stride;
+    return d >= wp && d + wq <= stride;
+}
+
 inline mx_status_t check_device() {
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0) return MX_ERR_HIP;

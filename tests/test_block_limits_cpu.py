@@ -26,3 +26,24 @@ def test_block_gemm_longest_k(L, out):
     for K in ((1 << 31) - 127, (1 << 31) - 1, 1 << 31, 1 << 40):
         args = [P(1 << 44), K, P(1 << 45), 1, E4M3, P(1 << 46), K, P(1 << 47), 1, E4M3, 0, 1, 1, K, P(1 << 32), out, 1, None]
         assert L.mx_block_gemm(*args) == UNSUPPORTED, K
+
+
+def test_interleaved_rows_that_touch(L):
+    """Rows in the gaps of another buffer's rows are refused where one byte is shared, where the strides differ, and
+    where a run of other memory lies between them (pointers are compared on the host only)."""
+    x = 0x100000000
+    y = lambda **k: [P(x), 10, 64, k.get("ldx", 200), None, None, BF16, 0, 1e-5, P(x + k.get("at", 128)), k.get("ldy", 200),
+                     P(k.get("mean", 0x200000000)), P(0x300000000), None]
+    for bad in (dict(at=126), dict(at=274), dict(at=0), dict(ldy=201), dict(at=128 + 2 * 200 * 3 + 146), dict(at=-2 * 200 * 3 + 126),
+                dict(mean=x + 300), dict(mean=x + 260)):
+        assert L.mx_layer_norm(*y(**bad)) == INVALID, bad
+    q = lambda s, ld: [P(x), 256, 64, 64, E4M3, 1, P(0x400000000), 512, P(0x400000000 + s), ld, None]  # 64 rows of 256 codes, 2 of scales
+    for s, ld in ((252, 128), (257, 128), (256, 129), (256, 64)):
+        assert L.mx_block_quantize(*q(s, ld)) == INVALID, (s, ld)
+
+
+def test_interleaved_rows_of_different_counts_are_counted_whole(L):
+    """(rows - 1) strides and a width that leave 64 bits are refused, a single row with any stride is not"""
+    args = lambda ld, rows: [P(0x100000000), rows, 64, ld, None, None, BF16, 0, 1e-5, None, 64, None, None, None]
+    assert L.mx_layer_norm(*args(1 << 62, 3)) == INVALID
+    assert L.mx_layer_norm(*args(1 << 62, 0)) == OK
