@@ -749,6 +749,9 @@ __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(BlockGemmArgs g) {
     int slot = 0;
     for (int i = 0; i < count; i++) {
         pipe::wait_vm<(S - 1) * LPB>();
+        // what the loads wrote to LDS is read below: no read may move up past the wait, which the compiler takes for
+        // an instruction without effect on memory
+        asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
         const uint8_t *const d = ring + slot * BLK;
         Frag2 fa[MT], fb[NT];
