@@ -421,9 +421,11 @@ mx_status_t mx_block_quantize_dual(const void *x_bf16, int64_t rows, int64_t col
  * `out`, ldc >= N.  Every block's sum is multiplied by its scales and added to
  * an fp32 accumulator.
  *   MX_OUT_F32   every product is exact and sums are fp32: |C - sum| <=
- *                1e-5 * sum |terms| up to K = 16384, and at the very worst
- *                2^-24 * sum |terms| more for each 128 of K beyond.  The codes
- *                travel as fp16 (exact) through the fp16 matrix instruction.
+ *                (130 + ceil(K / 128)) * 2^-24 * sum |terms|, which is one
+ *                rounding for each of a block's additions, for its scales and
+ *                for each block's addition to the rest (1e-5 up to K = 4736;
+ *                random data stays within it far beyond).  The codes travel as
+ *                fp16 (exact) through the fp16 matrix instruction.
  *   MX_OUT_BF16  the FP8 matrix instruction, at twice that rate.  It adds the
  *                32 products of a step in a window that ends 2^-13 below the
  *                largest, so a block's sum may be off by 2^-8 of its sum of

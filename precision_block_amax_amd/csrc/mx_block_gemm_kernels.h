@@ -12,7 +12,9 @@
 //
 // fp32 output: FP8 codes are converted to fp16 (exact) and multiplied by
 // V_MFMA_F32_32X32X16_F16, whose products are exact and whose sums lose no
-// more than fp32 does.  bf16 output: V_MFMA_F32_32X32X64_F8F6F4 on the
+// more than fp32 does (measured: 448 x 448 at any place among 127 equal terms from
+// 2^-9 to 2^-5, a block's sum is off by 10 * 2^-24 of its terms at most, where 127
+// roundings could cost 127).  bf16 output: V_MFMA_F32_32X32X64_F8F6F4 on the
 // codes themselves, twice the rate.  Measured on gfx950, that instruction adds
 // the products of 32 K in a window ending 2^-13 below the largest (the
 // unscaled FP8 instructions, 32x32x16 and 16x16x32, do the same): at most 31

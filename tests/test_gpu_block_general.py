@@ -113,3 +113,32 @@ def test_one_block_scales_of_any_stride(mx):
         assert mx.lib().mx_block_gemm(P(a[0]), K, P(a[1]), ld, 0, P(b[0]), K, P(b[1]), ld, 0, 0, M, N, K, P(c), 0, N,
                                       ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
         check(c, a, "e4m3", b, "e4m3", False, K)
+
+
+# every kernel: few rows (8 to 64), 64 x 32, 128 x 128 and 256 x 128 tiles, and any alignment
+@pytest.mark.parametrize("M,N", [(1, 64), (40, 64), (64, 300), (300, 256), (1200, 1200), (4200, 4100)])
+@pytest.mark.parametrize("aligned", [True, False])
+def test_fp32_sums_that_lose_the_most(mx, M, N, aligned):
+    """one term of 448 * 448 = 200704, whose fp32 step is 2^-6, among terms just under half a step and just under a
+    step of it (15/16 2^-7 and 15/16 2^-6), in its block and in 300 others, before and after it: every addition loses
+    nearly as much as it can"""
+    import torch
+    print("case", M, N, aligned, flush=True)
+    K = 128 * 301
+    one = lambda n: torch.ones(301, n, device="cuda")
+    code = lambda v: int(torch.tensor([v]).to(torch.float8_e4m3fn).view(torch.uint8).item())
+    place = (lambda t: t) if aligned else (lambda t: inside(t, 1, 2, 0x7F))
+    for where in (0, 64, 127, 128 * 150 + 3, K - 1):
+        for small in (1.875 * 2.0 ** -4, 1.875 * 2.0 ** -3):   # times 2^-4
+            for every in (1, 128):                             # every term, or one of each block
+                for sign in (0, 0x80):
+                    a = torch.zeros(1, K, dtype=torch.uint8, device="cuda")
+                    b = torch.zeros(1, K, dtype=torch.uint8, device="cuda")
+                    a[0, ::every], b[0, ::every] = code(small) | sign, code(2.0 ** -4)
+                    a[0, where], b[0, where] = code(448.0), code(448.0)
+                    va, vb = a.view(ref.F8["e4m3"]).double(), b.view(ref.F8["e4m3"]).double()
+                    C, S = (va * vb).sum().item(), (va * vb).abs().sum().item()
+                    c = mx.block_gemm(place(a.repeat(M, 1)), one(M), "e4m3", place(b.repeat(N, 1)), one(N), "e4m3",
+                                      out_dtype=torch.float32)
+                    off = (c.double() - C).abs().max().item()
+                    assert off <= sums_bound(K) * S, (where, small, every, sign, off / S * 2 ** 24)
