@@ -431,7 +431,7 @@ mx_status_t mx_block_quantize_dual(const void *x_bf16, int64_t rows, int64_t col
  *                largest, so a block's sum may be off by 2^-8 of its sum of
  *                |terms| in the worst case (2^-11 and less on random data):
  *                below the result's own rounding to bf16 unless the sum cancels
- *                far.  Call with MX_OUT_F32 where that matters.
+ *                far.  Where that matters, MX_OUT_F32 or mx_block_gemm_sums.
  * Products of two scales outside fp32's range are Inf or 0.  A NaN scale makes
  * every element of C that it contributes to NaN; NaN and Inf codes behave as
  * these values.  Fast are operands whose rows are aligned to 16 bytes (any K;
@@ -443,6 +443,21 @@ mx_status_t mx_block_gemm(const void *a_codes, int64_t lda, const float *a_scale
                           const void *b_codes, int64_t ldb, const float *b_scales, int64_t ldsb, mx_format_t fb,
                           int b_tile, int64_t M, int64_t N, int64_t K, void *c, mx_out_t out, int64_t ldc,
                           void *stream);
+
+/*
+ * mx_block_gemm_sums -- mx_block_gemm with the choice of how a block's sum is
+ * formed: MX_SUMS_F32 in fp32, as MX_OUT_F32 has it, for either output (bf16 is
+ * that result rounded once); MX_SUMS_FP8 by the FP8 matrix instruction, as
+ * MX_OUT_BF16 has it (with MX_OUT_F32 it is MX_ERR_INVALID_ARG).
+ */
+typedef enum {
+    MX_SUMS_FP8 = 0, /* a window of 13 bits within 32 products, fp32 from block to block */
+    MX_SUMS_F32 = 1  /* exact products, fp32 sums; half the matrix rate                  */
+} mx_sums_t;
+mx_status_t mx_block_gemm_sums(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa, mx_format_t fa,
+                               const void *b_codes, int64_t ldb, const float *b_scales, int64_t ldsb, mx_format_t fb,
+                               int b_tile, int64_t M, int64_t N, int64_t K, void *c, mx_out_t out, int64_t ldc,
+                               mx_sums_t sums, void *stream);
 
 /*
  * ---------------------------------------------------------------------------

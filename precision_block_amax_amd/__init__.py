@@ -73,13 +73,14 @@ def lib() -> ctypes.CDLL:
         L.mx_block_quantize.argtypes = [P, i64, i64, i64, i32, i32, P, i64, P, i64, P]
         L.mx_block_quantize_dual.argtypes = [P, i64, i64, i64, i32, i32, P, i64, P, i64, i32, P, i64, P, i64, P]
         L.mx_block_gemm.argtypes = [P, i64, P, i64, i32, P, i64, P, i64, i32, i32, i64, i64, i64, P, i32, i64, P]
+        L.mx_block_gemm_sums.argtypes = [P, i64, P, i64, i32, P, i64, P, i64, i32, i32, i64, i64, i64, P, i32, i64, i32, P]
         L.mx_layer_norm.argtypes = [P, i64, i64, i64, P, P, i32, i32, f32, P, i64, P, P, P]
         L.mx_layer_norm_quantize.argtypes = [P, i64, i64, i64, P, P, i32, i32, f32, i32, P, P, P, P, P]
         L.mx_layer_norm_block_quantize.argtypes = [P, i64, i64, i64, P, P, i32, i32, f32, i32, P, i64, P, i64, P, P, P]
         L.mx_layer_norm_backward.argtypes = [P, i64, P, i64, i64, i64, P, i32, i32, P, P, P, i64, P, P, P, i64, P]
         L.mx_layer_norm_backward_workspace.argtypes = [i64, i64]
         L.mx_layer_norm_backward_workspace.restype = i64
-        for fn in (L.mx_block_quantize, L.mx_block_quantize_dual, L.mx_block_gemm, L.mx_layer_norm,
+        for fn in (L.mx_block_quantize, L.mx_block_quantize_dual, L.mx_block_gemm, L.mx_block_gemm_sums, L.mx_layer_norm,
                    L.mx_layer_norm_quantize, L.mx_layer_norm_block_quantize, L.mx_layer_norm_backward):
             fn.restype = ctypes.c_int
         for fn in (L.mx_quantize, L.mx_quantize_transpose, L.mx_hadamard32_quantize, L.mx_quantize_dual,
@@ -468,12 +469,14 @@ def block_quantize_dual(x: torch.Tensor, fmt_row, fmt_t, tile: bool = False, out
 
 
 def block_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_codes: torch.Tensor, b_scales: torch.Tensor, fb,
-               out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+               out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None, stream=None,
+               full_sums: bool = False) -> torch.Tensor:
     """mx_block_gemm: C[M x N] = A[M x K] . B[N x K]^T on block-128 operands as block_quantize
     gives them: A in "row" or "transpose" form (scales [ceil(K/128) x M]), B in one of these or in
     tiles (scales [ceil(K/128) x ceil(N/128)]).  Any sizes; rows may be strided.  float32 output:
     exact products, fp32 sums.  bfloat16 output: the FP8 matrix instruction, whose sums of 32
-    products are good to 2^-13 of the largest (include/mx.h)."""
+    products are good to 2^-13 of the largest (include/mx.h); with full_sums (mx_block_gemm_sums)
+    the float32 result rounded once, at half the matrix rate."""
     f_a, f_b = _fp8(fa), _fp8(fb)
     if a_codes.dim() != 2 or b_codes.dim() != 2 or a_scales.dim() != 2 or b_scales.dim() != 2 or not a_codes.is_cuda:
         raise ValueError("expected 2-D operands on a GPU")
@@ -493,9 +496,11 @@ def block_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_codes: torch
     with _scope(dev, stream):
         if out is None:
             out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        _check(lib().mx_block_gemm(a_codes.data_ptr(), lda, a_scales.data_ptr(), ldsa, f_a, b_codes.data_ptr(), ldb,
-                                   b_scales.data_ptr(), ldsb, f_b, 1 if tile else 0, M, N, K, out.data_ptr(),
-                                   OUT_BF16 if out_dtype is _BF16 else OUT_F32, ldc, _current(dev)))
+        bf16 = out_dtype is _BF16
+        _check(lib().mx_block_gemm_sums(a_codes.data_ptr(), lda, a_scales.data_ptr(), ldsa, f_a, b_codes.data_ptr(), ldb,
+                                        b_scales.data_ptr(), ldsb, f_b, 1 if tile else 0, M, N, K, out.data_ptr(),
+                                        OUT_BF16 if bf16 else OUT_F32, ldc, 1 if full_sums or not bf16 else 0,
+                                        _current(dev)))
     return out
 
 

@@ -120,6 +120,31 @@ mx_status_t norm(const void *x, int64_t rows, int64_t cols, int64_t ldx, const v
     return launched(launch_norm(a, to, fmt, (hipStream_t)stream));
 }
 
+// mx_block_gemm_sums with its enum arguments already read as ints
+mx_status_t block_gemm(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa, int fa,
+                       const void *b_codes, int64_t ldb, const float *b_scales, int64_t ldsb, int fb, int b_tile,
+                       int64_t M, int64_t N, int64_t K, void *c, int out, int64_t ldc, int sums, void *stream) {
+    if (M < 0 || N < 0 || K < 0 || !fp8(fa) || !fp8(fb) || !type_ok(out) || (b_tile != 0 && b_tile != 1))
+        return MX_ERR_INVALID_ARG;
+    if (sums != MX_SUMS_F32 && (sums != MX_SUMS_FP8 || out != MX_OUT_BF16)) return MX_ERR_INVALID_ARG;
+    const int64_t nb = b_tile ? blocks(N) : N;
+    if (lda < K || ldb < K || ldsa < M || ldsb < nb || ldc < N) return MX_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return MX_OK;
+    if (!c || (K > 0 && (!a_codes || !a_scales || !b_codes || !b_scales))) return MX_ERR_INVALID_ARG;
+    const Range r[5] = {rows_at(a_codes, M, lda, K, 1), rows_at(a_scales, blocks(K), ldsa, M, 4),
+                        rows_at(b_codes, N, ldb, K, 1), rows_at(b_scales, blocks(K), ldsb, nb, 4),
+                        rows_at(c, M, ldc, N, out == MX_OUT_BF16 ? 2 : 4)};
+    mx_status_t st = check_ranges(r, 5, 4);
+    if (st != MX_OK) return st;
+    // sizes in 31 bits, K rounded up to whole blocks too; at most 2^22 workgroups of up to 512 threads
+    if (M >= kMaxDim || N >= kMaxDim || K > kMaxDim - kBlk || blocks(M) * blocks(N) >= ((int64_t)1 << 22))
+        return MX_ERR_UNSUPPORTED;
+    if ((st = check_device()) != MX_OK) return st;
+    BlockGemmArgs g{(const uint8_t *)a_codes, (const uint8_t *)b_codes, a_scales, b_scales, c, lda, ldb, ldsa, ldsb, ldc,
+                    (int)M, (int)N, (int)K, out == MX_OUT_BF16, 0, 0};
+    return launched(launch_block_gemm(g, fa, fb, b_tile != 0, sums == MX_SUMS_FP8, (hipStream_t)stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -148,25 +173,17 @@ mx_status_t mx_block_gemm(const void *a_codes, int64_t lda, const float *a_scale
                           const void *b_codes, int64_t ldb, const float *b_scales, int64_t ldsb, mx_format_t fb,
                           int b_tile, int64_t M, int64_t N, int64_t K, void *c, mx_out_t out, int64_t ldc,
                           void *stream) {
-    const int a = raw(fa), b = raw(fb), o = raw(out);
-    if (M < 0 || N < 0 || K < 0 || !fp8(a) || !fp8(b) || !type_ok(o) || (b_tile != 0 && b_tile != 1))
-        return MX_ERR_INVALID_ARG;
-    const int64_t nb = b_tile ? blocks(N) : N;
-    if (lda < K || ldb < K || ldsa < M || ldsb < nb || ldc < N) return MX_ERR_INVALID_ARG;
-    if (M == 0 || N == 0) return MX_OK;
-    if (!c || (K > 0 && (!a_codes || !a_scales || !b_codes || !b_scales))) return MX_ERR_INVALID_ARG;
-    const Range r[5] = {rows_at(a_codes, M, lda, K, 1), rows_at(a_scales, blocks(K), ldsa, M, 4),
-                        rows_at(b_codes, N, ldb, K, 1), rows_at(b_scales, blocks(K), ldsb, nb, 4),
-                        rows_at(c, M, ldc, N, o == MX_OUT_BF16 ? 2 : 4)};
-    mx_status_t st = check_ranges(r, 5, 4);
-    if (st != MX_OK) return st;
-    // sizes in 31 bits, K rounded up to whole blocks too; at most 2^22 workgroups of up to 512 threads
-    if (M >= kMaxDim || N >= kMaxDim || K > kMaxDim - kBlk || blocks(M) * blocks(N) >= ((int64_t)1 << 22))
-        return MX_ERR_UNSUPPORTED;
-    if ((st = check_device()) != MX_OK) return st;
-    BlockGemmArgs g{(const uint8_t *)a_codes, (const uint8_t *)b_codes, a_scales, b_scales, c, lda, ldb, ldsa, ldsb, ldc,
-                    (int)M, (int)N, (int)K, 0, 0};
-    return launched(launch_block_gemm(g, a, b, b_tile != 0, o == MX_OUT_BF16, (hipStream_t)stream));
+    const int o = raw(out);
+    return block_gemm(a_codes, lda, a_scales, ldsa, raw(fa), b_codes, ldb, b_scales, ldsb, raw(fb), b_tile, M, N, K, c,
+                      o, ldc, o == MX_OUT_BF16 ? MX_SUMS_FP8 : MX_SUMS_F32, stream);
+}
+
+mx_status_t mx_block_gemm_sums(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa, mx_format_t fa,
+                               const void *b_codes, int64_t ldb, const float *b_scales, int64_t ldsb, mx_format_t fb,
+                               int b_tile, int64_t M, int64_t N, int64_t K, void *c, mx_out_t out, int64_t ldc,
+                               mx_sums_t sums, void *stream) {
+    return block_gemm(a_codes, lda, a_scales, ldsa, raw(fa), b_codes, ldb, b_scales, ldsb, raw(fb), b_tile, M, N, K, c,
+                      raw(out), ldc, raw(sums), stream);
 }
 
 mx_status_t mx_layer_norm(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx, const void *weight,

@@ -5,19 +5,19 @@
 
 namespace mx {
 
-#define MX_PAIR(fa, fb) hipError_t launch_block_gemm_##fa##_##fb(const BlockGemmArgs &g, bool bt, bool bf16, hipStream_t s);
+#define MX_PAIR(fa, fb) hipError_t launch_block_gemm_##fa##_##fb(const BlockGemmArgs &g, bool bt, bool fp8_sums, hipStream_t s);
 MX_PAIR(0, 0) MX_PAIR(0, 1) MX_PAIR(1, 0) MX_PAIR(1, 1)
 #undef MX_PAIR
 
-hipError_t launch_block_gemm(const BlockGemmArgs &g, int fa, int fb, bool bt, bool bf16_out, hipStream_t s) {
+hipError_t launch_block_gemm(const BlockGemmArgs &g, int fa, int fb, bool bt, bool fp8_sums, hipStream_t s) {
     if (g.K == 0) {
         // 256 elements per workgroup, at most 2^31 of them per launch
         const int64_t rows = ((int64_t)1 << 31) / g.N > 0 ? ((int64_t)1 << 31) / g.N : 1;
         for (int64_t m = 0; m < g.M; m += rows) {
             const int mr = (int)min(rows, (int64_t)g.M - m);
             const dim3 grid((unsigned)(((int64_t)mr * g.N + 255) / 256));
-            uint8_t *c = (uint8_t *)g.c + m * g.ldc * (bf16_out ? 2 : 4);
-            if (bf16_out) hipLaunchKernelGGL((k_zero<true>), grid, dim3(256), 0, s, (void *)c, g.ldc, mr, g.N);
+            uint8_t *c = (uint8_t *)g.c + m * g.ldc * (g.c_bf16 ? 2 : 4);
+            if (g.c_bf16) hipLaunchKernelGGL((k_zero<true>), grid, dim3(256), 0, s, (void *)c, g.ldc, mr, g.N);
             else hipLaunchKernelGGL((k_zero<false>), grid, dim3(256), 0, s, (void *)c, g.ldc, mr, g.N);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
@@ -25,10 +25,10 @@ hipError_t launch_block_gemm(const BlockGemmArgs &g, int fa, int fb, bool bt, bo
         return hipSuccess;
     }
     switch (fa * 2 + fb) {
-    case 0: return launch_block_gemm_0_0(g, bt, bf16_out, s);
-    case 1: return launch_block_gemm_0_1(g, bt, bf16_out, s);
-    case 2: return launch_block_gemm_1_0(g, bt, bf16_out, s);
-    default: return launch_block_gemm_1_1(g, bt, bf16_out, s);
+    case 0: return launch_block_gemm_0_0(g, bt, fp8_sums, s);
+    case 1: return launch_block_gemm_0_1(g, bt, fp8_sums, s);
+    case 2: return launch_block_gemm_1_0(g, bt, fp8_sums, s);
+    default: return launch_block_gemm_1_1(g, bt, fp8_sums, s);
     }
 }
 

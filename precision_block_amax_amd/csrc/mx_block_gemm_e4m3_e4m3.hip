@@ -2,7 +2,7 @@
 #include "mx_block_gemm_kernels.h"
 
 namespace mx {
-hipError_t launch_block_gemm_0_0(const BlockGemmArgs &g, bool bt, bool bf16, hipStream_t s) {
-    return launch_block_gemm_fmt<0, 0>(g, bt, bf16, s);
+hipError_t launch_block_gemm_0_0(const BlockGemmArgs &g, bool bt, bool fp8_sums, hipStream_t s) {
+    return launch_block_gemm_fmt<0, 0>(g, bt, fp8_sums, s);
 }
 }  // namespace mx

@@ -10,17 +10,18 @@
 // holds one row m of C and 16 columns: sa is one value per lane, and with a
 // tiled B so is sa * sb.
 //
-// fp32 output: FP8 codes are converted to fp16 (exact) and multiplied by
+// Sums in fp32 (FP8SUMS = false; C in fp32 or bf16): FP8 codes are converted to fp16 (exact) and multiplied by
 // V_MFMA_F32_32X32X16_F16, whose products are exact and whose sums lose no
 // more than fp32 does (measured: 448 x 448 at any place among 127 equal terms from
 // 2^-9 to 2^-5, a block's sum is off by 10 * 2^-24 of its terms at most, where 127
-// roundings could cost 127).  bf16 output: V_MFMA_F32_32X32X64_F8F6F4 on the
-// codes themselves, twice the rate.  Measured on gfx950, that instruction adds
+// roundings could cost 127).  FP8SUMS (C in bf16): V_MFMA_F32_32X32X64_F8F6F4
+// on the codes themselves, twice the rate.  Measured on gfx950, that instruction adds
 // the products of 32 K in a window ending 2^-13 below the largest (the
 // unscaled FP8 instructions, 32x32x16 and 16x16x32, do the same): at most 31
 // of them lose less than 2^-13 of the largest each, 2^-8 of the block's sum of
 // |terms| at the very worst, 30 times below the output's rounding to bf16 on
-// data without cancellation.
+// data without cancellation.  Both to bf16, FP8 and fp32 sums: 8192 x 6144 x 4096
+// 187 and 367 us, 1000 x 4096 x 28672 157 and 225, 48 x 4096 x 14336 16.0 and 16.9.
 #pragma once
 #include "mx_block_internal.h"
 #include "mx_gemm_kernels.h"
@@ -44,11 +45,11 @@ __device__ __forceinline__ void block_tile_of(const BlockGemmArgs &g, int &tm, i
 }
 
 // four consecutive columns of row m, starting at n
-template <bool BF16OUT>
+template <bool FP8SUMS>
 __device__ __forceinline__ void block_store4(const BlockGemmArgs &g, int m, int n, const float *v) {
     if (m >= g.M) return;
     const int left = g.N - n;
-    if constexpr (BF16OUT) {
+    if (FP8SUMS || g.c_bf16) {
         uint16_t *p = reinterpret_cast<uint16_t *>(g.c) + (int64_t)m * g.ldc + n;
         const uint32_t t[2] = {bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
         if (left >= 4) {
@@ -171,8 +172,8 @@ __device__ __forceinline__ uint4 load16(const uint8_t *p, int n) {
     return v;
 }
 
-template <int FA, int FB, bool BT, bool BF16OUT>
-__global__ __launch_bounds__(GNT, BF16OUT ? 2 : 1) void k_block_gemm(BlockGemmArgs g) {
+template <int FA, int FB, bool BT, bool FP8SUMS>
+__global__ __launch_bounds__(GNT, FP8SUMS ? 2 : 1) void k_block_gemm(BlockGemmArgs g) {
     __shared__ __attribute__((aligned(16))) uint8_t sA[2][GB * kBlk], sB[2][GB * kBlk];
     __shared__ __attribute__((aligned(16))) float sS[2][2 * GB];  // A's rows, B's rows
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -229,14 +230,14 @@ __global__ __launch_bounds__(GNT, BF16OUT ? 2 : 1) void k_block_gemm(BlockGemmAr
         static_for<0, 2>([&](auto jj) {
             constexpr int j = decltype(jj)::value;
             fb[j] = read_frag(sB[b], wn * 64 + j * 32 + l32, h);
-            if constexpr (!BF16OUT) gb[j] = to_f16<FB>(fb[j]);
+            if constexpr (!FP8SUMS) gb[j] = to_f16<FB>(fb[j]);
         });
         static_for<0, 4>([&](auto tt) {
             constexpr int i = decltype(tt)::value / 2, j = decltype(tt)::value % 2;
             const Frag fa = read_frag(sA[b], wm * 64 + i * 32 + l32, h);
             const float sa = ss[wm * 64 + i * 32 + l32];
             v16f p;
-            if constexpr (BF16OUT) p = block_fp8<FA, FB>(fa, fb[j]);
+            if constexpr (FP8SUMS) p = block_fp8<FA, FB>(fa, fb[j]);
             else p = block_f16(to_f16<FA>(fa), gb[j]);
             if constexpr (BT) {
                 const float s = sa * ss[GB + wn * 64];
@@ -262,7 +263,7 @@ __global__ __launch_bounds__(GNT, BF16OUT ? 2 : 1) void k_block_gemm(BlockGemmAr
         for (int j = 0; j < 2; j++)
 #pragma unroll
             for (int q = 0; q < 4; q++)
-                block_store4<BF16OUT>(g, m0 + wm * 64 + i * 32 + l32, n0 + wn * 64 + j * 32 + 8 * q + 4 * h, &acc[i][j][4 * q]);
+                block_store4<FP8SUMS>(g, m0 + wm * 64 + i * 32 + l32, n0 + wn * 64 + j * 32 + 8 * q + 4 * h, &acc[i][j][4 * q]);
 }
 
 // ---------------------------------------------------------------------------
@@ -273,7 +274,7 @@ __global__ __launch_bounds__(GNT, BF16OUT ? 2 : 1) void k_block_gemm(BlockGemmAr
 // one another so that the matrix pipe never waits for the vector one: tile t's
 // instructions go out, and while they run, tile t - 1's sum is added to its
 // accumulators (16 multiply-adds, 64 clocks beside 128 of FP8 matrix work) and
-// the next row of A fragments is read from LDS (and, for fp32 output,
+// the next row of A fragments is read from LDS (and, for fp32 sums,
 // converted).  The last tile's sum is added in the next stage.
 //
 // 8192 x 6144 x 4096 to bf16, 256 x 256 tiles: 187 us, 2.2 PFLOP/s, the matrix
@@ -306,7 +307,7 @@ struct Cfg128x128Far : Cfg128x128 { static constexpr bool PF = true; };
 
 // RAG: K ends inside a chunk of 16 bytes.  The stages leave that chunk out, and its products are added after them
 // from registers (a branch for it in the loop made the compiler spill: up to 200 registers).
-template <int FA, int FB, bool BT, bool BF16OUT, class CFG, bool RAG>
+template <int FA, int FB, bool BT, bool FP8SUMS, class CFG, bool RAG>
 __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN * CFG::KG / 4) void k_block_gemm_pipe(BlockGemmArgs g) {
     constexpr int TI = CFG::TI, WM = CFG::WM, WN = CFG::WN, NS = 2, KG = CFG::KG;
     static_assert(KG == 1 || (KG == 2 && TI == 2), "the join swaps two rows of tiles");
@@ -467,10 +468,10 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
 
     // EARLY: a stage begins with its first fragments in registers.  All its LDS reads are out before its
     // last two tiles, so the next stage arrives there: the barrier, the loads' issue and the next stage's
-    // first reads fall into those tiles' matrix work instead of standing between two stages.  fp32 output,
-    // 6144 x 4096 x 8192: 400 -> 381 us.  bf16 output has no registers left for it in 256 x 256 tiles (13
-    // spilled: 187 -> 210 us) and gains nothing in 128 x 128 (47.7, 48.9 us).
-    constexpr bool EARLY = !BF16OUT;
+    // first reads fall into those tiles' matrix work instead of standing between two stages.  fp32 sums,
+    // 6144 x 4096 x 8192: 400 -> 381 us.  FP8 sums have no registers left for it in 256 x 256 tiles (13
+    // spilled: 187 -> 210 us) and gain nothing in 128 x 128 (47.7, 48.9 us).
+    constexpr bool EARLY = !FP8SUMS;
     Frag fa[2], fb[2];
     const auto stage = [&](int u, int it) {
         const float *const ss = sS + (it & (SR - 1)) * (PM + PN);
@@ -486,7 +487,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
 #pragma unroll
         for (int i = 0; i < TI; i++) sa[i] = ss[wm * TI * 32 + i * 32 + l32];
         const float sbt = BT ? ss[scol] : 1.0f;
-        if constexpr (!BF16OUT) {
+        if constexpr (!FP8SUMS) {
             ga = to_f16<FA>(fa[0]);
 #pragma unroll
             for (int j = 0; j < 2; j++) gb[j] = to_f16<FB>(fb[j]);
@@ -504,11 +505,11 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
             float4 sb[4];
             read_sb(sb);
             v16f p;
-            if constexpr (BF16OUT) p = block_fp8<FA, FB>(fa[i & 1], fb[j]);
+            if constexpr (FP8SUMS) p = block_fp8<FA, FB>(fa[i & 1], fb[j]);
             else p = block_f16(ga, gb[j]);
             __builtin_amdgcn_sched_barrier(0);
             promote(acc[pi][pj], sb);
-            if constexpr (!BF16OUT && j == 1 && i + 1 < TI) ga = to_f16<FA>(fa[(i + 1) & 1]);
+            if constexpr (!FP8SUMS && j == 1 && i + 1 < TI) ga = to_f16<FA>(fa[(i + 1) & 1]);
             pp = p;
             ps = BT ? sa[i] * sbt : sa[i];
             psb = ss + scol + j * 32;
@@ -566,7 +567,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
                     __builtin_amdgcn_sched_barrier(0);  // one tile at a time
                     const uint4 a = keep_bytes(ca[i], left);
                     v16f p = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    if constexpr (BF16OUT) {
+                    if constexpr (FP8SUMS) {
                         p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                             v8i{(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0},
                             v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0}, p, FB, FA, 0, 0, 0, 0);
@@ -605,7 +606,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
 
     // C through LDS, each wave its own part, TI2 x 32 rows at a time, so that rows leave as runs of 64
     // elements; 16-byte chunks are XOR-swizzled by the row
-    constexpr int ESZ = BF16OUT ? 2 : 4, ROWB = 64 * ESZ, CPR = ROWB / 16, REG = NS * ST / NW;
+    constexpr int ESZ = FP8SUMS ? 2 : 4, ROWB = 64 * ESZ, CPR = ROWB / 16, REG = NS * ST / NW;
     constexpr int TI2 = TK * 32 * ROWB <= REG ? TK : TK / 2;
     static_assert(TI2 >= 1 && TK % TI2 == 0 && TI2 * 32 * ROWB <= REG, "staging");
     uint8_t *const reg = sC + wave * REG;
@@ -621,7 +622,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
                     const float *v = &acc[pass * TI2 + ii][j][4 * q];
-                    if constexpr (BF16OUT)
+                    if constexpr (FP8SUMS)
                         *reinterpret_cast<uint2 *>(&reg[m * ROWB + (((4 * j + q) ^ (m & 7)) << 4) + 8 * h]) =
                             make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
                     else
@@ -635,18 +636,32 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
             const uint4 t = *reinterpret_cast<const uint4 *>(&reg[m * ROWB + ((c ^ (m & (CPR - 1))) << 4)]);
             const int gm = mbase + pass * TI2 * 32 + m, gn = nbase + c * (16 / ESZ);
             if (gm >= g.M) continue;
-            uint8_t *const d = reinterpret_cast<uint8_t *>(g.c) + ((int64_t)gm * g.ldc + gn) * ESZ;
-            if (vec) {
-                typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-                __builtin_nontemporal_store(u32x4{t.x, t.y, t.z, t.w}, reinterpret_cast<u32x4 *>(d));
-            } else {
+            const int64_t at = (int64_t)gm * g.ldc + gn;
+            typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+            typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+            if (FP8SUMS || !g.c_bf16) {
+                uint8_t *const d = reinterpret_cast<uint8_t *>(g.c) + at * ESZ;
+                if (vec) {
+                    __builtin_nontemporal_store(u32x4{t.x, t.y, t.z, t.w}, reinterpret_cast<u32x4 *>(d));
+                    continue;
+                }
                 const uint32_t w4[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
                 for (int e = 0; e < 16 / ESZ; e++) {
                     if (gn + e >= g.N) break;
-                    if constexpr (BF16OUT) reinterpret_cast<uint16_t *>(d)[e] = (uint16_t)(w4[e >> 1] >> (16 * (e & 1)));
+                    if constexpr (FP8SUMS) reinterpret_cast<uint16_t *>(d)[e] = (uint16_t)(w4[e >> 1] >> (16 * (e & 1)));
                     else reinterpret_cast<uint32_t *>(d)[e] = w4[e];
                 }
+            } else {  // four sums, rounded to bf16 here
+                uint16_t *const d = reinterpret_cast<uint16_t *>(g.c) + at;
+                const u32x2 b = {bf16x2(__uint_as_float(t.x), __uint_as_float(t.y)), bf16x2(__uint_as_float(t.z), __uint_as_float(t.w))};
+                if (vec) {
+                    __builtin_nontemporal_store(b, reinterpret_cast<u32x2 *>(d));
+                    continue;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (gn + e < g.N) d[e] = (uint16_t)(b[e >> 1] >> (16 * (e & 1)));
             }
         }
     }
@@ -671,11 +686,11 @@ struct Frag2 {
     uint4 c[2];
 };
 
-template <int FA, int FB, bool BF16OUT>
+template <int FA, int FB, bool FP8SUMS>
 __device__ __forceinline__ v4f few_block(const Frag2 &a, const Frag2 &b) {
     v4f p = {0.f, 0.f, 0.f, 0.f};
     const uint4 x = a.c[0], y = a.c[1], u = b.c[0], v = b.c[1];
-    if constexpr (BF16OUT) {
+    if constexpr (FP8SUMS) {
         p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
             v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)v.x, (int)v.y, (int)v.z, (int)v.w},
             v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w}, p, FB, FA, 0, 0, 0, 0);
@@ -690,7 +705,7 @@ __device__ __forceinline__ v4f few_block(const Frag2 &a, const Frag2 &b) {
 
 // AI: loads of 8 rows of A; with an odd AI the rest of the matrix instruction's 16 rows is whatever LDS
 // holds, and reaches only rows of C that do not exist
-template <int FA, int FB, bool BT, bool BF16OUT, int AI, int NT, int S>
+template <int FA, int FB, bool BT, bool FP8SUMS, int AI, int NT, int S>
 __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(BlockGemmArgs g) {
     constexpr int MT = (AI + 1) / 2, DM = 16 * MT, DN = 16 * NT, JP = DN + 4;
     constexpr int OB = MT * 2048, OS = OB + NT * 2048, BLK = OS + 512;  // a block: A's rows, B's, scales of A, of B
@@ -797,7 +812,7 @@ __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(BlockGemmArgs g) {
         for (int t = 0; t < MT; t++)
 #pragma unroll
             for (int j = 0; j < NT; j++) {
-                const v4f p = few_block<FA, FB, BF16OUT>(fa[t], fb[j]);
+                const v4f p = few_block<FA, FB, FP8SUMS>(fa[t], fb[j]);
 #pragma unroll
                 for (int r = 0; r < 4; r++) acc[t][j][r] = __builtin_fmaf(p[r], sa[t] * sb[j][BT ? 0 : r], acc[t][j][r]);
             }
@@ -825,37 +840,37 @@ __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(BlockGemmArgs g) {
             v[2] += x.z;
             v[3] += x.w;
         }
-        if (m < 8 * AI) block_store4<BF16OUT>(g, m0 + m, n0 + n, v);
+        if (m < 8 * AI) block_store4<FP8SUMS>(g, m0 + m, n0 + n, v);
     }
 }
 
-template <int FA, int FB, bool BT, bool BF16OUT, int AI, int NT, int S>
+template <int FA, int FB, bool BT, bool FP8SUMS, int AI, int NT, int S>
 hipError_t launch_block_gemm_few(BlockGemmArgs g, hipStream_t s) {
     g.tiles_m = (g.M + 8 * AI - 1) / (8 * AI);
     g.tiles_n = (g.N + 16 * NT - 1) / (16 * NT);
-    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, BT, BF16OUT, AI, NT, S>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
+    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, BT, FP8SUMS, AI, NT, S>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
                        dim3(64 * DW), 0, s, g);
     return hipGetLastError();
 }
 
-template <int FA, int FB, bool BT, bool BF16OUT, class CFG, bool RAG>
+template <int FA, int FB, bool BT, bool FP8SUMS, class CFG, bool RAG>
 hipError_t launch_block_gemm_pipe(BlockGemmArgs g, hipStream_t s) {
     constexpr int PM = CFG::WM * CFG::TI * 32, PN = CFG::WN * 64;
     g.tiles_m = (g.M + PM - 1) / PM;
     g.tiles_n = (g.N + PN - 1) / PN;
-    hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, BF16OUT, CFG, RAG>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
+    hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, FP8SUMS, CFG, RAG>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
                        dim3(64 * CFG::WM * CFG::WN * CFG::KG), 0, s, g);
     return hipGetLastError();
 }
 
-template <int FA, int FB, bool BT, bool BF16OUT, class CFG>
+template <int FA, int FB, bool BT, bool FP8SUMS, class CFG>
 hipError_t launch_block_gemm_k(const BlockGemmArgs &g, hipStream_t s) {
-    return g.K % 16 ? launch_block_gemm_pipe<FA, FB, BT, BF16OUT, CFG, true>(g, s)
-                    : launch_block_gemm_pipe<FA, FB, BT, BF16OUT, CFG, false>(g, s);
+    return g.K % 16 ? launch_block_gemm_pipe<FA, FB, BT, FP8SUMS, CFG, true>(g, s)
+                    : launch_block_gemm_pipe<FA, FB, BT, FP8SUMS, CFG, false>(g, s);
 }
 
-// The kernel for a product.  us measured on an MI355X, N = 4096 and bf16 output where not said otherwise.
-template <int FA, int FB, bool BT, bool BF16OUT>
+// The kernel for a product.  us measured on an MI355X, N = 4096 and FP8 sums where not said otherwise.
+template <int FA, int FB, bool BT, bool FP8SUMS>
 hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
     // All but the general kernel load straight to LDS: rows of whole aligned 16 bytes, offsets in 31 bits.
     if (g.M == 1) g.lda = (g.K + 15) / 16 * 16;  // a single row has no stride
@@ -867,46 +882,46 @@ hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
     const auto general = [&]() {
         g.tiles_m = (g.M + GB - 1) / GB;
         g.tiles_n = (g.N + GB - 1) / GB;
-        hipLaunchKernelGGL((k_block_gemm<FA, FB, BT, BF16OUT>), dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(GNT), 0, s, g);
+        hipLaunchKernelGGL((k_block_gemm<FA, FB, BT, FP8SUMS>), dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(GNT), 0, s, g);
         return hipGetLastError();
     };
     if (!aligned) return general();
     const auto tiles = [&](int64_t m, int64_t n) { return (g.M + m - 1) / m * ((g.N + n - 1) / n); };
     const int64_t wide = (int64_t)1 << 26;  // columns from which 16 of them per workgroup would be 2^31 threads
-    if (g.M <= 8 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 1, 1, 2>(g, s);
-    if (g.M <= 16 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 2, 1, 2>(g, s);
-    if (g.M <= 32 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 4, 1, 3>(g, s);
-    if (g.M <= 48 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 6, 1, 2>(g, s);
+    if (g.M <= 8 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 1, 1, 2>(g, s);
+    if (g.M <= 16 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 2, 1, 2>(g, s);
+    if (g.M <= 32 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 4, 1, 3>(g, s);
+    if (g.M <= 48 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 6, 1, 2>(g, s);
     // 64 rows: 32 columns per workgroup read A half as often, 16 make twice the workgroups: 42 against 55 at
     // N = 28672, K = 4096 (896 workgroups), 20 against 18 at K = 14336 (128)
-    if (g.M <= 64 && tiles(64, 32) < 256) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 8, 1, 1>(g, s);
+    if (g.M <= 64 && tiles(64, 32) < 256) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 8, 1, 1>(g, s);
     // Up to two rounds of 64 x 32 tiles on the 256 CUs (the 128 x 128 tiles are then 64 at most): K = 14336, one
     // round (M = 128) 21 against 64, two (256) 38 against 63; K = 4096, two 15 against 21, four (512) 27
-    // against 21.  float32: one 24 against 36, two 32 against 36, four 48 against 38.
-    if ((g.M <= 64 && g.N < wide) || tiles(64, 32) <= 512) return launch_block_gemm_few<FA, FB, BT, BF16OUT, 8, 2, 1>(g, s);
+    // against 21.  fp32 sums: one 24 against 36, two 32 against 36, four 48 against 38.
+    if ((g.M <= 64 && g.N < wide) || tiles(64, 32) <= 512) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 8, 2, 1>(g, s);
     if (g.K < 16) return general();  // no whole chunk for a stage
     const int64_t r128 = (tiles(128, 128) + 255) / 256;
-    if constexpr (BF16OUT && BT) {
+    if constexpr (FP8SUMS && BT) {
         // a round of 256 x 256 tiles takes 1.75 us per 128 K, one of 128 x 128 tiles 0.70
         const int64_t r256 = (tiles(256, 256) + 255) / 256;
-        if (5 * r256 <= 2 * r128) return launch_block_gemm_k<FA, FB, BT, BF16OUT, Cfg256x256>(g, s);
+        if (5 * r256 <= 2 * r128) return launch_block_gemm_k<FA, FB, BT, FP8SUMS, Cfg256x256>(g, s);
         // long rows, every CU busy: 1000 rows, K = 28672 184 without and 157 with the prefetch; 14336 79 and 75;
         // 8192 43 and 45
         if (g.K >= 12288 && tiles(128, 128) >= 256)
-            return launch_block_gemm_k<FA, FB, BT, BF16OUT, Cfg128x128Far>(g, s);
+            return launch_block_gemm_k<FA, FB, BT, FP8SUMS, Cfg128x128Far>(g, s);
     } else {
-        // (with fp32 output or B's scales by column 256 x 256 tiles need more registers than there are)
+        // (with fp32 sums or B's scales by column 256 x 256 tiles need more registers than there are)
         // a round of 256 x 128 tiles takes 2.0 us per 128 K (fp32), one of 128 x 128 tiles 1.05
         const int64_t r256 = (tiles(256, 128) + 255) / 256;
-        if (2 * r256 <= r128) return launch_block_gemm_k<FA, FB, BT, BF16OUT, Cfg256x128>(g, s);
+        if (2 * r256 <= r128) return launch_block_gemm_k<FA, FB, BT, FP8SUMS, Cfg256x128>(g, s);
     }
-    return launch_block_gemm_k<FA, FB, BT, BF16OUT, Cfg128x128>(g, s);
+    return launch_block_gemm_k<FA, FB, BT, FP8SUMS, Cfg128x128>(g, s);
 }
 
 template <int FA, int FB>
-hipError_t launch_block_gemm_fmt(const BlockGemmArgs &g, bool bt, bool bf16, hipStream_t s) {
-    if (bt) return bf16 ? launch_block_gemm_as<FA, FB, true, true>(g, s) : launch_block_gemm_as<FA, FB, true, false>(g, s);
-    return bf16 ? launch_block_gemm_as<FA, FB, false, true>(g, s) : launch_block_gemm_as<FA, FB, false, false>(g, s);
+hipError_t launch_block_gemm_fmt(const BlockGemmArgs &g, bool bt, bool fp8_sums, hipStream_t s) {
+    if (bt) return fp8_sums ? launch_block_gemm_as<FA, FB, true, true>(g, s) : launch_block_gemm_as<FA, FB, true, false>(g, s);
+    return fp8_sums ? launch_block_gemm_as<FA, FB, false, true>(g, s) : launch_block_gemm_as<FA, FB, false, false>(g, s);
 }
 
 }  // namespace

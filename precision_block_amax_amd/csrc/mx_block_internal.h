@@ -30,11 +30,12 @@ struct BlockGemmArgs {
     void *c;
     int64_t lda, ldb, ldsa, ldsb, ldc;
     int M, N, K;
+    bool c_bf16;
     int tiles_m, tiles_n;
 };
 
-// M, N > 0; K == 0 clears C
-hipError_t launch_block_gemm(const BlockGemmArgs &g, int fa, int fb, bool b_tile, bool bf16_out, hipStream_t stream);
+// M, N > 0; K == 0 clears C.  fp8_sums: blocks' sums by the FP8 instruction (C in bf16 only), else in fp32
+hipError_t launch_block_gemm(const BlockGemmArgs &g, int fa, int fb, bool b_tile, bool fp8_sums, hipStream_t stream);
 
 struct NormArgs {
     const uint16_t *x;

@@ -47,3 +47,16 @@ def test_interleaved_rows_of_different_counts_are_counted_whole(L):
     args = lambda ld, rows: [P(0x100000000), rows, 64, ld, None, None, BF16, 0, 1e-5, None, 64, None, None, None]
     assert L.mx_layer_norm(*args(1 << 62, 3)) == INVALID
     assert L.mx_layer_norm(*args(1 << 62, 0)) == OK
+
+
+def test_block_gemm_sums_rejects(L):
+    args = lambda **k: [P(0x100000000), 208, P(0x200000000), 70, k.get("fa", E4M3), P(0x300000000), 208, P(0x400000000), 300, E4M3,
+                        k.get("tile", 0), k.get("M", 70), 300, k.get("K", 200), P(k.get("c", 0x500000000)), k.get("out", BF16), 300,
+                        k.get("sums", 1), None]
+    f = L.mx_block_gemm_sums
+    for bad in (dict(sums=2), dict(sums=-1), dict(sums=0, out=F32), dict(sums=1, out=2), dict(sums=0, out=3), dict(fa=2), dict(tile=2),
+                dict(M=-1), dict(c=0x100000000)):
+        assert f(*args(**bad)) == INVALID, bad
+    for sums, out in ((0, BF16), (1, BF16), (1, F32)):
+        assert f(*args(sums=sums, out=out, M=0)) == OK
+        assert f(*args(sums=sums, out=out, K=(1 << 31) - 1)) != OK
