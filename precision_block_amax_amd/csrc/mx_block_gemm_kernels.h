@@ -892,9 +892,10 @@ hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
     if (g.M <= 16 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 2, 1, 2>(g, s);
     if (g.M <= 32 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 4, 1, 3>(g, s);
     if (g.M <= 48 && g.N < wide) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 6, 1, 2>(g, s);
-    // 64 rows: 32 columns per workgroup read A half as often, 16 make twice the workgroups: 42 against 55 at
-    // N = 28672, K = 4096 (896 workgroups), 20 against 18 at K = 14336 (128)
-    if (g.M <= 64 && tiles(64, 32) < 256) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 8, 1, 1>(g, s);
+    // 64 rows: 32 columns per workgroup read A half as often, 16 make twice the workgroups, one per CU either way.  16
+    // while that is one round: K = 14336, N = 4096 (256 workgroups of 16) 25.7 against 30; K = 4096, N = 6144 (384) 13.8
+    // against 9.6, 8192 (512) 16.7 against 12, 28672 (1792) 56 against 44.
+    if (g.M <= 64 && tiles(64, 16) <= 256) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 8, 1, 1>(g, s);
     // Up to two rounds of 64 x 32 tiles on the 256 CUs (the 128 x 128 tiles are then 64 at most): K = 14336, one
     // round (M = 128) 21 against 64, two (256) 38 against 63; K = 4096, two 15 against 21, four (512) 27
     // against 21.  fp32 sums: one 24 against 36, two 32 against 36, four 48 against 38.
