@@ -277,7 +277,7 @@ __global__ __launch_bounds__(GNT, FP8SUMS ? 2 : 1) void k_block_gemm(BlockGemmAr
 // the next row of A fragments is read from LDS (and, for fp32 sums,
 // converted).  The last tile's sum is added in the next stage.
 //
-// 8192 x 6144 x 4096 to bf16, 256 x 256 tiles: 187 us, 2.2 PFLOP/s, the matrix
+// 8192 x 6144 x 4096 with FP8 sums, 256 x 256 tiles: 187 us, 2.2 PFLOP/s, the matrix
 // pipe busy 55% of the time at 1.9 GHz; without the loads 140, without the sums'
 // additions 171, without the matrix instructions 120, so no one of them bounds
 // it.  6144 x 4096 x 8192 to fp32, 256 x 128 tiles: 395 us, 1.04 PFLOP/s, bound by
@@ -306,7 +306,9 @@ struct Cfg128x128 { static constexpr int TI = 2, WM = 2, WN = 2, KG = 2; static 
 struct Cfg128x128Far : Cfg128x128 { static constexpr bool PF = true; };
 
 // RAG: K ends inside a chunk of 16 bytes.  The stages leave that chunk out, and its products are added after them
-// from registers (a branch for it in the loop made the compiler spill: up to 200 registers).
+// from registers (a branch for it in the loop made the compiler spill: up to 200 registers).  256 x 256 tiles spill
+// 48 registers there, 24 instructions after the loop and none in it: 8192 x 6144 x 4095 to bf16 217 us beside 194 of
+// 4096; 4104 238, rows of 4112 bytes, whose 128 of a stage lie in two lines.
 template <int FA, int FB, bool BT, bool FP8SUMS, class CFG, bool RAG>
 __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN * CFG::KG / 4) void k_block_gemm_pipe(BlockGemmArgs g) {
     constexpr int TI = CFG::TI, WM = CFG::WM, WN = CFG::WN, NS = 2, KG = CFG::KG;
@@ -373,9 +375,11 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     // the last-level cache then open a DRAM page for every one of them, and a stage's loads wait for its
     // slowest.  One wave of either group fetches a word of every line of whole KiB of rows, the next KiB of
     // K, a few rows per stage: the first group A's rows, the second B's.  The 32 tiles that an XCD works on
-    // are 8 x 4 (block_tile_of), so a workgroup takes a quarter of its A rows and an eighth of its B rows.
-    // 1000 x 4096 x 28672: 184 us without, 157 with; two or four KiB ahead 166, 168; a line per row and
-    // stage, three stages ahead, 168.
+    // are 8 x 4 (block_tile_of), so a workgroup takes a quarter of its A rows and an eighth of its B rows; with
+    // fewer than eight rows of tiles the eighths of B that would be theirs are not fetched ahead.
+    // Operands from HBM, without and with: 1000 x 4096 x 28672 180 and 155 us, 512 x 8192 x 28672 (four rows of
+    // tiles) 188 and 177, 256 x 16384 x 28672 (two) 200 and 193.  1000 rows, two or four KiB ahead 166, 168; a line
+    // per row and stage, three stages ahead, 168.
     static_assert(!PF || KG == 2, "a group for each operand");
     constexpr int PW = 8 / KG;  // stages of a group per KiB
     const bool pw = PF && wave == 0;
@@ -869,7 +873,8 @@ hipError_t launch_block_gemm_k(const BlockGemmArgs &g, hipStream_t s) {
                     : launch_block_gemm_pipe<FA, FB, BT, FP8SUMS, CFG, false>(g, s);
 }
 
-// The kernel for a product.  us measured on an MI355X, N = 4096 and FP8 sums where not said otherwise.
+// The kernel for a product.  us measured on an MI355X, N = 4096 and FP8 sums where not said otherwise, operands taking
+// turns beyond what the last-level cache holds.
 template <int FA, int FB, bool BT, bool FP8SUMS>
 hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
     // All but the general kernel load straight to LDS: rows of whole aligned 16 bytes, offsets in 31 bits.
@@ -897,8 +902,8 @@ hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
     // against 9.6, 8192 (512) 16.7 against 12, 28672 (1792) 56 against 44.
     if (g.M <= 64 && tiles(64, 16) <= 256) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 8, 1, 1>(g, s);
     // Up to two rounds of 64 x 32 tiles on the 256 CUs (the 128 x 128 tiles are then 64 at most): K = 14336, one
-    // round (M = 128) 21 against 64, two (256) 38 against 63; K = 4096, two 15 against 21, four (512) 27
-    // against 21.  fp32 sums: one 24 against 36, two 32 against 36, four 48 against 38.
+    // round (M = 128) 30 against 92, two (256) 49 against 90; K = 4096, one 9.2 against 19.6, two 16.6 against 20,
+    // four (512) 30 against 20.5.  fp32 sums, K = 4096: one 10.6 against 31, two 19 against 31, four 34 against 32.
     if ((g.M <= 64 && g.N < wide) || tiles(64, 32) <= 512) return launch_block_gemm_few<FA, FB, BT, FP8SUMS, 8, 2, 1>(g, s);
     if (g.K < 16) return general();  // no whole chunk for a stage
     const int64_t r128 = (tiles(128, 128) + 255) / 256;
@@ -906,13 +911,16 @@ hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
         // a round of 256 x 256 tiles takes 1.75 us per 128 K, one of 128 x 128 tiles 0.70
         const int64_t r256 = (tiles(256, 256) + 255) / 256;
         if (5 * r256 <= 2 * r128) return launch_block_gemm_k<FA, FB, BT, FP8SUMS, Cfg256x256>(g, s);
-        // long rows, every CU busy: 1000 rows, K = 28672 184 without and 157 with the prefetch; 14336 79 and 75;
-        // 8192 43 and 45
+        // long rows, every CU busy: 1000 rows, operands from HBM, K = 28672 180 without and 155 with the prefetch;
+        // 14336 91 and 82; 12288 81 and 76; 8192 43 and 45.  (Operands that the last-level cache holds: 14336 72
+        // and 78.)
         if (g.K >= 12288 && tiles(128, 128) >= 256)
             return launch_block_gemm_k<FA, FB, BT, FP8SUMS, Cfg128x128Far>(g, s);
     } else {
         // (with fp32 sums or B's scales by column 256 x 256 tiles need more registers than there are)
-        // a round of 256 x 128 tiles takes 2.0 us per 128 K (fp32), one of 128 x 128 tiles 1.05
+        // a round of 256 x 128 tiles takes 2.0 us per 128 K (fp32 sums), one of 128 x 128 tiles 1.05; FP8 sums, B's
+        // scales by column: 1.3 and 0.70 (6144 x 4096 x 8192 in 3 rounds 249, in 6 of 128 x 128 tiles 271; 1536 x
+        // 4096 x 4096 in one 44, in two 50; 1024 x 4096 x 4096 in one of either 38 and 29)
         const int64_t r256 = (tiles(256, 128) + 255) / 256;
         if (2 * r256 <= r128) return launch_block_gemm_k<FA, FB, BT, FP8SUMS, Cfg256x128>(g, s);
     }

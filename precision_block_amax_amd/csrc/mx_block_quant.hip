@@ -14,10 +14,12 @@
 // reduction dimension's blocks are their outer dimension.
 //
 // Bound by memory: 2 bytes read and 1 byte (and 1/32) written per element and
-// form.  Measured over inputs that take turns: 28672 x 4096 in tiles, both forms
-// (470 MB) 74 us, 6.4 TB/s; 8192 x 4096 by rows (102 MB) 18 us, 5.6 TB/s; 1000 x
-// 6144, both forms (25 MB, 384 workgroups) 10.3 us, of which launch, one read's
-// latency, two barriers and the stores, one after the other, are the most.
+// form.  Measured over inputs and outputs that take turns: 28672 x 4096 in tiles,
+// both forms (470 MB) 92 us, 5.1 TB/s as a large copy (75 where the outputs go
+// over the same memory call after call, which the last-level cache then holds);
+// 8192 x 4096 by rows (102 MB) 21 us (18.6 over the same outputs); 1000 x 6144, both
+// forms (25 MB, 384 workgroups) 10.4 us, of which launch, one read's latency, two
+// barriers and the stores, one after the other, are the most.
 #include "mx_block_util.h"
 
 namespace mx {
@@ -190,8 +192,9 @@ hipError_t launch_forms(const uint16_t *x, int64_t rows, int64_t cols, int64_t l
     const dim3 grid(tc * trn), block(kQT);
     const FastDiv d(tc);
     // Input larger than half of the 256 MB last-level cache is read past it: less of it would be found there
-    // than it pushes out.  28672 x 4096 in tiles, both forms: 91 us through the cache, 81 past it; but
-    // 8192 x 4096 (67 MB, partly still cached), one form: 20 and 24.
+    // than it pushes out.  Through the cache and past it, with outputs over the same memory call after call:
+    // 28672 x 4096 in tiles, both forms 91 and 75 us, 8192 x 4096 (67 MB, partly still cached), one form 18.6 and
+    // 20.0; with outputs in turn 92 either way, and 21.3 and 20.0.
     const bool whole = cols % 8 == 0, nt = whole && rows * cols > (int64_t)1 << 26;
 #define MX_Q(fr, ft, row, tr)                                                                                             \
     do {                                                                                                                  \

@@ -20,11 +20,16 @@
 // Bound by memory: 2 bytes read and 2 (1 for FP8) written per element forward,
 // 4 read and 2 written backward; to FP8 the vector units, busy half of the time,
 // and the two barriers per row come next.
-// Measured: 8192 x 4096 to bf16 (134 MB) 25.8 us, 5.2 TB/s, to FP8 (102 MB) 22.8
-// us, 4.5 TB/s; backward (201 MB) 47.4 us, 43 of them the first kernel's; 1001 x
-// 8192 backward (49 MB) 18.8 us: 2 rows at a time in a workgroup leave two or
-// three latencies in a row, and the chunks' sums are a third of the bytes again.
-// One row of 4096: 4 us, launch and latency.
+// Measured with outputs over the same memory call after call: 8192 x 4096 to bf16
+// (134 MB) 25.7 us, 5.2 TB/s, to FP8 (102 MB) 23.4 us, 4.4 TB/s; backward (201 MB)
+// 47.8 us, 43 of them the first kernel's (outputs in turn, so that nothing stays in
+// the last-level cache: 29.6, 27.6, 51.3; to MX E4M3 25.0, E2M1 (85 MB) 19.5);
+// without the parameters' sums 42.7.  1001 x 8192 backward (49 MB) 18.8 us: 2 rows
+// at a time in a workgroup leave two or three latencies in a row, and the chunks'
+// sums are a third of the bytes again.  2048 x 32768 to FP8 (203 MB) 73 us: four
+// vectors per thread leave no registers for the next row; backward (403 MB) 189:
+// the parameters' kernel reads x and dy a second time.  One row of 4096: 4 us,
+// launch and latency.
 #include <type_traits>
 
 #include "mx_block_util.h"
@@ -33,8 +38,9 @@ namespace mx {
 namespace {
 
 // bf16 input larger than half of the 256 MB last-level cache is read past it: less of it would be found there
-// than it pushes out.  32768 x 4096: to bf16 117 us through the cache, 90 past it, backward 168 and 145; but
-// 8192 x 4096 (67 MB, partly still cached) 27 and 32.
+// than it pushes out.  Through the cache and past it, with outputs over the same memory call after call: 32768 x 4096
+// to bf16 115 and 89 us, backward 169 and 140, 8192 x 4096 (67 MB, partly still cached) to bf16 25.7 and 28.2; with
+// outputs in turn 114 and 118, 169 and 160, 29.9 and 28.4.
 bool past_cache(int64_t rows, int64_t cols) { return rows * cols > (int64_t)1 << 26; }
 
 // sum over the wave, in every lane: within rows of 16 lanes by DPP (neighbours, pairs, mirrored halves,
