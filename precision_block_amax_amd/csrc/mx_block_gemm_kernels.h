@@ -29,21 +29,6 @@
 namespace mx {
 namespace {
 
-// XCD-aware tile order (as tile_of): consecutive workgroups go to the 8 XCDs in
-// turn, so each XCD gets a contiguous run of tiles, in groups of 8 tile rows
-__device__ __forceinline__ void block_tile_of(const BlockGemmArgs &g, int &tm, int &tn) {
-    const int ntiles = g.tiles_m * g.tiles_n;
-    const int wg = blockIdx.x, xcd = wg & 7, idx = wg >> 3;
-    const int per = ntiles >> 3, rem = ntiles & 7;
-    const int lt = xcd * per + (xcd < rem ? xcd : rem) + idx;
-    constexpr int GROUP = 8;
-    const int group_tiles = GROUP * g.tiles_n;
-    const int grp = lt / group_tiles, first = grp * GROUP;
-    const int gsz = min(g.tiles_m - first, GROUP), in = lt - grp * group_tiles;
-    tm = first + in % gsz;
-    tn = in / gsz;
-}
-
 // four consecutive columns of row m, starting at n
 template <bool FP8SUMS>
 __device__ __forceinline__ void block_store4(const BlockGemmArgs &g, int m, int n, const float *v) {
@@ -179,7 +164,7 @@ __global__ __launch_bounds__(GNT, FP8SUMS ? 2 : 1) void k_block_gemm(BlockGemmAr
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1, l32 = lane & 31, h = lane >> 5;
     int tm, tn;
-    block_tile_of(g, tm, tn);
+    tile_index(g.tiles_m, g.tiles_n, tm, tn);
     const int m0 = tm * GB, n0 = tn * GB;
     const int nk = (g.K + kBlk - 1) / kBlk;
 
@@ -334,7 +319,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     float *const sS = sScales + grp * SR * (PM + PN);
     const int wm = wave / WN, wn = wave % WN, l32 = lane & 31, h = lane >> 5;
     int tm, tn;
-    block_tile_of(g, tm, tn);
+    tile_index(g.tiles_m, g.tiles_n, tm, tn);
     const int m0 = tm * PM, n0 = tn * PN;
     const int K = RAG ? g.K & ~15 : g.K, nk = (K + kBlk - 1) / kBlk, ktail = K - (nk - 1) * kBlk;
     const int mrows = min(PM, g.M - m0), nrows = min(PN, g.N - n0);
@@ -375,7 +360,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     // the last-level cache then open a DRAM page for every one of them, and a stage's loads wait for its
     // slowest.  One wave of either group fetches a word of every line of whole KiB of rows, the next KiB of
     // K, a few rows per stage: the first group A's rows, the second B's.  The 32 tiles that an XCD works on
-    // are 8 x 4 (block_tile_of), so a workgroup takes a quarter of its A rows and an eighth of its B rows; with
+    // are 8 x 4 (tile_index), so a workgroup takes a quarter of its A rows and an eighth of its B rows; with
     // fewer than eight rows of tiles the eighths of B that would be theirs are not fetched ahead.
     // Operands from HBM, without and with: 1000 x 4096 x 28672 180 and 155 us, 512 x 8192 x 28672 (four rows of
     // tiles) 188 and 177, 256 x 16384 x 28672 (two) 200 and 193.  1000 rows, two or four KiB ahead 166, 168; a line
@@ -719,7 +704,7 @@ __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(BlockGemmArgs g) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, h = lane >> 4;
     int tm, tn;
-    block_tile_of(g, tm, tn);
+    tile_index(g.tiles_m, g.tiles_n, tm, tn);
     const int m0 = tm * 8 * AI, n0 = tn * DN;
     const int nk = (g.K + kBlk - 1) / kBlk, ktail = g.K - (nk - 1) * kBlk;
     const int lda = (int)g.lda, ldb = (int)g.ldb, mrows = min(8 * AI, g.M - m0), nrows = min(DN, g.N - n0);

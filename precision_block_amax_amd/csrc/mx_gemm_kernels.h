@@ -119,21 +119,28 @@ __device__ __forceinline__ uint32_t bf16_rne(float f) { return bf16x2(f, 0.0f) &
 // MI355X: 256 CUs in 8 XCDs, so an XCD runs 32 workgroups of one per CU at a time
 constexpr int kCusPerXcd = 32;
 
-// XCD-aware tile order: wg -> (tile row, tile column)
-__device__ __forceinline__ void tile_of(const GemmArgs &g, int &m0, int &n0) {
-    const int ntiles = g.tiles_m * g.tiles_n;
+// XCD-aware tile order: wg -> (tile row, tile column).  Consecutive workgroups go to the 8 XCDs in turn, so each XCD
+// gets a contiguous run of tiles, in groups of 8 tile rows
+__device__ __forceinline__ void tile_index(int tiles_m, int tiles_n, int &tm, int &tn) {
+    const int ntiles = tiles_m * tiles_n;
     const int wg = blockIdx.x;
     const int xcd = wg & 7, idx = wg >> 3;
     const int per = ntiles >> 3, rem = ntiles & 7;
     const int lt = xcd * per + (xcd < rem ? xcd : rem) + idx;
     constexpr int GROUP = 8;
-    const int group_tiles = GROUP * g.tiles_n;
+    const int group_tiles = GROUP * tiles_n;
     const int grp = lt / group_tiles;
     const int first_m = grp * GROUP;
-    const int gsz = (g.tiles_m - first_m) < GROUP ? (g.tiles_m - first_m) : GROUP;
+    const int gsz = (tiles_m - first_m) < GROUP ? (tiles_m - first_m) : GROUP;
     const int in_grp = lt - grp * group_tiles;
-    m0 = (first_m + in_grp % gsz) * BM;
-    n0 = (in_grp / gsz) * BN;
+    tm = first_m + in_grp % gsz;
+    tn = in_grp / gsz;
+}
+// its first row and column
+__device__ __forceinline__ void tile_of(const GemmArgs &g, int &m0, int &n0) {
+    tile_index(g.tiles_m, g.tiles_n, m0, n0);
+    m0 *= BM;
+    n0 *= BN;
 }
 
 // Global -> register -> LDS staging of one K tile of codes (RBA / RBB bytes
