@@ -349,24 +349,16 @@ __global__ __launch_bounds__(T *R) void k_norm_bwd(NormBwdArgs a, int per) {
                 cx[u][k] = wx[u][k];
                 cd[u][k] = wd[u][k];
             }
-            // past the row's end x and dy are 0, and mu too: mean * rstd may be beyond fp32 where no xh is, and
-            // Inf times a dy of 0 is NaN
-            const int n = a.cols - 8 * (u * T + t);
-            const float mu = n > 0 ? mn : 0.f;
-            float xm[8];
-#pragma unroll
-            for (int i = 0; i < 8; i++) xm[i] = get(cx[u], i) - mu;
-            if (!WHOLE && n < 8) {
-#pragma unroll
-                for (int i = 0; i < 8; i++) xm[i] = i < n ? xm[i] : 0.f;
-            }
+            // Past the row's end x, dy and g are 0 and x - mean is -mean, and nothing of it may reach the sums over the
+            // row: g * rstd comes first, because mean * rstd may be beyond fp32 where no xh is, and 0 * Inf is NaN.
+            // (dweight past the end is not stored.)
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                const float d = get(cd[u], i), xh = xm[i] * rs, g = d * wt[u][i];
+                const float d = get(cd[u], i), xm = get(cx[u], i) - mn, g = d * wt[u][i];
                 sg += g;
-                sgx = __builtin_fmaf(g, xh, sgx);
+                sgx = __builtin_fmaf(g * rs, xm, sgx);
                 if constexpr (PARAMS) {
-                    dw[u][i] = __builtin_fmaf(d, xh, dw[u][i]);
+                    dw[u][i] = __builtin_fmaf(d, xm * rs, dw[u][i]);
                     db[u][i] += d;
                     // here and now: left alone, the compiler moves these sums to the end of the loop and
                     // holds every d and xh until then
