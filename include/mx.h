@@ -432,7 +432,8 @@ mx_status_t mx_block_quantize_dual(const void *x_bf16, int64_t rows, int64_t col
  *                |terms| in the worst case (2^-11 and less on random data):
  *                below the result's own rounding to bf16 unless the sum cancels
  *                far.  Where that matters, MX_OUT_F32 or mx_block_gemm_sums.
- * Products of two scales outside fp32's range are Inf or 0.  A NaN scale makes
+ * Products of two scales outside fp32's range are Inf or 0, those below 2^-126
+ * keep the bits that a subnormal number has.  A NaN scale makes
  * every element of C that it contributes to NaN; NaN and Inf codes behave as
  * these values.  Fast are operands whose rows are aligned to 16 bytes (any K;
  * as the quantizers' callers lay them out); others take a general kernel, at
