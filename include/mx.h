@@ -417,9 +417,9 @@ mx_status_t mx_block_quantize_dual(const void *x_bf16, int64_t rows, int64_t col
  * with A [M x K] in blocks of 128 along K and B [N x K] likewise (b_tile = 0)
  * or in 128 x 128 tiles (b_tile = 1: sb[b][n / 128]).  Any M, N and K (K = 0
  * writes C = 0; M or N of 2^31 and more, K above 2^31 - 128 and 2^22 or more
- * tiles of 128 x 128 are MX_ERR_UNSUPPORTED); lda, ldb in bytes, ldsa, ldsb in floats, c [M x ldc] per
- * `out`, ldc >= N.  Every block's sum is multiplied by its scales and added to
- * an fp32 accumulator.
+ * tiles of 128 x 128 are MX_ERR_UNSUPPORTED); lda, ldb in bytes, ldsa, ldsb in
+ * floats, c [M x ldc] per `out`, ldc >= N.  Every block's sum is multiplied by
+ * its scales and added to an fp32 accumulator.
  *   MX_OUT_F32   every product is exact and sums are fp32: |C - sum| <=
  *                (130 + ceil(K / 128)) * 2^-24 * sum |terms|, which is one
  *                rounding for each of a block's additions, for its scales and

@@ -28,7 +28,8 @@ Range run(const void *p, int64_t n) { return {p, n, n, 0}; }
 // row stride ld, `width` used, in units of `size` bytes
 Range rows_at(const void *p, int64_t rows, int64_t ld, int64_t width, int64_t size) {
     if (rows <= 0 || width <= 0) return run(p, 0);
-    if (rows == 1 && width <= INT64_MAX / size) return run(p, width * size);
+    if (width > INT64_MAX / size) return run(p, -1);
+    if (rows == 1) return run(p, width * size);
     if (rows - 1 > (INT64_MAX / size - width) / ld) return run(p, -1);
     return {p, ((rows - 1) * ld + width) * size, width * size, ld * size};
 }

@@ -60,3 +60,11 @@ def test_block_gemm_sums_rejects(L):
     for sums, out in ((0, BF16), (1, BF16), (1, F32)):
         assert f(*args(sums=sums, out=out, M=0)) == OK
         assert f(*args(sums=sums, out=out, K=(1 << 31) - 1)) != OK
+
+
+def test_single_rows_of_any_width(L):
+    """one row whose bytes leave 64 bits is refused, whatever the stride"""
+    for cols in ((1 << 62), (1 << 62) + 5, (1 << 63) - 1):
+        args = [P(1 << 20), 1, cols, (1 << 63) - 1, E4M3, 0, P(1 << 30), (1 << 63) - 1, P(1 << 40), 1, None]
+        assert L.mx_block_quantize(*args) == INVALID, cols
+    assert L.mx_layer_norm(P(1 << 20), 1, 1 << 62, 1 << 62, None, None, BF16, 0, 1e-5, P(1 << 30), 1 << 62, None, None, None) == UNSUPPORTED
