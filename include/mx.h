@@ -521,6 +521,96 @@ mx_status_t mx_layer_norm_backward(const void *dy_bf16, int64_t lddy, const void
                                    const float *mean, const float *rstd, void *dx_bf16, int64_t lddx, float *dweight,
                                    float *dbias, void *workspace, int64_t workspace_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Queries and keys after the QKV product: rotary positions, alone or behind an
+ * RMS norm of each head, and the backward pass.
+ *
+ * Queries and keys are two sets of heads of `dim` bf16 elements over the same
+ * tokens: element i of head h of token t is at t * ld + h * ld_head + i.  Any
+ * strides with tokens outermost (views of one QKV output row included) or heads
+ * outermost, no element twice; either set may have no heads.  dim is at most 512,
+ * heads at most 2^16 each, tokens at most 2^31 (else MX_ERR_UNSUPPORTED).
+ *
+ * Rotation.  The first `rot` elements of a head (even, 0 .. dim) form rot / 2
+ * pairs, the others stay.  With p the token's position (int32 or int64, negative
+ * ones too) and pair i's angle p * freqs[i] (radians, double, device memory):
+ *     (a, b) -> (a c - b s, b c + a s),   c, s = scale * (cos, sin)(angle)
+ * Angles are taken in fp64 and reduced to one turn there, so far positions lose
+ * nothing: |error| <= 2^-21 + |p| freqs[i] 2^-51 radians; the rest is fp32,
+ * rounded once to bf16.  inverse = 1 turns by -angle: with the same scale that is
+ * the transpose, the backward pass of the rotation.
+ */
+typedef enum {
+    MX_ROPE_HALF = 0,       /* pair i: elements i and i + rot / 2  */
+    MX_ROPE_INTERLEAVED = 1 /* pair i: elements 2 i and 2 i + 1    */
+} mx_rope_layout_t;
+typedef enum {
+    MX_POS_I32 = 0,
+    MX_POS_I64 = 1
+} mx_pos_t;
+
+/*
+ * mx_rope_frequencies -- freqs[0 .. rot / 2 - 1] in HOST memory:
+ *     theta^(-2 i / rot),
+ * for contexts `factor` times as long as the model's first one divided by factor
+ * (MX_ROPE_LINEAR), or (MX_ROPE_BANDS) divided only where a pair makes fewer than
+ * `low` turns within `original` positions, kept where it makes more than `high`,
+ * in between f * keep + f / factor * (1 - keep), keep = (turns - low) / (high -
+ * low).  Recipes that also sharpen the attention pass their factor as `scale`.
+ * A host function: no GPU is needed.
+ */
+typedef enum {
+    MX_ROPE_PLAIN = 0,  /* factor, low, high and original are not read */
+    MX_ROPE_LINEAR = 1, /* low, high and original are not read         */
+    MX_ROPE_BANDS = 2
+} mx_rope_scaling_t;
+mx_status_t mx_rope_frequencies(int64_t rot, double theta, mx_rope_scaling_t scaling, double factor, double low,
+                                double high, double original, double *freqs);
+
+mx_status_t mx_rope(const void *q_bf16, int64_t ldq, int64_t ldq_head, int64_t q_heads, const void *k_bf16, int64_t ldk,
+                    int64_t ldk_head, int64_t k_heads, int64_t tokens, int64_t dim, const void *positions,
+                    mx_pos_t pos_type, const double *freqs, int64_t rot, mx_rope_layout_t layout, float scale,
+                    int inverse, void *q_out, int64_t ldqo, int64_t ldqo_head, void *k_out, int64_t ldko,
+                    int64_t ldko_head, void *stream);
+
+/*
+ * mx_qk_norm_rope -- for every head
+ *     xh = x * rstd, rstd = 1 / sqrt(mean(x^2) + eps), y = rotation of xh * weight,
+ * weight the `dim` values (of `param` type, NULL: 1) that all query heads, or all
+ * key heads, share.  One pass, fp32 until y's one rounding.  eps >= 0, finite;
+ * rot = 0 leaves the norm alone (positions and freqs may then be NULL).  As in
+ * mx_layer_norm, a head of zeros with eps = 0 gives NaN.
+ */
+mx_status_t mx_qk_norm_rope(const void *q_bf16, int64_t ldq, int64_t ldq_head, int64_t q_heads, const void *k_bf16,
+                            int64_t ldk, int64_t ldk_head, int64_t k_heads, int64_t tokens, int64_t dim,
+                            const void *q_weight, const void *k_weight, mx_out_t param, float eps,
+                            const void *positions, mx_pos_t pos_type, const double *freqs, int64_t rot,
+                            mx_rope_layout_t layout, float scale, void *q_out, int64_t ldqo, int64_t ldqo_head,
+                            void *k_out, int64_t ldko, int64_t ldko_head, void *stream);
+
+/*
+ * mx_qk_norm_rope_backward -- with dy the gradient of y, u the transposed rotation
+ * of dy and g = u * weight:
+ *     dx = rstd * (g - xh * mean(g * xh)),  dweight = sum over tokens and heads of u * xh
+ * from x as the forward call read it (rstd is made again).  dx: bf16, rounded once;
+ * dq_weight, dk_weight: fp32 [dim], overwritten (zeros where there are no tokens or
+ * no heads), either may be NULL.  workspace as in mx_layer_norm_backward,
+ * mx_qk_norm_rope_backward_workspace(tokens, q_heads, k_heads, dim) bytes.  Sums are
+ * in a fixed order: the same inputs give the same bits.
+ */
+int64_t mx_qk_norm_rope_backward_workspace(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim);
+mx_status_t mx_qk_norm_rope_backward(const void *dq_bf16, int64_t lddq, int64_t lddq_head, const void *dk_bf16,
+                                     int64_t lddk, int64_t lddk_head, const void *q_bf16, int64_t ldq,
+                                     int64_t ldq_head, int64_t q_heads, const void *k_bf16, int64_t ldk,
+                                     int64_t ldk_head, int64_t k_heads, int64_t tokens, int64_t dim,
+                                     const void *q_weight, const void *k_weight, mx_out_t param, float eps,
+                                     const void *positions, mx_pos_t pos_type, const double *freqs, int64_t rot,
+                                     mx_rope_layout_t layout, float scale, void *dxq_bf16, int64_t lddxq,
+                                     int64_t lddxq_head, void *dxk_bf16, int64_t lddxk, int64_t lddxk_head,
+                                     float *dq_weight, float *dk_weight, void *workspace, int64_t workspace_bytes,
+                                     void *stream);
+
 /* Static, NUL-terminated name of a status code. */
 const char *mx_status_string(mx_status_t s);
 

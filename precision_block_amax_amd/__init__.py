@@ -3,9 +3,10 @@
 OCP-MX micro-scaling quantization (block 32, E8M0 scales, E4M3 / E5M2 / E2M1
 elements), the fixed-sign 32-point block-Hadamard rotation used on the
 weight-gradient path, and the MX-scaled GEMM; FP8 operands with one fp32 scale
-for each block of 128 (quantizers and product); and the norm in front of a
+for each block of 128 (quantizers and product); the norm in front of a
 linear layer (layer norm or RMS norm, forward, straight to a quantized operand,
-and backward), as hand-written gfx950 HIP kernels behind a C ABI.
+and backward); and rotary positions and the norm of each head of queries and
+keys, as hand-written gfx950 HIP kernels behind a C ABI.
 
 This module only marshals arguments: it checks tensor shapes, dtypes and
 devices, allocates outputs with torch (device memory and streams are all
@@ -27,7 +28,8 @@ __all__ = [
     "quantize", "quantize_transpose", "hadamard32_quantize", "quantize_dual",
     "quantize_transpose_sr", "quantize_pair", "gemm", "fsdp_payload", "payload_views",
     "payload_width", "block_quantize", "block_quantize_dual", "block_gemm", "layer_norm",
-    "layer_norm_quantize", "layer_norm_backward",
+    "layer_norm_quantize", "layer_norm_backward", "rope_frequencies", "rope", "qk_norm_rope",
+    "qk_norm_rope_backward",
 ]
 
 E4M3, E5M2, E2M1 = 0, 1, 2
@@ -80,6 +82,17 @@ def lib() -> ctypes.CDLL:
         L.mx_layer_norm_backward.argtypes = [P, i64, P, i64, i64, i64, P, i32, i32, P, P, P, i64, P, P, P, i64, P]
         L.mx_layer_norm_backward_workspace.argtypes = [i64, i64]
         L.mx_layer_norm_backward_workspace.restype = i64
+        f64 = ctypes.c_double
+        heads, rotation = [P, i64, i64, i64] * 2 + [i64, i64], [P, i32, P, i64, i32, f32]
+        L.mx_rope_frequencies.argtypes = [i64, f64, i32, f64, f64, f64, f64, P]
+        L.mx_rope.argtypes = heads + rotation + [i32] + [P, i64, i64] * 2 + [P]
+        L.mx_qk_norm_rope.argtypes = heads + [P, P, i32, f32] + rotation + [P, i64, i64] * 2 + [P]
+        L.mx_qk_norm_rope_backward.argtypes = ([P, i64, i64] * 2 + heads + [P, P, i32, f32] + rotation + [P, i64, i64] * 2 +
+                                               [P, P, P, i64, P])
+        L.mx_qk_norm_rope_backward_workspace.argtypes = [i64, i64, i64, i64]
+        L.mx_qk_norm_rope_backward_workspace.restype = i64
+        for fn in (L.mx_rope_frequencies, L.mx_rope, L.mx_qk_norm_rope, L.mx_qk_norm_rope_backward):
+            fn.restype = ctypes.c_int
         for fn in (L.mx_block_quantize, L.mx_block_quantize_dual, L.mx_block_gemm, L.mx_block_gemm_sums, L.mx_layer_norm,
                    L.mx_layer_norm_quantize, L.mx_layer_norm_block_quantize, L.mx_layer_norm_backward):
             fn.restype = ctypes.c_int
@@ -602,3 +615,141 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
         _check(lib().mx_layer_norm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, rows, cols, w, p, 1 if rms else 0, m, r,
                                             out.data_ptr(), lddx, _ptr(dw), _ptr(db), _ptr(ws), need, _current(dev)))
     return out, dw, db
+
+
+# ---------------------------------------------------------------------------
+# queries and keys: rotary positions and the norm of each head
+
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROPE_SCALINGS = {"plain": 0, "linear": 1, "bands": 2}
+_I32, _I64, _F64 = torch.int32, torch.int64, torch.float64
+
+
+def rope_frequencies(rot: int, theta: float = 10000.0, scaling: str = "plain", factor: float = 1.0, low: float = 1.0,
+                     high: float = 4.0, original: float = 8192.0, device="cuda") -> torch.Tensor:
+    """mx_rope_frequencies: radians per position of each of the rot / 2 pairs (float64 on
+    `device`), for rope and qk_norm_rope.  scaling "linear" divides them by factor; "bands" divides
+    those of fewer than `low` turns within `original` positions, keeps those of more than `high`,
+    and mixes in between."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % sorted(_ROPE_SCALINGS))
+    f = torch.empty((max(rot, 0) // 2,), dtype=_F64)
+    _check(lib().mx_rope_frequencies(rot, theta, _ROPE_SCALINGS[scaling], factor, low, high, original, f.data_ptr()))
+    return f.to(device)
+
+
+def _heads(x: Optional[torch.Tensor], device, what: str) -> Tuple[int, int, int, int]:
+    """address, token stride, head stride and number of heads of a [tokens x heads x dim] tensor"""
+    if x is None:
+        return 0, 0, 0, 0
+    if x.dtype is not _BF16 or x.dim() != 3 or not x.is_cuda or x.device != device:
+        raise ValueError("%s must be a 3-D bf16 tensor [tokens x heads x dim] on %s" % (what, device))
+    (tokens, heads, dim), (lt, lh, step) = x.shape, x.stride()
+    if step != 1 and dim > 1 and x.numel():
+        raise ValueError("the last dimension of %s must be contiguous" % what)
+    return x.data_ptr(), lt, lh, heads
+
+
+def _rotation(tokens: int, dim: int, device, positions, freqs, layout: str) -> Tuple[int, int, int, int, int]:
+    """addresses of positions and freqs, the positions' type, rot and the layout"""
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError("layout must be one of %s" % sorted(_ROPE_LAYOUTS))
+    if freqs is None:
+        return 0, 0, 0, 0, _ROPE_LAYOUTS[layout]
+    if freqs.dtype is not _F64 or freqs.dim() != 1 or freqs.device != device or not freqs.is_contiguous():
+        raise ValueError("freqs must be contiguous float64 of one dimension on %s" % device)
+    if 2 * freqs.shape[0] > dim:
+        raise ValueError("%d frequencies rotate more than the head's %d elements" % (freqs.shape[0], dim))
+    if positions is None or (positions.dtype is not _I64 and positions.dtype is not _I32) or positions.shape != (tokens,) \
+            or positions.device != device or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous int32 or int64 of shape (%d,) on %s" % (tokens, device))
+    return (positions.data_ptr(), freqs.data_ptr(), 1 if positions.dtype is _I64 else 0, 2 * freqs.shape[0],
+            _ROPE_LAYOUTS[layout])
+
+
+def _qk(q: torch.Tensor, k: Optional[torch.Tensor]):
+    """tokens, dim and device of queries and keys, and what _heads says of each"""
+    if q.dim() != 3 or not q.is_cuda:
+        raise ValueError("q must be a 3-D bf16 tensor [tokens x heads x dim] on a GPU")
+    tokens, _, dim = q.shape
+    if k is not None and (k.dim() != 3 or k.shape[0] != tokens or k.shape[2] != dim):
+        raise ValueError("q and k must agree in tokens and dim")
+    return tokens, dim, q.device, _heads(q, q.device, "q"), _heads(k, q.device, "k")
+
+
+def _like(x: Optional[torch.Tensor], out: Optional[torch.Tensor], device, what: str):
+    """the output for x: the one given, after its checks, or a new one"""
+    if x is None:
+        if out is not None:
+            raise ValueError("%s given without its input" % what)
+        return None
+    if out is None:
+        return torch.empty(x.shape, dtype=_BF16, device=device)
+    if out.shape != x.shape:
+        raise ValueError("%s must have shape %s" % (what, tuple(x.shape)))
+    return out
+
+
+def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor], freqs: Optional[torch.Tensor],
+         layout: str = "half", scale: float = 1.0, inverse: bool = False, out=None, stream=None):
+    """mx_rope: (q, k) with the first 2 * len(freqs) elements of every head rotated by
+    positions[token] * freqs (rope_frequencies).  q, k: bf16 [tokens x heads x dim], any token and
+    head strides; k may be None.  layout "half": pairs (i, i + len(freqs)), "interleaved": (2 i,
+    2 i + 1).  scale multiplies what is rotated; inverse turns the other way, which with the same
+    scale is the backward pass.  `out` = (q_out, k_out)."""
+    tokens, dim, dev, qh, kh = _qk(q, k)
+    pos, fr, pt, rot, lay = _rotation(tokens, dim, dev, positions, freqs, layout)
+    oq, ok = (None, None) if out is None else out
+    with _scope(dev, stream):
+        oq, ok = _like(q, oq, dev, "q_out"), _like(k, ok, dev, "k_out")
+        qo, ko = _heads(oq, dev, "q_out"), _heads(ok, dev, "k_out")
+        _check(lib().mx_rope(*qh, *kh, tokens, dim, pos, pt, fr, rot, lay, scale, 1 if inverse else 0, *qo[:3], *ko[:3],
+                             _current(dev)))
+    return oq, ok
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
+                 k_weight: Optional[torch.Tensor], positions: Optional[torch.Tensor] = None,
+                 freqs: Optional[torch.Tensor] = None, eps: float = 1e-5, layout: str = "half", scale: float = 1.0,
+                 out=None, stream=None):
+    """mx_qk_norm_rope: the RMS norm of every head of q and k (bf16 [tokens x heads x dim], as in
+    rope), times q_weight or k_weight ([dim], float32 or bfloat16, or None), then rope, in one
+    pass.  Without freqs the norm alone."""
+    tokens, dim, dev, qh, kh = _qk(q, k)
+    wq, wk, p = _param(q_weight, dim, dev, "q_weight"), _param(k_weight, dim, dev, "k_weight"), _param_type(q_weight, k_weight)
+    pos, fr, pt, rot, lay = _rotation(tokens, dim, dev, positions, freqs, layout)
+    oq, ok = (None, None) if out is None else out
+    with _scope(dev, stream):
+        oq, ok = _like(q, oq, dev, "q_out"), _like(k, ok, dev, "k_out")
+        qo, ko = _heads(oq, dev, "q_out"), _heads(ok, dev, "k_out")
+        _check(lib().mx_qk_norm_rope(*qh, *kh, tokens, dim, wq, wk, p, eps, pos, pt, fr, rot, lay, scale, *qo[:3], *ko[:3],
+                                     _current(dev)))
+    return oq, ok
+
+
+def qk_norm_rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tensor, k: Optional[torch.Tensor],
+                          q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                          positions: Optional[torch.Tensor] = None, freqs: Optional[torch.Tensor] = None,
+                          eps: float = 1e-5, layout: str = "half", scale: float = 1.0, weight_grad: bool = True, out=None,
+                          stream=None):
+    """mx_qk_norm_rope_backward: (dxq, dxk, dq_weight, dk_weight) for the gradients dq, dk (bf16)
+    of what qk_norm_rope returned for the same arguments; dxq, dxk are bf16, the weights'
+    gradients float32, None without weight_grad (dxk and dk_weight also without k).  `out` =
+    (dxq, dxk)."""
+    tokens, dim, dev, qh, kh = _qk(q, k)
+    if dq.shape != q.shape or (dk is None) != (k is None) or (dk is not None and dk.shape != k.shape):
+        raise ValueError("dq and dk must agree in shape with q and k")
+    gq, gk = _heads(dq, dev, "dq"), _heads(dk, dev, "dk")
+    wq, wk, p = _param(q_weight, dim, dev, "q_weight"), _param(k_weight, dim, dev, "k_weight"), _param_type(q_weight, k_weight)
+    pos, fr, pt, rot, lay = _rotation(tokens, dim, dev, positions, freqs, layout)
+    oq, ok = (None, None) if out is None else out
+    with _scope(dev, stream):
+        oq, ok = _like(q, oq, dev, "dxq"), _like(k, ok, dev, "dxk")
+        qo, ko = _heads(oq, dev, "dxq"), _heads(ok, dev, "dxk")
+        dwq = torch.empty((dim,), dtype=_F32, device=dev) if weight_grad else None
+        dwk = torch.empty((dim,), dtype=_F32, device=dev) if weight_grad and k is not None else None
+        need = lib().mx_qk_norm_rope_backward_workspace(tokens, qh[3], kh[3], dim) if weight_grad else 0
+        ws = torch.empty((need,), dtype=_U8, device=dev) if need else None
+        _check(lib().mx_qk_norm_rope_backward(*gq[:3], *gk[:3], *qh, *kh, tokens, dim, wq, wk, p, eps, pos, pt, fr, rot, lay,
+                                              scale, *qo[:3], *ko[:3], _ptr(dwq), _ptr(dwk), _ptr(ws), need, _current(dev)))
+    return oq, ok, dwq, dwk

@@ -18,36 +18,6 @@ bool fp8(int f) { return f == MX_E4M3 || f == MX_E5M2; }
 bool type_ok(int t) { return t == MX_OUT_F32 || t == MX_OUT_BF16; }
 int64_t blocks(int64_t n) { return (n + kBlk - 1) / kBlk; }
 
-// `rows` rows of `width` used bytes, one every `stride` bytes (0: a single row); `n` bytes from the first of them to the
-// end of the last, -1 if that leaves 64 bits
-struct Range {
-    const void *p;
-    int64_t n, width, stride;
-};
-Range run(const void *p, int64_t n) { return {p, n, n, 0}; }
-// row stride ld, `width` used, in units of `size` bytes
-Range rows_at(const void *p, int64_t rows, int64_t ld, int64_t width, int64_t size) {
-    if (rows <= 0 || width <= 0) return run(p, 0);
-    if (width > INT64_MAX / size) return run(p, -1);
-    if (rows == 1) return run(p, width * size);
-    if (rows - 1 > (INT64_MAX / size - width) / ld) return run(p, -1);
-    return {p, ((rows - 1) * ld + width) * size, width * size, ld * size};
-}
-// no byte belongs to both: their whole extents are disjoint, or the rows of one lie in the gaps of the other's
-bool disjoint(const Range &a, const Range &b) {
-    if (!overlap(a.p, a.n, b.p, b.n)) return true;
-    return a.stride > 0 && a.stride == b.stride && interleaved(a.p, a.width, b.p, b.width, a.stride);
-}
-// every range exists (n >= 0) and no range from `first_out` on overlaps another one
-mx_status_t check_ranges(const Range *r, int count, int first_out) {
-    for (int i = 0; i < count; i++)
-        if (r[i].n < 0) return MX_ERR_INVALID_ARG;
-    for (int i = first_out; i < count; i++)
-        for (int j = 0; j < i; j++)
-            if (!disjoint(r[i], r[j])) return MX_ERR_INVALID_ARG;
-    return MX_OK;
-}
-
 // one output form: codes [n x k] with k the reduction dimension, scales [blocks(k)][n or blocks(n)]
 mx_status_t check_form(int64_t n, int64_t k, bool tile, int fmt, const void *codes, int64_t ld_codes,
                        const float *scales, int64_t ld_scales, Range *r) {

@@ -1,5 +1,5 @@
 // mx_check.h -- argument checks and device check shared by the entry points
-// (mx_api.hip, mx_block_api.hip).  Everything here runs on the host before the
+// (mx_api.hip, mx_block_api.hip, mx_rope_api.hip).  Everything here runs on the host before the
 // first launch.
 #pragma once
 #include <atomic>
@@ -43,6 +43,36 @@ inline bool interleaved(const void *p, int64_t wp, const void *q, int64_t wq, in
     int64_t d = (int64_t)((uintptr_t)q - (uintptr_t)p) % stride;
     if (d < 0) d += stride;
     return d >= wp && d + wq <= stride;
+}
+
+// `rows` rows of `width` used bytes, one every `stride` bytes (0: a single row); `n` bytes from the first of them to the
+// end of the last, -1 if that leaves 64 bits
+struct Range {
+    const void *p;
+    int64_t n, width, stride;
+};
+inline Range run(const void *p, int64_t n) { return {p, n, n, 0}; }
+// row stride ld, `width` used, in units of `size` bytes
+inline Range rows_at(const void *p, int64_t rows, int64_t ld, int64_t width, int64_t size) {
+    if (rows <= 0 || width <= 0) return run(p, 0);
+    if (width > INT64_MAX / size) return run(p, -1);
+    if (rows == 1) return run(p, width * size);
+    if (rows - 1 > (INT64_MAX / size - width) / ld) return run(p, -1);
+    return {p, ((rows - 1) * ld + width) * size, width * size, ld * size};
+}
+// no byte belongs to both: their whole extents are disjoint, or the rows of one lie in the gaps of the other's
+inline bool disjoint(const Range &a, const Range &b) {
+    if (!overlap(a.p, a.n, b.p, b.n)) return true;
+    return a.stride > 0 && a.stride == b.stride && interleaved(a.p, a.width, b.p, b.width, a.stride);
+}
+// every range exists (n >= 0) and no range from `first_out` on overlaps another one
+inline mx_status_t check_ranges(const Range *r, int count, int first_out) {
+    for (int i = 0; i < count; i++)
+        if (r[i].n < 0) return MX_ERR_INVALID_ARG;
+    for (int i = first_out; i < count; i++)
+        for (int j = 0; j < i; j++)
+            if (!disjoint(r[i], r[j])) return MX_ERR_INVALID_ARG;
+    return MX_OK;
 }
 
 inline mx_status_t check_device() {

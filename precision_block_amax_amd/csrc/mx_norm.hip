@@ -57,14 +57,6 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
-// 1 / sqrt(v), good to 2^-23: the instruction's value and one Newton step, in 5 operations for 30 of a square root
-// and a division.  Zero, very small, infinite and NaN v take those; all lanes hold the same v.
-__device__ __forceinline__ float rsqrt1(float v) {
-    if (!(v >= 0x1p-100f && v < INFINITY)) return 1.0f / __builtin_sqrtf(v);
-    const float y = __builtin_amdgcn_rsqf(v);
-    return __builtin_fmaf(0.5f * y, __builtin_fmaf(-(v * y), y, 1.0f), y);
-}
-
 // sum / n, correctly rounded unless it is subnormal: an approximation and one correction by its exact remainder, as
 // block_scale (n: a whole number, rn its rounded reciprocal).  sum * rn alone gives constant rows of 896, 1000 or
 // 7168 columns a mean beside their value, and y then shows the difference times a very large rstd.  An infinite

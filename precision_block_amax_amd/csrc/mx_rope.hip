@@ -1,0 +1,406 @@
+// mx_rope.hip -- rotary positions of queries and keys for gfx950, alone or after
+// the RMS norm of each head in one pass, and the backward pass of both.
+//
+// Rotation at position p: pair i (a, b) of a head becomes (a c - b s, b c + a s),
+// c, s = scale * (cos, sin)(p * freq_i).  Its transpose, the backward pass, is the
+// rotation by the opposite angle.  The angle is taken in fp64 as turns, p * freq_i /
+// 2 pi less the nearest whole number: what is left is exact to p * 2^-53 turns,
+// then rounded to fp32, 2^-25 of a turn, 2^-23 of its radius (fp32 products of far
+// positions, 2^17 and more, would be off by 2^-8 and more).  One lane makes one
+// angle; they go through LDS to the lanes that need them, once for all heads.
+//
+// Norm: xh = x * rstd, rstd = 1 / sqrt(mean(x^2) + eps) over the head, y = rope(xh * w).
+// Backward, with u = inverse rotation of dy, g = u * w:
+//   dx = rstd * (g - xh * mean(g * xh)),  dw = sum over tokens and heads of u * xh
+// rstd is made again from x, which is read anyway.  The sums of dw stay in registers
+// for all heads that a wave meets, then go through the workspace to a second kernel;
+// every sum is in a fixed order, so the same inputs give the same bits.
+//
+// A wave takes the heads of one token, 64 / L at a time: a head is 16 elements of
+// each of L lanes, two vectors of eight.  In the half layout these are the two
+// halves of eight pairs, so pairs never cross lanes and a head's sums are a DPP tree
+// over L lanes.  Everything is fp32 until the one rounding to bf16.
+#include <type_traits>
+
+#include "mx_block_util.h"
+#include "mx_rope_internal.h"
+
+namespace mx {
+namespace {
+
+constexpr int kHW = 4;  // waves of a workgroup
+constexpr int kMaxPairs = kHeadMaxDim / 2;
+
+// sum over groups of L neighbouring lanes, in every lane of the group
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+    const auto add = [&](auto ctrl) { v += __uint_as_float(dpp<decltype(ctrl)::value>(__float_as_uint(v))); };
+    if constexpr (L >= 2) add(std::integral_constant<int, kDppXor1>{});
+    if constexpr (L >= 4) add(std::integral_constant<int, kDppXor2>{});
+    if constexpr (L >= 8) add(std::integral_constant<int, kDppHalfMirror>{});
+    if constexpr (L >= 16) add(std::integral_constant<int, kDppMirror>{});
+    if constexpr (L >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if constexpr (L >= 64) {
+        const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(q[0]) + __uint_as_float(q[1]);
+    }
+    return v;
+}
+
+// How a head lies in L lanes.  A lane has NS = 2 H slots, slot i and i + H (half layout) or 2 i and 2 i + 1
+// (interleaved) a pair.  V > 0: slots are two vectors of V elements, from o0 and o1 on, all of its pairs rotated or
+// none.  V = 0, any dim and rot: every pair is (i, i + H); the first four of a lane are pairs lane + 64 i of the
+// rotation, the others elements behind it.
+template <int V, int L, bool INTER>
+struct Map {
+    static constexpr int H = V ? V : 8, NS = 2 * H;
+    int o0, o1, l;
+    bool act, rot;  // (V > 0) the lane has elements; they are rotated
+    int dim, pairs, nrot;
+
+    __device__ __forceinline__ Map(int lane, int dim_, int rot_) : dim(dim_), pairs(rot_ / 2), nrot(rot_) {
+        l = lane % L;
+        if constexpr (V > 0) {
+            act = 2 * V * l < dim;
+            rot = 2 * V * l < nrot;
+            const bool halves = !INTER && rot;
+            o0 = halves ? V * l : 2 * V * l;
+            o1 = halves ? pairs + V * l : 2 * V * l + V;
+        } else {
+            act = rot = true;
+            o0 = o1 = 0;
+        }
+    }
+    // (V = 0) element of a slot, -1: none
+    __device__ __forceinline__ int elem(int s) const {
+        const int i = s & 7, second = s >> 3;
+        if (i < 4) {
+            const int j = l + 64 * i;
+            return j < pairs ? (INTER ? 2 * j + second : j + second * pairs) : -1;
+        }
+        const int e = nrot + l + 64 * (i - 4 + 4 * second);
+        return e < dim ? e : -1;
+    }
+    // element of any slot; V > 0: of a lane that has elements
+    __device__ __forceinline__ int index(int s) const {
+        if constexpr (V > 0) return s < V ? o0 + s : o1 + s - V;
+        else return elem(s);
+    }
+
+    __device__ __forceinline__ void load(float (&v)[NS], const uint16_t *p, bool live) const {
+        if constexpr (V > 0) {
+            uint32_t w[V];
+#pragma unroll
+            for (int i = 0; i < V; i++) w[i] = 0u;
+            if (live && act) {
+                __builtin_memcpy(&w[0], p + o0, 2 * V);
+                __builtin_memcpy(&w[V / 2], p + o1, 2 * V);
+            }
+#pragma unroll
+            for (int i = 0; i < V; i++) {
+                v[2 * i] = bf16_lo(w[i]);
+                v[2 * i + 1] = bf16_hi(w[i]);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < NS; s++) {
+                const int e = elem(s);
+                v[s] = live && e >= 0 ? __uint_as_float((uint32_t)p[e] << 16) : 0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t *p, const float (&v)[NS], bool live) const {
+        if constexpr (V > 0) {
+            uint32_t w[V];
+#pragma unroll
+            for (int i = 0; i < V; i++) w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[2 * i], v[2 * i + 1]}, v2bf));
+            if (live && act) {
+                __builtin_memcpy(p + o0, &w[0], 2 * V);
+                __builtin_memcpy(p + o1, &w[V / 2], 2 * V);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < NS; s++) {
+                const int e = elem(s);
+                const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[s], 0.f}, v2bf));
+                if (live && e >= 0) p[e] = (uint16_t)w;
+            }
+        }
+    }
+    // a weight of the head's elements as fp32, 1 where there is none
+    __device__ __forceinline__ void load_weight(float (&v)[NS], const void *p, bool bf16) const {
+#pragma unroll
+        for (int s = 0; s < NS; s++) v[s] = 1.f;
+        if (!p) return;
+        if (bf16) {
+            load(v, reinterpret_cast<const uint16_t *>(p), true);
+            return;
+        }
+        const float *const q = reinterpret_cast<const float *>(p);
+        if constexpr (V > 0) {
+            if (act) {
+                __builtin_memcpy(&v[0], q + o0, 4 * V);
+                __builtin_memcpy(&v[V], q + o1, 4 * V);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < NS; s++) {
+                const int e = elem(s);
+                v[s] = e >= 0 ? q[e] : 0.f;
+            }
+        }
+    }
+
+    // cosines and sines of the lane's pairs
+    __device__ __forceinline__ void angles(float2 (&cs)[H], const float2 *all) const {
+#pragma unroll
+        for (int i = 0; i < H; i++) {
+            if constexpr (V > 0) cs[i] = all[rot ? V * l + i : 0];
+            else cs[i] = all[i < 4 && l + 64 * i < pairs ? l + 64 * i : 0];
+        }
+    }
+    // v: rotated in place; sign -1: the other way round
+    __device__ __forceinline__ void rotate(float (&v)[NS], const float2 (&cs)[H], float sign) const {
+        const auto turn = [&](float &a, float &b, float2 t) {
+            const float s = sign * t.y, u = __builtin_fmaf(a, t.x, -(b * s)), w = __builtin_fmaf(b, t.x, a * s);
+            a = u;
+            b = w;
+        };
+        if constexpr (V > 0) {
+            if (rot) {
+#pragma unroll
+                for (int i = 0; i < V; i++) turn(v[INTER ? 2 * i : i], v[INTER ? 2 * i + 1 : i + V], cs[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (l + 64 * i < pairs) turn(v[i], v[i + 8], cs[i]);
+        }
+    }
+
+    typedef float f2 __attribute__((ext_vector_type(2)));
+};
+
+// scale * (cos, sin) of every pair's angle at one position, into the wave's part of LDS
+__device__ __forceinline__ void make_angles(float2 *cs, const RopeArgs &a, int64_t token, int lane) {
+    if (a.rot == 0) return;  // there may be no positions
+    const double pos = a.pos64 ? (double)reinterpret_cast<const int64_t *>(a.pos)[token]
+                               : (double)reinterpret_cast<const int32_t *>(a.pos)[token];
+    __builtin_amdgcn_wave_barrier();  // the angles of the token before have been read
+    for (int i = lane; i < a.rot / 2; i += 64) {
+        const double t = pos * a.freqs[i] * 0.15915494309189533577;  // 1 / (2 pi)
+        float s, c;
+        sincospif(2.0f * (float)(t - __builtin_rint(t)), &s, &c);
+        cs[i] = make_float2(c * a.scale, s * a.scale);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Forward.  A token's heads are `passes` passes of 64 / L, queries first; `parts` waves share them, `per` each.
+template <bool NORM, int V, int L, bool INTER>
+__global__ __launch_bounds__(64 * kHW) void k_heads(RopeArgs a, FastDiv parts, int per) {
+    typedef Map<V, L, INTER> M;
+    constexpr int G = 64 / L;
+    __shared__ float2 sCS[kHW][kMaxPairs];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = lane / L;
+    const uint32_t item = blockIdx.x * kHW + wave, tok = parts.div(item);
+    if (tok >= a.tokens) return;  // a whole wave; no barriers of the workgroup below
+    const int p0 = (int)(item - tok * parts.d) * per;
+    const M m(lane, a.dim, a.rot);
+    make_angles(sCS[wave], a, tok, lane);
+    float2 cs[M::H];
+    m.angles(cs, sCS[wave]);
+    const float sign = !NORM && a.inverse ? -1.f : 1.f, rn = 1.0f / (float)a.dim;
+    int base = 0;
+#pragma unroll 1
+    for (int si = 0; si < 2; si++) {
+        const HeadSet &h = a.s[si];
+        const int n = (h.heads + G - 1) / G, lo = max(p0 - base, 0), hi = min(p0 + per - base, n);
+        base += n;
+        if (lo >= hi) continue;
+        float w[M::NS];
+        if constexpr (NORM) m.load_weight(w, h.weight, a.param_bf16);
+        const uint16_t *const px = h.x + tok * h.xt;
+        uint16_t *const po = h.out + tok * h.ot;
+#pragma unroll 2
+        for (int p = lo; p < hi; p++) {
+            const int head = p * G + sub;
+            const bool live = head < h.heads;
+            float v[M::NS];
+            m.load(v, px + head * h.xh, live);
+            if constexpr (NORM) {
+                float sq = 0.f;
+#pragma unroll
+                for (int s = 0; s < M::NS; s++) sq = __builtin_fmaf(v[s], v[s], sq);
+                const float rstd = rsqrt1(__builtin_fmaf(group_sum<L>(sq), rn, a.eps));
+#pragma unroll
+                for (int s = 0; s < M::NS; s++) v[s] = v[s] * rstd * w[s];
+            }
+            m.rotate(v, cs, sign);
+            m.store(po + head * h.oh, v, live);
+        }
+    }
+}
+
+// Backward of the norm and the rotation: a workgroup's waves take every gridDim-th token, all heads.
+template <int V, int L, bool INTER>
+__global__ __launch_bounds__(64 * kHW) void k_heads_bwd(RopeArgs a) {
+    typedef Map<V, L, INTER> M;
+    constexpr int G = 64 / L;
+    __shared__ union {
+        float2 cs[kHW][kMaxPairs];
+        float sum[kHW][2][kHeadMaxDim];
+    } sh;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = lane / L;
+    const M m(lane, a.dim, a.rot);
+    const float rn = 1.0f / (float)a.dim;
+    float acc[2][M::NS];
+#pragma unroll
+    for (int si = 0; si < 2; si++)
+#pragma unroll
+        for (int s = 0; s < M::NS; s++) acc[si][s] = 0.f;
+    for (int64_t tok = (int64_t)blockIdx.x * kHW + wave; tok < a.tokens; tok += (int64_t)gridDim.x * kHW) {
+        make_angles(sh.cs[wave], a, tok, lane);
+        float2 cs[M::H];
+        m.angles(cs, sh.cs[wave]);
+#pragma unroll
+        for (int si = 0; si < 2; si++) {
+            const HeadSet &h = a.s[si];
+            float w[M::NS];
+            m.load_weight(w, h.weight, a.param_bf16);
+            const uint16_t *const px = h.x + tok * h.xt, *const pd = h.dy + tok * h.dt;
+            uint16_t *const po = h.out + tok * h.ot;
+            for (int p = 0; p < h.heads; p += G) {
+                const int head = p + sub;
+                const bool live = head < h.heads;
+                float v[M::NS], u[M::NS];
+                m.load(v, px + head * h.xh, live);
+                m.load(u, pd + head * h.dh, live);
+                m.rotate(u, cs, -1.f);
+                float sq = 0.f, sg = 0.f;
+#pragma unroll
+                for (int s = 0; s < M::NS; s++) {
+                    sq = __builtin_fmaf(v[s], v[s], sq);
+                    sg = __builtin_fmaf(u[s] * w[s], v[s], sg);
+                }
+                const float rstd = live ? rsqrt1(__builtin_fmaf(group_sum<L>(sq), rn, a.eps)) : 0.f;
+                const float mean = group_sum<L>(sg) * rstd * rn;  // of g * xh
+#pragma unroll
+                for (int s = 0; s < M::NS; s++) {
+                    const float xh = v[s] * rstd;
+                    acc[si][s] = __builtin_fmaf(u[s], xh, acc[si][s]);
+                    v[s] = __builtin_fmaf(-xh, mean, u[s] * w[s]) * rstd;
+                }
+                m.store(po + head * h.oh, v, live);
+            }
+        }
+    }
+    if (!a.s[0].dw && !a.s[1].dw) return;
+    __syncthreads();  // the angles are done with
+#pragma unroll
+    for (int si = 0; si < 2; si++)
+#pragma unroll
+        for (int s = 0; s < M::NS; s++) {
+            float v = acc[si][s];
+#pragma unroll
+            for (int o = L; o < 64; o *= 2) v += __shfl_xor(v, o);
+            const int e = m.index(s);
+            if (sub == 0 && m.act && e >= 0) sh.sum[wave][si][e] = v;
+        }
+    __syncthreads();
+    float *const d = a.ws + (int64_t)blockIdx.x * 2 * a.dim;
+    for (int i = threadIdx.x; i < 2 * a.dim; i += 64 * kHW) {
+        const int si = i >= a.dim, e = i - si * a.dim;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kHW; w++) v += sh.sum[w][si][e];
+        d[i] = v;
+    }
+}
+
+// the workgroups' sums: 64 elements of both weights per workgroup, sixteen waves taking every sixteenth chunk
+constexpr int kSW = 16;
+__global__ __launch_bounds__(64 * kSW) void k_heads_dw(const float *ws, int chunks, int dim, float *dwq, float *dwk) {
+    __shared__ float s[kSW][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = blockIdx.x * 64 + lane;
+    float v = 0.f;
+    if (i < 2 * dim)
+        for (int c = wave; c < chunks; c += kSW) v += ws[(int64_t)c * 2 * dim + i];
+    s[wave][lane] = v;
+    __syncthreads();
+    if (wave > 0 || i >= 2 * dim) return;
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSW; w++) v += s[w][lane];
+    float *const out = i < dim ? dwq : dwk;
+    if (out) out[i < dim ? i : i - dim] = v;
+}
+
+int64_t bwd_groups(int64_t tokens) {
+    const int64_t n = (tokens + kHW - 1) / kHW;
+    return n < 1024 ? n : 1024;
+}
+
+template <int V, int L, bool INTER>
+hipError_t launch_as(const RopeArgs &all, int op, hipStream_t s) {
+    if (op == NORM_ROPE_BWD) {
+        hipLaunchKernelGGL((k_heads_bwd<V, L, INTER>), dim3((unsigned)bwd_groups(all.tokens)), dim3(64 * kHW), 0, s, all);
+        return hipGetLastError();
+    }
+    constexpr int G = 64 / L;
+    const int64_t passes = ((int64_t)all.s[0].heads + G - 1) / G + ((int64_t)all.s[1].heads + G - 1) / G;
+    // waves enough to fill the chip, each with as many of a token's passes as that leaves
+    const int64_t want = (8192 + all.tokens - 1) / all.tokens, parts0 = want < passes ? want : passes;
+    const int64_t per = (passes + parts0 - 1) / parts0, parts = (passes + per - 1) / per;
+    const int64_t most = ((int64_t)1 << 25) / parts;  // tokens per launch: waves and threads in 32 bits
+    for (int64_t t = 0; t < all.tokens; t += most) {
+        RopeArgs a = all;
+        a.tokens = all.tokens - t < most ? all.tokens - t : most;
+        a.pos = (const uint8_t *)a.pos + t * (a.pos64 ? 8 : 4);
+        for (HeadSet &h : a.s) {
+            h.x += t * h.xt;
+            h.out += t * h.ot;
+        }
+        const dim3 grid((unsigned)((a.tokens * parts + kHW - 1) / kHW));
+        if (op == ROPE) hipLaunchKernelGGL((k_heads<false, V, L, INTER>), grid, dim3(64 * kHW), 0, s, a, FastDiv((uint32_t)parts), (int)per);
+        else hipLaunchKernelGGL((k_heads<true, V, L, INTER>), grid, dim3(64 * kHW), 0, s, a, FastDiv((uint32_t)parts), (int)per);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <bool INTER>
+hipError_t launch_layout(const RopeArgs &a, int op, hipStream_t s) {
+    if (a.dim % 16 == 0 && a.rot % 16 == 0) {
+        if (a.dim <= 64) return launch_as<8, 4, INTER>(a, op, s);
+        if (a.dim <= 128) return launch_as<8, 8, INTER>(a, op, s);
+        if (a.dim <= 256) return launch_as<8, 16, INTER>(a, op, s);
+        return launch_as<8, 32, INTER>(a, op, s);
+    }
+    if (a.dim % 8 == 0 && a.rot % 8 == 0 && a.dim <= 128) return launch_as<4, 16, INTER>(a, op, s);
+    return launch_as<0, 64, INTER>(a, op, s);
+}
+
+}  // namespace
+
+int64_t heads_workspace(int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t dim) {
+    return heads_q + heads_k > 0 ? bwd_groups(tokens) * 2 * dim : 0;
+}
+
+hipError_t launch_heads(const RopeArgs &a, int op, hipStream_t s) {
+    hipError_t e = hipSuccess;
+    if (a.tokens > 0 && a.s[0].heads + (int64_t)a.s[1].heads > 0)
+        e = a.interleaved ? launch_layout<true>(a, op, s) : launch_layout<false>(a, op, s);
+    if (e != hipSuccess || op != NORM_ROPE_BWD || (!a.s[0].dw && !a.s[1].dw)) return e;
+    const int chunks = a.s[0].heads + (int64_t)a.s[1].heads > 0 ? (int)bwd_groups(a.tokens) : 0;
+    hipLaunchKernelGGL(k_heads_dw, dim3((unsigned)((2 * a.dim + 63) / 64)), dim3(64 * kSW), 0, s, (const float *)a.ws, chunks,
+                       a.dim, a.s[0].dw, a.s[1].dw);
+    return hipGetLastError();
+}
+
+}  // namespace mx
