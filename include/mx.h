@@ -462,6 +462,76 @@ mx_status_t mx_block_gemm_sums(const void *a_codes, int64_t lda, const float *a_
 
 /*
  * ---------------------------------------------------------------------------
+ * Block-128 products by group: a layer of experts, each with a weight of its own.
+ *
+ * Rows (tokens, sorted by expert) are in `groups` groups, given by the ends of
+ * their ranges in DEVICE memory, so that nothing waits for the host to learn them:
+ * group i is the rows from ends[i - 1] (0 for the first) to ends[i] - 1, ends not
+ * decreasing and at most `rows`.  Groups may be empty; rows from the last end on
+ * belong to none, and what is at their place in an output is left as it was.  (An
+ * end below the one before it or above `rows` is taken as these; nothing outside
+ * the buffers is touched whatever ends holds.)  At most 2^16 groups.
+ *
+ * Operands whose reduction dimension is the rows (both of a weight gradient) have
+ * their blocks of 128 start anew at every group: block b of the transposed form is
+ * 128 rows of one group or its last ones, and the columns behind these hold zeros.
+ * mx_block_grouped_cols(rows, groups) columns (a multiple of 128) are enough
+ * whatever the groups; blocks behind the last group's are not written.  (0 for
+ * sizes that the calls refuse.)
+ */
+int64_t mx_block_grouped_cols(int64_t rows, int64_t groups);
+
+/*
+ * mx_block_quantize_grouped -- the transposed form: codes [cols x ld_codes],
+ * ld_codes >= mx_block_grouped_cols(rows, groups); scales [that / 128][ld_scales],
+ * ld_scales >= cols.  mx_block_quantize_grouped_dual writes the row form (as
+ * MX_BLOCK_ROW) from the same read.  Each block as mx_block_quantize gives it.
+ */
+mx_status_t mx_block_quantize_grouped(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx, const int32_t *ends,
+                                      int64_t groups, mx_format_t fmt, void *codes, int64_t ld_codes, float *scales,
+                                      int64_t ld_scales, void *stream);
+mx_status_t mx_block_quantize_grouped_dual(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx,
+                                           const int32_t *ends, int64_t groups, mx_format_t fmt_row, void *codes_row,
+                                           int64_t ld_codes_row, float *scales_row, int64_t ld_scales_row,
+                                           mx_format_t fmt_t, void *codes_t, int64_t ld_codes_t, float *scales_t,
+                                           int64_t ld_scales_t, void *stream);
+
+/*
+ * mx_block_gemm_grouped -- for every row m of group g
+ *     C[m, n] = sum over blocks b of sa[b][m] * sb[g][b][n] * sum_{k in b} A[m, k] * B[g][n, k]
+ * A [rows x K] and C [rows x N] as in mx_block_gemm_sums; B[g] [N x K] with codes at
+ * b_codes + g * ldb_group and scales at b_scales + g * ldsb_group, each as there
+ * (b_tile: in 128 x 128 tiles).  The weights of all groups quantized as one matrix
+ * of groups * N rows, N a multiple of 128, qualify in both forms: with
+ * MX_BLOCK_TILE ldb_group = N * ldb, ldsb_group = N / 128 (ldsb = groups * that);
+ * its transposed form is B for the gradient of A: ldb_group = N, ldsb_group = N /
+ * 128 * ldsb.  Types, sums, accuracy, limits and alignment as in
+ * mx_block_gemm_sums; ldb_group a multiple of 16 is the fast case.  K = 0 writes
+ * zeros to the groups' rows.
+ */
+mx_status_t mx_block_gemm_grouped(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa, mx_format_t fa,
+                                  const void *b_codes, int64_t ldb_group, int64_t ldb, const float *b_scales,
+                                  int64_t ldsb_group, int64_t ldsb, mx_format_t fb, int b_tile, const int32_t *ends,
+                                  int64_t groups, int64_t rows, int64_t N, int64_t K, void *c, mx_out_t out,
+                                  int64_t ldc, mx_sums_t sums, void *stream);
+
+/*
+ * mx_block_gemm_grouped_k -- for every group g, its rows being the reduction dimension
+ *     C[g][m, n] = sum over the blocks b of g of sa[b][m] * sb[b][n] * sum_{k in b} A[m, k] * B[n, k]
+ * A [M x cols] and B [N x cols] as mx_block_quantize_grouped writes them for the same
+ * ends, cols a multiple of 128 that holds all the groups' blocks; scales [cols / 128][M]
+ * and [.. N].  C[g] [M x ldc] at c + g * ldc_group elements, ldc_group >= (M - 1) *
+ * ldc + N.  An empty group's C is zeros.  Types, sums and accuracy as in
+ * mx_block_gemm_sums, K being the group's rows.
+ */
+mx_status_t mx_block_gemm_grouped_k(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa,
+                                    mx_format_t fa, const void *b_codes, int64_t ldb, const float *b_scales,
+                                    int64_t ldsb, mx_format_t fb, const int32_t *ends, int64_t groups, int64_t M,
+                                    int64_t N, int64_t cols, void *c, mx_out_t out, int64_t ldc_group, int64_t ldc,
+                                    mx_sums_t sums, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * The norm in front of a linear layer, forward and backward.
  *
  *   mean = sum_j x_j / cols (0 for MX_NORM_RMS),

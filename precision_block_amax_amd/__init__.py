@@ -3,10 +3,11 @@
 OCP-MX micro-scaling quantization (block 32, E8M0 scales, E4M3 / E5M2 / E2M1
 elements), the fixed-sign 32-point block-Hadamard rotation used on the
 weight-gradient path, and the MX-scaled GEMM; FP8 operands with one fp32 scale
-for each block of 128 (quantizers and product); the norm in front of a
-linear layer (layer norm or RMS norm, forward, straight to a quantized operand,
-and backward); and rotary positions and the norm of each head of queries and
-keys, as hand-written gfx950 HIP kernels behind a C ABI.
+for each block of 128 (quantizers and products, also by groups of rows with a
+weight of their own each); the norm in front of a linear layer (layer norm or
+RMS norm, forward, straight to a quantized operand, and backward); and rotary
+positions and the norm of each head of queries and keys, as hand-written gfx950
+HIP kernels behind a C ABI.
 
 This module only marshals arguments: it checks tensor shapes, dtypes and
 devices, allocates outputs with torch (device memory and streams are all
@@ -27,7 +28,8 @@ __all__ = [
     "E4M3", "E5M2", "E2M1", "MXError", "lib", "library_path", "code_cols",
     "quantize", "quantize_transpose", "hadamard32_quantize", "quantize_dual",
     "quantize_transpose_sr", "quantize_pair", "gemm", "fsdp_payload", "payload_views",
-    "payload_width", "block_quantize", "block_quantize_dual", "block_gemm", "layer_norm",
+    "payload_width", "block_quantize", "block_quantize_dual", "block_gemm", "block_grouped_cols",
+    "block_quantize_grouped", "block_quantize_grouped_dual", "block_gemm_grouped", "block_gemm_grouped_k", "layer_norm",
     "layer_norm_quantize", "layer_norm_backward", "rope_frequencies", "rope", "qk_norm_rope",
     "qk_norm_rope_backward",
 ]
@@ -82,6 +84,17 @@ def lib() -> ctypes.CDLL:
         L.mx_layer_norm_backward.argtypes = [P, i64, P, i64, i64, i64, P, i32, i32, P, P, P, i64, P, P, P, i64, P]
         L.mx_layer_norm_backward_workspace.argtypes = [i64, i64]
         L.mx_layer_norm_backward_workspace.restype = i64
+        L.mx_block_grouped_cols.argtypes = [i64, i64]
+        L.mx_block_grouped_cols.restype = i64
+        L.mx_block_quantize_grouped.argtypes = [P, i64, i64, i64, P, i64, i32, P, i64, P, i64, P]
+        L.mx_block_quantize_grouped_dual.argtypes = [P, i64, i64, i64, P, i64, i32, P, i64, P, i64, i32, P, i64, P, i64, P]
+        L.mx_block_gemm_grouped.argtypes = [P, i64, P, i64, i32, P, i64, i64, P, i64, i64, i32, i32, P, i64, i64, i64, i64, P,
+                                            i32, i64, i32, P]
+        L.mx_block_gemm_grouped_k.argtypes = [P, i64, P, i64, i32, P, i64, P, i64, i32, P, i64, i64, i64, i64, P, i32, i64, i64,
+                                              i32, P]
+        for fn in (L.mx_block_quantize_grouped, L.mx_block_quantize_grouped_dual, L.mx_block_gemm_grouped,
+                   L.mx_block_gemm_grouped_k):
+            fn.restype = ctypes.c_int
         f64 = ctypes.c_double
         heads, rotation = [P, i64, i64, i64] * 2 + [i64, i64], [P, i32, P, i64, i32, f32]
         L.mx_rope_frequencies.argtypes = [i64, f64, i32, f64, f64, f64, f64, P]
@@ -514,6 +527,132 @@ def block_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_codes: torch
                                         b_scales.data_ptr(), ldsb, f_b, 1 if tile else 0, M, N, K, out.data_ptr(),
                                         OUT_BF16 if bf16 else OUT_F32, ldc, 1 if full_sums or not bf16 else 0,
                                         _current(dev)))
+    return out
+
+
+def _ends(ends: torch.Tensor, device) -> int:
+    """the number of groups"""
+    if ends.dtype is not torch.int32 or ends.dim() != 1 or ends.device != device or not ends.is_contiguous():
+        raise ValueError("ends must be contiguous int32 of one dimension on %s" % device)
+    return ends.shape[0]
+
+
+def block_grouped_cols(rows: int, groups: int) -> int:
+    """mx_block_grouped_cols: columns of the transposed form of `rows` rows in `groups` groups"""
+    return lib().mx_block_grouped_cols(rows, groups)
+
+
+def block_quantize_grouped(x: torch.Tensor, ends: torch.Tensor, fmt, out=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """mx_block_quantize_grouped: the transposed form of x [R x C] with blocks of 128 rows that
+    start anew at every group: codes [C x block_grouped_cols(R, groups)], scales [its blocks x C].
+    Group i is the rows ends[i - 1] .. ends[i] - 1 (ends: int32 on the GPU).  A group's last block
+    is filled with zeros; blocks behind the last group's are not written."""
+    rows, cols, ldx = _input(x)
+    f, dev = _fp8(fmt), x.device
+    groups = _ends(ends, dev)
+    k = lib().mx_block_grouped_cols(rows, groups)
+    with _scope(dev, stream):
+        codes, ldc, scales, lds = _block_outputs(dev, cols, k, False, out)
+        _check(lib().mx_block_quantize_grouped(x.data_ptr(), rows, cols, ldx, ends.data_ptr(), groups, f, codes.data_ptr(), ldc,
+                                               scales.data_ptr(), lds, _current(dev)))
+    return codes, scales
+
+
+def block_quantize_grouped_dual(x: torch.Tensor, ends: torch.Tensor, fmt_row, fmt_t, out=None,
+                                stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """mx_block_quantize_grouped_dual: (codes, scales, codes_t, scales_t) from one read of x: the
+    row form as block_quantize(x, fmt_row) and the transposed one as block_quantize_grouped(x,
+    ends, fmt_t).  Rows behind the last group are left out of both."""
+    rows, cols, ldx = _input(x)
+    fr, ft, dev = _fp8(fmt_row), _fp8(fmt_t), x.device
+    groups = _ends(ends, dev)
+    k = lib().mx_block_grouped_cols(rows, groups)
+    with _scope(dev, stream):
+        cr, ldcr, sr, ldsr = _block_outputs(dev, rows, cols, False, None if out is None else out[:2])
+        ct, ldct, st, ldst = _block_outputs(dev, cols, k, False, None if out is None else out[2:])
+        _check(lib().mx_block_quantize_grouped_dual(x.data_ptr(), rows, cols, ldx, ends.data_ptr(), groups, fr, cr.data_ptr(),
+                                                    ldcr, sr.data_ptr(), ldsr, ft, ct.data_ptr(), ldct, st.data_ptr(), ldst,
+                                                    _current(dev)))
+    return cr, sr, ct, st
+
+
+def _stacked(t: torch.Tensor, dtype: torch.dtype, groups: int, rows: int, width: int, device, what: str) -> Tuple[int, int]:
+    """group and row strides (elements) of a [groups x rows x width] tensor with contiguous rows"""
+    if t.dtype is not dtype or t.shape != (groups, rows, width) or t.device != device:
+        raise ValueError("%s must be %s of shape (%d, %d, %d) on %s" % (what, dtype, groups, rows, width, device))
+    lg, ld, step = t.stride()
+    if step != 1 and width > 1 and t.numel():
+        raise ValueError("the rows of %s must be contiguous" % what)
+    ld = ld if rows > 1 else width
+    return (lg if groups > 1 else rows * ld), ld
+
+
+def block_gemm_grouped(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_codes: torch.Tensor, b_scales: torch.Tensor, fb,
+                       ends: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                       stream=None, full_sums: bool = False) -> torch.Tensor:
+    """mx_block_gemm_grouped: C[R x N] with rows ends[i - 1] .. ends[i] - 1 of C = A . B[i]^T.  A [R x K]
+    in "row" form, B [groups x N x K] with scales [groups x ceil(K/128) x ceil(N/128)] (tiles) or
+    [.. x N]; any strides with contiguous rows, so the forms that block_quantize_dual gives of all
+    weights as one [groups * N x K] matrix may be viewed as B for the product and for its gradient
+    (include/mx.h).  Rows of C behind the last end are left as they are.  out_dtype and full_sums
+    as in block_gemm."""
+    f_a, f_b = _fp8(fa), _fp8(fb)
+    if a_codes.dim() != 2 or a_scales.dim() != 2 or b_codes.dim() != 3 or b_scales.dim() != 3 or not a_codes.is_cuda:
+        raise ValueError("expected a 2-D A and a 3-D B on a GPU")
+    dev = a_codes.device
+    groups = _ends(ends, dev)
+    (M, K), N = a_codes.shape, b_codes.shape[1]
+    if out_dtype is not _BF16 and out_dtype is not _F32:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    kb, tiles = _cdiv(K, BLOCK), _cdiv(N, BLOCK)
+    tile = tiles != N and b_scales.shape[2] == tiles
+    lda = _rows_of(a_codes, _U8, M, K, dev, "A's codes")
+    ldsa = _rows_of(a_scales, _F32, kb, M, dev, "A's scales")
+    ldbg, ldb = _stacked(b_codes, _U8, groups, N, K, dev, "B's codes")
+    ldsbg, ldsb = _stacked(b_scales, _F32, groups, kb, tiles if tile else N, dev, "B's scales")
+    ldc = N if out is None else _rows_of(out, out_dtype, M, N, dev, "out")
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        bf16 = out_dtype is _BF16
+        _check(lib().mx_block_gemm_grouped(a_codes.data_ptr(), lda, a_scales.data_ptr(), ldsa, f_a, b_codes.data_ptr(), ldbg, ldb,
+                                           b_scales.data_ptr(), ldsbg, ldsb, f_b, 1 if tile else 0, ends.data_ptr(), groups, M,
+                                           N, K, out.data_ptr(), OUT_BF16 if bf16 else OUT_F32, ldc,
+                                           1 if full_sums or not bf16 else 0, _current(dev)))
+    return out
+
+
+def block_gemm_grouped_k(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_codes: torch.Tensor, b_scales: torch.Tensor, fb,
+                         ends: torch.Tensor, out_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
+                         stream=None, full_sums: bool = False) -> torch.Tensor:
+    """mx_block_gemm_grouped_k: C[groups x M x N], C[i] = A . B^T over the columns of group i, for A
+    [M x cols] and B [N x cols] as block_quantize_grouped gives them for the same ends: the
+    groups' weight gradients.  An empty group's C is zeros.  out_dtype and full_sums as in
+    block_gemm."""
+    f_a, f_b = _fp8(fa), _fp8(fb)
+    if a_codes.dim() != 2 or b_codes.dim() != 2 or a_scales.dim() != 2 or b_scales.dim() != 2 or not a_codes.is_cuda:
+        raise ValueError("expected 2-D operands on a GPU")
+    dev = a_codes.device
+    groups = _ends(ends, dev)
+    (M, K), N = a_codes.shape, b_codes.shape[0]
+    if b_codes.shape[1] != K:
+        raise ValueError("A and B disagree on the columns")
+    if out_dtype is not _BF16 and out_dtype is not _F32:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    kb = _cdiv(K, BLOCK)
+    lda = _rows_of(a_codes, _U8, M, K, dev, "A's codes")
+    ldb = _rows_of(b_codes, _U8, N, K, dev, "B's codes")
+    ldsa = _rows_of(a_scales, _F32, kb, M, dev, "A's scales")
+    ldsb = _rows_of(b_scales, _F32, kb, N, dev, "B's scales")
+    ldcg, ldc = (M * N, N) if out is None else _stacked(out, out_dtype, groups, M, N, dev, "out")
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((groups, M, N), dtype=out_dtype, device=dev)
+        bf16 = out_dtype is _BF16
+        _check(lib().mx_block_gemm_grouped_k(a_codes.data_ptr(), lda, a_scales.data_ptr(), ldsa, f_a, b_codes.data_ptr(), ldb,
+                                             b_scales.data_ptr(), ldsb, f_b, ends.data_ptr(), groups, M, N, K, out.data_ptr(),
+                                             OUT_BF16 if bf16 else OUT_F32, ldcg, ldc, 1 if full_sums or not bf16 else 0,
+                                             _current(dev)))
     return out
 
 

@@ -12,7 +12,7 @@ namespace {
 
 using namespace mx;
 
-constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int64_t kMaxDim = (int64_t)1 << 31, kMaxGroups = 1 << 16;
 
 bool fp8(int f) { return f == MX_E4M3 || f == MX_E5M2; }
 bool type_ok(int t) { return t == MX_OUT_F32 || t == MX_OUT_BF16; }
@@ -116,6 +116,46 @@ mx_status_t block_gemm(const void *a_codes, int64_t lda, const float *a_scales, 
     return launched(launch_block_gemm(g, fa, fb, b_tile != 0, sums == MX_SUMS_FP8, (hipStream_t)stream));
 }
 
+// the columns that the transposed form of `rows` rows may take
+int64_t grouped_cols(int64_t rows, int64_t groups) { return rows > 0 && groups > 0 ? grouped_units(rows, groups, kBlk) * kBlk : 0; }
+
+mx_status_t block_quantize_grouped(const void *x, int64_t rows, int64_t cols, int64_t ldx, const int32_t *ends,
+                                   int64_t groups, const BlockForm *row, const BlockForm &tr, void *stream) {
+    if (rows < 0 || cols < 0 || ldx < cols || groups < 0) return MX_ERR_INVALID_ARG;
+    const bool none = rows == 0 || groups == 0;
+    if (!none && (rows >= kMaxDim || cols >= kMaxDim || groups > kMaxGroups)) return MX_ERR_UNSUPPORTED;
+    const int64_t k = grouped_cols(rows, groups);
+    Range r[6];
+    mx_status_t st;
+    if (row && (st = check_form(none ? 0 : rows, cols, false, row->fmt, row->codes, row->ld_codes, row->scales, row->ld_scales,
+                                r + 4)) != MX_OK)
+        return st;
+    if ((st = check_form(cols, k, false, tr.fmt, tr.codes, tr.ld_codes, tr.scales, tr.ld_scales, r + 2)) != MX_OK) return st;
+    if (none || cols == 0) return MX_OK;
+    if (!x || !ends) return MX_ERR_INVALID_ARG;
+    r[0] = rows_at(x, rows, ldx, cols, 2);
+    r[1] = run(ends, groups * 4);
+    if ((st = check_ranges(r, row ? 6 : 4, 2)) != MX_OK) return st;
+    if (k / kBlk * blocks(cols) >= ((int64_t)1 << 24)) return MX_ERR_UNSUPPORTED;  // workgroups, as block_quantize
+    if ((st = check_device()) != MX_OK) return st;
+    const BlockForm no_row{nullptr, 0, nullptr, 0, 0};
+    return launched(launch_block_quantize_grouped((const uint16_t *)x, rows, cols, ldx, ends, (int)groups, row ? *row : no_row,
+                                                  tr, (hipStream_t)stream));
+}
+
+// bytes of `groups` pieces of n bytes, one every `step` bytes, as one extent
+Range pieces(const void *p, int64_t groups, int64_t step, int64_t n) {
+    if (groups <= 0 || n <= 0) return run(p, n < 0 ? -1 : 0);
+    if (groups > 1 && step > (INT64_MAX - n) / (groups - 1)) return run(p, -1);
+    return run(p, (groups - 1) * step + n);
+}
+
+mx_status_t check_grouped(int64_t groups, int fa, int fb, int out, int sums) {
+    if (groups < 0 || !fp8(fa) || !fp8(fb) || !type_ok(out)) return MX_ERR_INVALID_ARG;
+    if (sums != MX_SUMS_F32 && (sums != MX_SUMS_FP8 || out != MX_OUT_BF16)) return MX_ERR_INVALID_ARG;
+    return MX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -155,6 +195,94 @@ mx_status_t mx_block_gemm_sums(const void *a_codes, int64_t lda, const float *a_
                                mx_sums_t sums, void *stream) {
     return block_gemm(a_codes, lda, a_scales, ldsa, raw(fa), b_codes, ldb, b_scales, ldsb, raw(fb), b_tile, M, N, K, c,
                       raw(out), ldc, raw(sums), stream);
+}
+
+int64_t mx_block_grouped_cols(int64_t rows, int64_t groups) {
+    return rows >= kMaxDim || groups > kMaxGroups ? 0 : grouped_cols(rows, groups);
+}
+
+mx_status_t mx_block_quantize_grouped(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx, const int32_t *ends,
+                                      int64_t groups, mx_format_t fmt, void *codes, int64_t ld_codes, float *scales,
+                                      int64_t ld_scales, void *stream) {
+    const BlockForm t{(uint8_t *)codes, ld_codes, scales, ld_scales, raw(fmt)};
+    return block_quantize_grouped(x_bf16, rows, cols, ldx, ends, groups, nullptr, t, stream);
+}
+
+mx_status_t mx_block_quantize_grouped_dual(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx, const int32_t *ends,
+                                           int64_t groups, mx_format_t fmt_row, void *codes_row, int64_t ld_codes_row,
+                                           float *scales_row, int64_t ld_scales_row, mx_format_t fmt_t, void *codes_t,
+                                           int64_t ld_codes_t, float *scales_t, int64_t ld_scales_t, void *stream) {
+    const BlockForm r{(uint8_t *)codes_row, ld_codes_row, scales_row, ld_scales_row, raw(fmt_row)};
+    const BlockForm t{(uint8_t *)codes_t, ld_codes_t, scales_t, ld_scales_t, raw(fmt_t)};
+    return block_quantize_grouped(x_bf16, rows, cols, ldx, ends, groups, &r, t, stream);
+}
+
+mx_status_t mx_block_gemm_grouped(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa, mx_format_t fa,
+                                  const void *b_codes, int64_t ldb_group, int64_t ldb, const float *b_scales,
+                                  int64_t ldsb_group, int64_t ldsb, mx_format_t fb, int b_tile, const int32_t *ends,
+                                  int64_t groups, int64_t rows, int64_t N, int64_t K, void *c, mx_out_t out, int64_t ldc,
+                                  mx_sums_t sums, void *stream) {
+    const int f_a = raw(fa), f_b = raw(fb), o = raw(out), su = raw(sums);
+    mx_status_t st = check_grouped(groups, f_a, f_b, o, su);
+    if (st != MX_OK) return st;
+    if (rows < 0 || N < 0 || K < 0 || (b_tile != 0 && b_tile != 1)) return MX_ERR_INVALID_ARG;
+    const int64_t nb = b_tile ? blocks(N) : N;
+    if (lda < K || ldb < K || ldsa < rows || ldsb < nb || ldc < N || ldb_group < 0 || ldsb_group < 0) return MX_ERR_INVALID_ARG;
+    if (rows == 0 || N == 0 || groups == 0) return MX_OK;
+    if (!c || !ends || (K > 0 && (!a_codes || !a_scales || !b_codes || !b_scales))) return MX_ERR_INVALID_ARG;
+    const Range one = rows_at(b_codes, N, ldb, K, 1), scale = rows_at(b_scales, blocks(K), ldsb, nb, 4);
+    if (ldsb_group > INT64_MAX / 4) return MX_ERR_INVALID_ARG;
+    const Range r[6] = {rows_at(a_codes, rows, lda, K, 1), rows_at(a_scales, blocks(K), ldsa, rows, 4),
+                        pieces(b_codes, groups, ldb_group, one.n), pieces(b_scales, groups, ldsb_group * 4, scale.n),
+                        run(ends, groups > INT64_MAX / 4 ? -1 : groups * 4),
+                        rows_at(c, rows, ldc, N, o == MX_OUT_BF16 ? 2 : 4)};
+    if ((st = check_ranges(r, 6, 5)) != MX_OK) return st;
+    if (rows >= kMaxDim || N >= kMaxDim || K > kMaxDim - kBlk || groups > kMaxGroups ||
+        grouped_units(rows, groups, kBlk) * blocks(N) >= ((int64_t)1 << 22))
+        return MX_ERR_UNSUPPORTED;
+    if ((st = check_device()) != MX_OK) return st;
+    GroupedGemmArgs g{};
+    static_cast<BlockGemmArgs &>(g) = {(const uint8_t *)a_codes, (const uint8_t *)b_codes, a_scales, b_scales, c, lda, ldb,
+                                       ldsa, ldsb, ldc, (int)rows, (int)N, (int)K, o == MX_OUT_BF16, 0, 0};
+    g.ends = ends;
+    g.groups = (int)groups;
+    g.rows = (int)rows;
+    g.ldbg = ldb_group;
+    g.ldsbg = ldsb_group;
+    return launched(launch_block_gemm_grouped(g, f_a, f_b, b_tile != 0, su == MX_SUMS_FP8, (hipStream_t)stream));
+}
+
+mx_status_t mx_block_gemm_grouped_k(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa, mx_format_t fa,
+                                    const void *b_codes, int64_t ldb, const float *b_scales, int64_t ldsb, mx_format_t fb,
+                                    const int32_t *ends, int64_t groups, int64_t M, int64_t N, int64_t cols, void *c,
+                                    mx_out_t out, int64_t ldc_group, int64_t ldc, mx_sums_t sums, void *stream) {
+    const int f_a = raw(fa), f_b = raw(fb), o = raw(out), su = raw(sums);
+    mx_status_t st = check_grouped(groups, f_a, f_b, o, su);
+    if (st != MX_OK) return st;
+    if (M < 0 || N < 0 || cols < 0 || cols % kBlk != 0) return MX_ERR_INVALID_ARG;
+    if (lda < cols || ldb < cols || ldsa < M || ldsb < N || ldc < N) return MX_ERR_INVALID_ARG;
+    if (M == 0 || N == 0 || groups == 0) return MX_OK;
+    if (!c || !ends || (cols > 0 && (!a_codes || !a_scales || !b_codes || !b_scales))) return MX_ERR_INVALID_ARG;
+    const int64_t size = o == MX_OUT_BF16 ? 2 : 4;
+    const Range one = rows_at(c, M, ldc, N, size);
+    if (one.n < 0 || (groups > 1 && (ldc_group < one.n / size || ldc_group > INT64_MAX / size))) return MX_ERR_INVALID_ARG;
+    const Range r[6] = {rows_at(a_codes, M, lda, cols, 1), rows_at(a_scales, cols / kBlk, ldsa, M, 4),
+                        rows_at(b_codes, N, ldb, cols, 1), rows_at(b_scales, cols / kBlk, ldsb, N, 4),
+                        run(ends, groups > INT64_MAX / 4 ? -1 : groups * 4),
+                        groups > 1 ? pieces(c, groups, ldc_group * size, one.n) : one};
+    if ((st = check_ranges(r, 6, 5)) != MX_OK) return st;
+    if (M >= kMaxDim || N >= kMaxDim || cols >= kMaxDim || groups > kMaxGroups ||
+        blocks(M) * blocks(N) >= ((int64_t)1 << 22) / groups)
+        return MX_ERR_UNSUPPORTED;
+    if ((st = check_device()) != MX_OK) return st;
+    GroupedGemmArgs g{};
+    static_cast<BlockGemmArgs &>(g) = {(const uint8_t *)a_codes, (const uint8_t *)b_codes, a_scales, b_scales, c, lda, ldb,
+                                       ldsa, ldsb, ldc, (int)M, (int)N, (int)cols, o == MX_OUT_BF16, 0, 0};
+    g.ends = ends;
+    g.groups = (int)groups;
+    g.rows = (int)cols;
+    g.ldcg = groups > 1 ? ldc_group : 0;
+    return launched(launch_block_gemm_grouped_k(g, f_a, f_b, su == MX_SUMS_FP8, (hipStream_t)stream));
 }
 
 mx_status_t mx_layer_norm(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx, const void *weight,

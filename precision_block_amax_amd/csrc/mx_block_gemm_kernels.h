@@ -23,11 +23,53 @@
 // data without cancellation.  Both to bf16, FP8 and fp32 sums: 8192 x 6144 x 4096
 // 187 and 367 us, 1000 x 4096 x 28672 157 and 225, 48 x 4096 x 14336 16.0 and 16.9.
 #pragma once
+#include "mx_block_group.h"
 #include "mx_block_internal.h"
 #include "mx_gemm_kernels.h"
 
 namespace mx {
 namespace {
+
+// Groups (GRP): none, or a workgroup finds its own group and tile and then works on that group's product alone, its
+// rows (ROWS) or its columns (COLS) as the whole of the operands.
+enum Grouping : int { NOT = 0, ROWS = 1, COLS = 2 };
+template <int GRP>
+using ArgsOf = std::conditional_t<GRP == NOT, BlockGemmArgs, GroupedGemmArgs>;
+
+// The tile of C, PM rows each, that this workgroup computes, g made the product of its group; false: none is left for it.
+template <int GRP, int PM>
+__device__ __forceinline__ bool take_tile(ArgsOf<GRP> &g, int &tm, int &tn) {
+    const auto add = [&](auto *&p, int64_t n) { p += n; };
+    if constexpr (GRP == NOT) {
+        tile_index(g.tiles_m, g.tiles_n, tm, tn);
+    } else if constexpr (GRP == ROWS) {
+        GroupChunk<PM> chunk;
+        const int tiles = group_units(chunk, g.ends, g.groups, g.rows);
+        if ((int)blockIdx.x >= tiles * g.tiles_n) return false;
+        tile_index(tiles, g.tiles_n, tm, tn);
+        const Group e = group_of_unit(chunk, g.ends, g.groups, g.rows, tm);
+        tm -= e.first;
+        add(g.a, e.start * g.lda);
+        add(g.as, e.start);
+        add(g.b, e.index * g.ldbg);
+        add(g.bs, e.index * g.ldsbg);
+        g.c = (uint8_t *)g.c + e.start * g.ldc * (g.c_bf16 ? 2 : 4);
+        g.M = e.count;
+    } else {
+        const int per = g.tiles_m * g.tiles_n, index = (int)blockIdx.x / per;
+        tile_index_of((int)blockIdx.x - index * per, g.tiles_m, g.tiles_n, tm, tn);
+        const Group e = group_number<kBlk>(g.ends, g.groups, g.rows, index);
+        // ends that the operands were not made with must not lead past them
+        const int blocks = g.K / kBlk, first = min(e.first, blocks);
+        add(g.a, (int64_t)first * kBlk);
+        add(g.b, (int64_t)first * kBlk);
+        add(g.as, first * g.ldsa);
+        add(g.bs, first * g.ldsb);
+        g.c = (uint8_t *)g.c + index * g.ldcg * (g.c_bf16 ? 2 : 4);
+        g.K = min((e.count + kBlk - 1) / kBlk, blocks - first) * kBlk;
+    }
+    return true;
+}
 
 // four consecutive columns of row m, starting at n
 template <bool FP8SUMS>
@@ -53,6 +95,16 @@ __device__ __forceinline__ void block_store4(const BlockGemmArgs &g, int m, int 
             for (int e = 0; e < 3; e++)  // constant indices: v is in registers
                 if (e < left) p[e] = v[e];
         }
+    }
+}
+
+// C = 0 in a PM x PN tile, for a group without columns
+template <int PM, int PN, int THREADS>
+__device__ __forceinline__ void zero_tile(const BlockGemmArgs &g, int m0, int n0) {
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = threadIdx.x; i < PM * PN / 4; i += THREADS) {
+        const int n = n0 + i % (PN / 4) * 4;
+        if (n < g.N) block_store4<false>(g, m0 + i / (PN / 4), n, zero);
     }
 }
 
@@ -157,15 +209,16 @@ __device__ __forceinline__ uint4 load16(const uint8_t *p, int n) {
     return v;
 }
 
-template <int FA, int FB, bool BT, bool FP8SUMS>
-__global__ __launch_bounds__(GNT, FP8SUMS ? 2 : 1) void k_block_gemm(BlockGemmArgs g) {
+template <int FA, int FB, bool BT, bool FP8SUMS, int GRP>
+__global__ __launch_bounds__(GNT, FP8SUMS ? 2 : 1) void k_block_gemm(ArgsOf<GRP> g) {
     __shared__ __attribute__((aligned(16))) uint8_t sA[2][GB * kBlk], sB[2][GB * kBlk];
     __shared__ __attribute__((aligned(16))) float sS[2][2 * GB];  // A's rows, B's rows
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1, l32 = lane & 31, h = lane >> 5;
     int tm, tn;
-    tile_index(g.tiles_m, g.tiles_n, tm, tn);
+    if (!take_tile<GRP, GB>(g, tm, tn)) return;
     const int m0 = tm * GB, n0 = tn * GB;
+    if (GRP == COLS && g.K == 0) return zero_tile<GB, GB, GNT>(g, m0, n0);
     const int nk = (g.K + kBlk - 1) / kBlk;
 
     uint4 ra[4], rb[4];
@@ -294,8 +347,8 @@ struct Cfg128x128Far : Cfg128x128 { static constexpr bool PF = true; };
 // from registers (a branch for it in the loop made the compiler spill: up to 200 registers).  256 x 256 tiles spill
 // 48 registers there, 24 instructions after the loop and none in it: 8192 x 6144 x 4095 to bf16 217 us beside 194 of
 // 4096; 4104 238, rows of 4112 bytes, whose 128 of a stage lie in two lines.
-template <int FA, int FB, bool BT, bool FP8SUMS, class CFG, bool RAG>
-__global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN * CFG::KG / 4) void k_block_gemm_pipe(BlockGemmArgs g) {
+template <int FA, int FB, bool BT, bool FP8SUMS, class CFG, bool RAG, int GRP>
+__global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN * CFG::KG / 4) void k_block_gemm_pipe(ArgsOf<GRP> g) {
     constexpr int TI = CFG::TI, WM = CFG::WM, WN = CFG::WN, NS = 2, KG = CFG::KG;
     static_assert(KG == 1 || (KG == 2 && TI == 2), "the join swaps two rows of tiles");
     constexpr int NW = WM * WN, PM = WM * TI * 32, PN = WN * 64;
@@ -319,8 +372,9 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
     float *const sS = sScales + grp * SR * (PM + PN);
     const int wm = wave / WN, wn = wave % WN, l32 = lane & 31, h = lane >> 5;
     int tm, tn;
-    tile_index(g.tiles_m, g.tiles_n, tm, tn);
+    if (!take_tile<GRP, PM>(g, tm, tn)) return;
     const int m0 = tm * PM, n0 = tn * PN;
+    if (GRP == COLS && g.K == 0) return zero_tile<PM, PN, 64 * NW * KG>(g, m0, n0);
     const int K = RAG ? g.K & ~15 : g.K, nk = (K + kBlk - 1) / kBlk, ktail = K - (nk - 1) * kBlk;
     const int mrows = min(PM, g.M - m0), nrows = min(PN, g.N - n0);
     const int lda = (int)g.lda, ldb = (int)g.ldb;
@@ -694,8 +748,9 @@ __device__ __forceinline__ v4f few_block(const Frag2 &a, const Frag2 &b) {
 
 // AI: loads of 8 rows of A; with an odd AI the rest of the matrix instruction's 16 rows is whatever LDS
 // holds, and reaches only rows of C that do not exist
-template <int FA, int FB, bool BT, bool FP8SUMS, int AI, int NT, int S>
-__global__ __launch_bounds__(64 * DW) void k_block_gemm_few(BlockGemmArgs g) {
+template <int FA, int FB, bool BT, bool FP8SUMS, int AI, int NT, int S, int GRP>
+__global__ __launch_bounds__(64 * DW) void k_block_gemm_few(ArgsOf<GRP> g) {
+    static_assert(GRP != COLS, "a group without columns has no block");
     constexpr int MT = (AI + 1) / 2, DM = 16 * MT, DN = 16 * NT, JP = DN + 4;
     constexpr int OB = MT * 2048, OS = OB + NT * 2048, BLK = OS + 512;  // a block: A's rows, B's, scales of A, of B
     constexpr int LPB = AI + 2 * NT + 2;                                // loads per block
@@ -704,7 +759,7 @@ __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(BlockGemmArgs g) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, h = lane >> 4;
     int tm, tn;
-    tile_index(g.tiles_m, g.tiles_n, tm, tn);
+    if (!take_tile<GRP, 8 * AI>(g, tm, tn)) return;
     const int m0 = tm * 8 * AI, n0 = tn * DN;
     const int nk = (g.K + kBlk - 1) / kBlk, ktail = g.K - (nk - 1) * kBlk;
     const int lda = (int)g.lda, ldb = (int)g.ldb, mrows = min(8 * AI, g.M - m0), nrows = min(DN, g.N - n0);
@@ -837,7 +892,7 @@ template <int FA, int FB, bool BT, bool FP8SUMS, int AI, int NT, int S>
 hipError_t launch_block_gemm_few(BlockGemmArgs g, hipStream_t s) {
     g.tiles_m = (g.M + 8 * AI - 1) / (8 * AI);
     g.tiles_n = (g.N + 16 * NT - 1) / (16 * NT);
-    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, BT, FP8SUMS, AI, NT, S>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
+    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, BT, FP8SUMS, AI, NT, S, NOT>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
                        dim3(64 * DW), 0, s, g);
     return hipGetLastError();
 }
@@ -847,7 +902,7 @@ hipError_t launch_block_gemm_pipe(BlockGemmArgs g, hipStream_t s) {
     constexpr int PM = CFG::WM * CFG::TI * 32, PN = CFG::WN * 64;
     g.tiles_m = (g.M + PM - 1) / PM;
     g.tiles_n = (g.N + PN - 1) / PN;
-    hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, FP8SUMS, CFG, RAG>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
+    hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, FP8SUMS, CFG, RAG, NOT>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
                        dim3(64 * CFG::WM * CFG::WN * CFG::KG), 0, s, g);
     return hipGetLastError();
 }
@@ -872,7 +927,7 @@ hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
     const auto general = [&]() {
         g.tiles_m = (g.M + GB - 1) / GB;
         g.tiles_n = (g.N + GB - 1) / GB;
-        hipLaunchKernelGGL((k_block_gemm<FA, FB, BT, FP8SUMS>), dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(GNT), 0, s, g);
+        hipLaunchKernelGGL((k_block_gemm<FA, FB, BT, FP8SUMS, NOT>), dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(GNT), 0, s, g);
         return hipGetLastError();
     };
     if (!aligned) return general();
@@ -910,6 +965,93 @@ hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
         if (2 * r256 <= r128) return launch_block_gemm_k<FA, FB, BT, FP8SUMS, Cfg256x128>(g, s);
     }
     return launch_block_gemm_k<FA, FB, BT, FP8SUMS, Cfg128x128>(g, s);
+}
+
+// ---------------------------------------------------------------------------
+// Products by group.  The host does not know the groups' sizes, so the grid is made for the most tiles that they can
+// take, and workgroups without one end at once (they are the last ones).
+
+template <int FA, int FB, bool BT, bool FP8SUMS, int AI, int NT, int S>
+hipError_t launch_grouped_few(GroupedGemmArgs g, hipStream_t s) {
+    g.tiles_n = (g.N + 16 * NT - 1) / (16 * NT);
+    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, BT, FP8SUMS, AI, NT, S, ROWS>),
+                       dim3((unsigned)(grouped_units(g.M, g.groups, 8 * AI) * g.tiles_n)), dim3(64 * DW), 0, s, g);
+    return hipGetLastError();
+}
+
+template <int FA, int FB, bool BT, bool FP8SUMS, class CFG>
+hipError_t launch_grouped_rows(GroupedGemmArgs g, hipStream_t s) {
+    constexpr int PM = CFG::WM * CFG::TI * 32, PN = CFG::WN * 64;
+    g.tiles_n = (g.N + PN - 1) / PN;
+    const dim3 grid((unsigned)(grouped_units(g.M, g.groups, PM) * g.tiles_n)), block(64 * CFG::WM * CFG::WN * CFG::KG);
+    if (g.K % 16) hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, FP8SUMS, CFG, true, ROWS>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, BT, FP8SUMS, CFG, false, ROWS>), grid, block, 0, s, g);
+    return hipGetLastError();
+}
+
+template <int FA, int FB, bool FP8SUMS, class CFG>
+hipError_t launch_grouped_cols(GroupedGemmArgs g, hipStream_t s) {
+    constexpr int PM = CFG::WM * CFG::TI * 32, PN = CFG::WN * 64;
+    g.tiles_m = (g.M + PM - 1) / PM;
+    g.tiles_n = (g.N + PN - 1) / PN;
+    hipLaunchKernelGGL((k_block_gemm_pipe<FA, FB, false, FP8SUMS, CFG, false, COLS>),
+                       dim3((unsigned)(g.tiles_m * g.tiles_n * g.groups)), dim3(64 * CFG::WM * CFG::WN * CFG::KG), 0, s, g);
+    return hipGetLastError();
+}
+
+// rows of whole aligned 16 bytes, offsets in 31 bits (what all but the general kernel need); nk blocks of K
+inline bool grouped_aligned(const GroupedGemmArgs &g, int64_t nk) {
+    const int64_t lim = (int64_t)1 << 31, lim_code = lim / 256, lim_scale = (lim / 4 - 257) / (nk > 0 ? nk : 1);
+    return g.lda % 16 == 0 && g.ldb % 16 == 0 && g.ldbg % 16 == 0 && (uintptr_t)g.a % 16 == 0 && (uintptr_t)g.b % 16 == 0 &&
+           g.lda < lim_code && g.ldb < lim_code && g.ldsa <= lim_scale && g.ldsb <= lim_scale;
+}
+
+template <int FA, int FB, bool BT, bool FP8SUMS>
+hipError_t launch_grouped_as(GroupedGemmArgs g, hipStream_t s) {
+    const int64_t mean = (g.M + g.groups - 1) / g.groups;  // rows of a group
+    if (g.M == 1) g.lda = (g.K + 15) / 16 * 16;  // a single row has no stride
+    if (g.N == 1) g.ldb = (g.K + 15) / 16 * 16;
+    if (!grouped_aligned(g, (g.K + kBlk - 1) / kBlk) || g.K < 16) {
+        g.tiles_n = (g.N + GB - 1) / GB;
+        hipLaunchKernelGGL((k_block_gemm<FA, FB, BT, FP8SUMS, ROWS>),
+                           dim3((unsigned)(grouped_units(g.M, g.groups, GB) * g.tiles_n)), dim3(GNT), 0, s, g);
+        return hipGetLastError();
+    }
+    // (tiles of 8 rows and 16 columns, counted in 32 bits together with their threads)
+    if (grouped_units(g.M, g.groups, 8) * ((g.N + 15) / 16) < (int64_t)1 << 22) {
+        if (mean <= 8) return launch_grouped_few<FA, FB, BT, FP8SUMS, 1, 1, 2>(g, s);
+        if (mean <= 16) return launch_grouped_few<FA, FB, BT, FP8SUMS, 2, 1, 2>(g, s);
+        if (mean <= 32) return launch_grouped_few<FA, FB, BT, FP8SUMS, 4, 1, 3>(g, s);
+    }
+    if constexpr (FP8SUMS && BT) {
+        if (mean >= 512) return launch_grouped_rows<FA, FB, BT, FP8SUMS, Cfg256x256>(g, s);
+    } else {
+        if (mean >= 512) return launch_grouped_rows<FA, FB, BT, FP8SUMS, Cfg256x128>(g, s);
+    }
+    return launch_grouped_rows<FA, FB, BT, FP8SUMS, Cfg128x128>(g, s);
+}
+
+template <int FA, int FB, bool FP8SUMS>
+hipError_t launch_grouped_k_as(GroupedGemmArgs g, hipStream_t s) {
+    if (!grouped_aligned(g, g.K / kBlk)) {
+        g.tiles_m = (g.M + GB - 1) / GB;
+        g.tiles_n = (g.N + GB - 1) / GB;
+        hipLaunchKernelGGL((k_block_gemm<FA, FB, false, FP8SUMS, COLS>), dim3((unsigned)(g.tiles_m * g.tiles_n * g.groups)),
+                           dim3(GNT), 0, s, g);
+        return hipGetLastError();
+    }
+    if (g.M > 128) return launch_grouped_cols<FA, FB, FP8SUMS, Cfg256x128>(g, s);
+    return launch_grouped_cols<FA, FB, FP8SUMS, Cfg128x128>(g, s);
+}
+
+template <int FA, int FB>
+hipError_t launch_block_gemm_grouped_fmt(const GroupedGemmArgs &g, bool bt, bool fp8_sums, hipStream_t s) {
+    if (bt) return fp8_sums ? launch_grouped_as<FA, FB, true, true>(g, s) : launch_grouped_as<FA, FB, true, false>(g, s);
+    return fp8_sums ? launch_grouped_as<FA, FB, false, true>(g, s) : launch_grouped_as<FA, FB, false, false>(g, s);
+}
+template <int FA, int FB>
+hipError_t launch_block_gemm_grouped_k_fmt(const GroupedGemmArgs &g, bool fp8_sums, hipStream_t s) {
+    return fp8_sums ? launch_grouped_k_as<FA, FB, true>(g, s) : launch_grouped_k_as<FA, FB, false>(g, s);
 }
 
 template <int FA, int FB>

@@ -23,6 +23,10 @@ struct BlockForm {
 // At least one of them is wanted; rows, cols > 0.
 hipError_t launch_block_quantize(const uint16_t *x, int64_t rows, int64_t cols, int64_t ldx, bool tile,
                                  const BlockForm &row, const BlockForm &tr, hipStream_t stream);
+// The transposed form with blocks that start anew at every group of rows, and the row form (its codes nullptr: not
+// written) of the groups' rows.
+hipError_t launch_block_quantize_grouped(const uint16_t *x, int64_t rows, int64_t cols, int64_t ldx, const int32_t *ends,
+                                         int groups, const BlockForm &row, const BlockForm &tr, hipStream_t stream);
 
 struct BlockGemmArgs {
     const uint8_t *a, *b;
@@ -33,6 +37,23 @@ struct BlockGemmArgs {
     bool c_bf16;
     int tiles_m, tiles_n;
 };
+
+// A product for each group of rows (or of columns of the operands), `ends` as in mx_block_group.h
+struct GroupedGemmArgs : BlockGemmArgs {
+    const int32_t *ends;
+    int groups, rows;              // rows: what ends are cut to
+    int64_t ldbg, ldsbg, ldcg;     // from one group's B, its scales or C to the next one's
+};
+
+// Rows: A's and C's rows in groups, B a matrix per group.  M is the number of rows, 0 < N, K; K == 0 clears C's rows.
+// K: A's and B's columns in groups, every group from a block of its own on; K columns in all, a C per group.
+hipError_t launch_block_gemm_grouped(const GroupedGemmArgs &g, int fa, int fb, bool b_tile, bool fp8_sums, hipStream_t stream);
+hipError_t launch_block_gemm_grouped_k(const GroupedGemmArgs &g, int fa, int fb, bool fp8_sums, hipStream_t stream);
+
+// the most units of `unit` rows that `rows` rows take in `groups` groups
+inline int64_t grouped_units(int64_t rows, int64_t groups, int64_t unit) {
+    return (rows + (unit - 1) * (rows < groups ? rows : groups)) / unit;
+}
 
 // M, N > 0; K == 0 clears C.  fp8_sums: blocks' sums by the FP8 instruction (C in bf16 only), else in fp32
 hipError_t launch_block_gemm(const BlockGemmArgs &g, int fa, int fb, bool b_tile, bool fp8_sums, hipStream_t stream);

@@ -20,6 +20,7 @@
 // 8192 x 4096 by rows (102 MB) 21 us (18.6 over the same outputs); 1000 x 6144, both
 // forms (25 MB, 384 workgroups) 10.4 us, of which launch, one read's latency, two
 // barriers and the stores, one after the other, are the most.
+#include "mx_block_group.h"
 #include "mx_block_util.h"
 
 namespace mx {
@@ -27,16 +28,34 @@ namespace {
 
 constexpr int kQT = 256;
 
-template <int FR, int FT, bool ROW, bool TR, bool TILE, bool WHOLE, bool NT>
+// GRP: a tile's rows are 128 of one group, or its last ones; in the transposed form the rest of their block is zeros.
+struct QuantGroups {
+    const int32_t *ends;
+    int groups;
+};
+struct NoGroups {};
+
+template <int FR, int FT, bool ROW, bool TR, bool TILE, bool WHOLE, bool NT, class GRP>
 __global__ __launch_bounds__(kQT) void k_block_quantize(const uint16_t *__restrict__ x, int64_t rows, int64_t cols,
                                                         int64_t ldx, uint32_t tiles_c, FastDiv tc_div, BlockForm fr,
-                                                        BlockForm ft) {
+                                                        BlockForm ft, GRP grp) {
+    constexpr bool GROUPED = std::is_same_v<GRP, QuantGroups>;
     __shared__ __attribute__((aligned(16))) uint8_t sT[TR ? kBlk * kBlk : 16];
     __shared__ __attribute__((aligned(16))) uint32_t sM[4][16][4];
     const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4, wave = tid >> 6;
     const uint32_t tr_i = tc_div.div(blockIdx.x), tc_i = blockIdx.x - tr_i * tiles_c;
-    const int64_t r0 = (int64_t)tr_i * kBlk, c0 = (int64_t)tc_i * kBlk;
-    const int nr = (int)min((int64_t)kBlk, rows - r0), nc = (int)min((int64_t)kBlk, cols - c0);
+    const int64_t c0 = (int64_t)tc_i * kBlk;
+    int64_t r0 = (int64_t)tr_i * kBlk;
+    int nr = (int)min((int64_t)kBlk, rows - r0);
+    const int nc = (int)min((int64_t)kBlk, cols - c0);
+    if constexpr (GROUPED) {
+        GroupChunk<kBlk> chunk;
+        if ((int)tr_i >= group_units(chunk, grp.ends, grp.groups, (int)rows)) return;  // the whole workgroup
+        const Group g = group_of_unit(chunk, grp.ends, grp.groups, (int)rows, (int)tr_i);
+        const int at = ((int)tr_i - g.first) * kBlk;
+        r0 = g.start + at;
+        nr = min(kBlk, g.count - at);
+    }
     const int nrt = nr - 8 * rg, nct = nc - 8 * cg;  // this thread's rows and columns inside the matrix (may be <= 0)
 
     uint32_t w[8][4];
@@ -171,11 +190,11 @@ __global__ __launch_bounds__(kQT) void k_block_quantize(const uint16_t *__restri
 #pragma unroll
         for (int k = 0; k < 4; k++) {
             const int t = k * kQT + tid, c = t >> 3, q = t & 7, g = c >> 3;
-            if (c >= nc || 16 * q >= nr) continue;
+            if (c >= nc || (!GROUPED && 16 * q >= nr)) continue;
             const uint4 v = *reinterpret_cast<const uint4 *>(&sT[c * kBlk + ((q ^ (g >> 1)) << 4)]);
             const uint4 u = (g & 1) ? make_uint4(v.z, v.w, v.x, v.y) : v;
-            uint8_t *d = ft.codes + (c0 + c) * ft.ld_codes + r0 + 16 * q;
-            if (16 * q + 16 <= nr) {
+            uint8_t *d = ft.codes + (c0 + c) * ft.ld_codes + (GROUPED ? (int64_t)tr_i * kBlk : r0) + 16 * q;
+            if (GROUPED || 16 * q + 16 <= nr) {
                 __builtin_memcpy(d, &u, 16);
             } else {
                 store8(d, u.x, u.y, min(8, nr - 16 * q));
@@ -185,10 +204,12 @@ __global__ __launch_bounds__(kQT) void k_block_quantize(const uint16_t *__restri
     }
 }
 
-template <bool TILE>
-hipError_t launch_forms(const uint16_t *x, int64_t rows, int64_t cols, int64_t ldx, const BlockForm &r,
-                        const BlockForm &t, hipStream_t s) {
-    const uint32_t tc = (uint32_t)((cols + kBlk - 1) / kBlk), trn = (uint32_t)((rows + kBlk - 1) / kBlk);
+// trn: row blocks
+template <bool TILE, class GRP>
+hipError_t launch_forms(const uint16_t *x, int64_t rows, int64_t cols, int64_t ldx, uint32_t trn, const BlockForm &r,
+                        const BlockForm &t, const GRP &grp, hipStream_t s) {
+    constexpr bool GROUPED = std::is_same_v<GRP, QuantGroups>;
+    const uint32_t tc = (uint32_t)((cols + kBlk - 1) / kBlk);
     const dim3 grid(tc * trn), block(kQT);
     const FastDiv d(tc);
     // Input larger than half of the 256 MB last-level cache is read past it: less of it would be found there
@@ -198,12 +219,12 @@ hipError_t launch_forms(const uint16_t *x, int64_t rows, int64_t cols, int64_t l
     const bool whole = cols % 8 == 0, nt = whole && rows * cols > (int64_t)1 << 26;
 #define MX_Q(fr, ft, row, tr)                                                                                             \
     do {                                                                                                                  \
-        if (nt) hipLaunchKernelGGL((k_block_quantize<fr, ft, row, tr, TILE, true, true>), grid, block, 0, s, x, rows,     \
-                                   cols, ldx, tc, d, r, t);                                                               \
-        else if (whole) hipLaunchKernelGGL((k_block_quantize<fr, ft, row, tr, TILE, true, false>), grid, block, 0, s, x,  \
-                                           rows, cols, ldx, tc, d, r, t);                                                 \
-        else hipLaunchKernelGGL((k_block_quantize<fr, ft, row, tr, TILE, false, false>), grid, block, 0, s, x, rows,      \
-                                cols, ldx, tc, d, r, t);                                                                  \
+        if (nt) hipLaunchKernelGGL((k_block_quantize<fr, ft, row, tr, TILE, true, true, GRP>), grid, block, 0, s, x, rows,     \
+                                   cols, ldx, tc, d, r, t, grp);                                                             \
+        else if (whole) hipLaunchKernelGGL((k_block_quantize<fr, ft, row, tr, TILE, true, false, GRP>), grid, block, 0, s, x,  \
+                                           rows, cols, ldx, tc, d, r, t, grp);                                               \
+        else hipLaunchKernelGGL((k_block_quantize<fr, ft, row, tr, TILE, false, false, GRP>), grid, block, 0, s, x, rows,      \
+                                cols, ldx, tc, d, r, t, grp);                                                                \
     } while (0)
     if (r.codes && t.codes) {
         switch (r.fmt * 2 + t.fmt) {
@@ -212,9 +233,11 @@ hipError_t launch_forms(const uint16_t *x, int64_t rows, int64_t cols, int64_t l
         case 2: MX_Q(1, 0, true, true); break;
         default: MX_Q(1, 1, true, true); break;
         }
-    } else if (r.codes) {
-        if (r.fmt == E4M3) MX_Q(0, 0, true, false);
-        else MX_Q(1, 1, true, false);
+    } else if (!GROUPED && r.codes) {
+        if constexpr (!GROUPED) {
+            if (r.fmt == E4M3) MX_Q(0, 0, true, false);
+            else MX_Q(1, 1, true, false);
+        }
     } else {
         if (t.fmt == E4M3) MX_Q(0, 0, false, true);
         else MX_Q(1, 1, false, true);
@@ -227,8 +250,15 @@ hipError_t launch_forms(const uint16_t *x, int64_t rows, int64_t cols, int64_t l
 
 hipError_t launch_block_quantize(const uint16_t *x, int64_t rows, int64_t cols, int64_t ldx, bool tile,
                                  const BlockForm &row, const BlockForm &tr, hipStream_t stream) {
-    return tile ? launch_forms<true>(x, rows, cols, ldx, row, tr, stream)
-                : launch_forms<false>(x, rows, cols, ldx, row, tr, stream);
+    const uint32_t trn = (uint32_t)((rows + kBlk - 1) / kBlk);
+    return tile ? launch_forms<true>(x, rows, cols, ldx, trn, row, tr, NoGroups{}, stream)
+                : launch_forms<false>(x, rows, cols, ldx, trn, row, tr, NoGroups{}, stream);
+}
+
+hipError_t launch_block_quantize_grouped(const uint16_t *x, int64_t rows, int64_t cols, int64_t ldx, const int32_t *ends,
+                                         int groups, const BlockForm &row, const BlockForm &tr, hipStream_t stream) {
+    return launch_forms<false>(x, rows, cols, ldx, (uint32_t)grouped_units(rows, groups, kBlk), row, tr,
+                               QuantGroups{ends, groups}, stream);
 }
 
 }  // namespace mx

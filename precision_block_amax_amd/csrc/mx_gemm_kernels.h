@@ -121,9 +121,8 @@ constexpr int kCusPerXcd = 32;
 
 // XCD-aware tile order: wg -> (tile row, tile column).  Consecutive workgroups go to the 8 XCDs in turn, so each XCD
 // gets a contiguous run of tiles, in groups of 8 tile rows
-__device__ __forceinline__ void tile_index(int tiles_m, int tiles_n, int &tm, int &tn) {
+__device__ __forceinline__ void tile_index_of(int wg, int tiles_m, int tiles_n, int &tm, int &tn) {
     const int ntiles = tiles_m * tiles_n;
-    const int wg = blockIdx.x;
     const int xcd = wg & 7, idx = wg >> 3;
     const int per = ntiles >> 3, rem = ntiles & 7;
     const int lt = xcd * per + (xcd < rem ? xcd : rem) + idx;
@@ -135,6 +134,9 @@ __device__ __forceinline__ void tile_index(int tiles_m, int tiles_n, int &tm, in
     const int in_grp = lt - grp * group_tiles;
     tm = first_m + in_grp % gsz;
     tn = in_grp / gsz;
+}
+__device__ __forceinline__ void tile_index(int tiles_m, int tiles_n, int &tm, int &tn) {
+    tile_index_of((int)blockIdx.x, tiles_m, tiles_n, tm, tn);
 }
 // its first row and column
 __device__ __forceinline__ void tile_of(const GemmArgs &g, int &m0, int &n0) {
