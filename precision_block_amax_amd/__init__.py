@@ -761,7 +761,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
 
 _ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 _ROPE_SCALINGS = {"plain": 0, "linear": 1, "bands": 2}
-_I32, _I64, _F64 = torch.int32, torch.int64, torch.float64
+_POS_TYPES = {torch.int32: 0, torch.int64: 1}
+_F64 = torch.float64
 
 
 def rope_frequencies(rot: int, theta: float = 10000.0, scaling: str = "plain", factor: float = 1.0, low: float = 1.0,
@@ -777,73 +778,81 @@ def rope_frequencies(rot: int, theta: float = 10000.0, scaling: str = "plain", f
     return f.to(device)
 
 
-def _heads(x: Optional[torch.Tensor], device, what: str) -> Tuple[int, int, int, int]:
+def _heads(x: Optional[torch.Tensor], index: int, what: str) -> Tuple[int, int, int, int]:
     """address, token stride, head stride and number of heads of a [tokens x heads x dim] tensor"""
     if x is None:
         return 0, 0, 0, 0
-    if x.dtype is not _BF16 or x.dim() != 3 or not x.is_cuda or x.device != device:
-        raise ValueError("%s must be a 3-D bf16 tensor [tokens x heads x dim] on %s" % (what, device))
-    (tokens, heads, dim), (lt, lh, step) = x.shape, x.stride()
-    if step != 1 and dim > 1 and x.numel():
+    st = x.stride()
+    if x.dtype is not _BF16 or len(st) != 3 or x.get_device() != index:
+        raise ValueError("%s must be a 3-D bf16 tensor [tokens x heads x dim] on GPU %d" % (what, index))
+    shape = x.shape
+    if st[2] != 1 and shape[2] > 1 and x.numel():
         raise ValueError("the last dimension of %s must be contiguous" % what)
-    return x.data_ptr(), lt, lh, heads
+    return x.data_ptr(), st[0], st[1], shape[1]
 
 
-def _rotation(tokens: int, dim: int, device, positions, freqs, layout: str) -> Tuple[int, int, int, int, int]:
-    """addresses of positions and freqs, the positions' type, rot and the layout"""
-    if layout not in _ROPE_LAYOUTS:
+def _rotation(tokens: int, dim: int, index: int, positions, freqs, layout: str) -> Tuple[int, int, int, int, int]:
+    """address and type of the positions, address of freqs, rot and the layout"""
+    lay = _ROPE_LAYOUTS.get(layout)
+    if lay is None:
         raise ValueError("layout must be one of %s" % sorted(_ROPE_LAYOUTS))
     if freqs is None:
-        return 0, 0, 0, 0, _ROPE_LAYOUTS[layout]
-    if freqs.dtype is not _F64 or freqs.dim() != 1 or freqs.device != device or not freqs.is_contiguous():
-        raise ValueError("freqs must be contiguous float64 of one dimension on %s" % device)
-    if 2 * freqs.shape[0] > dim:
-        raise ValueError("%d frequencies rotate more than the head's %d elements" % (freqs.shape[0], dim))
-    if positions is None or (positions.dtype is not _I64 and positions.dtype is not _I32) or positions.shape != (tokens,) \
-            or positions.device != device or not positions.is_contiguous():
-        raise ValueError("positions must be contiguous int32 or int64 of shape (%d,) on %s" % (tokens, device))
-    return (positions.data_ptr(), freqs.data_ptr(), 1 if positions.dtype is _I64 else 0, 2 * freqs.shape[0],
-            _ROPE_LAYOUTS[layout])
+        return 0, 0, 0, 0, lay
+    if freqs.dtype is not _F64 or freqs.dim() != 1 or freqs.get_device() != index or not freqs.is_contiguous():
+        raise ValueError("freqs must be contiguous float64 of one dimension on GPU %d" % index)
+    rot = 2 * freqs.shape[0]
+    if rot > dim:
+        raise ValueError("%d frequencies rotate more than the head's %d elements" % (rot // 2, dim))
+    pt = None if positions is None else _POS_TYPES.get(positions.dtype)
+    if pt is None or positions.shape != (tokens,) or positions.get_device() != index or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous int32 or int64 of shape (%d,) on GPU %d" % (tokens, index))
+    return positions.data_ptr(), pt, freqs.data_ptr(), rot, lay
 
 
 def _qk(q: torch.Tensor, k: Optional[torch.Tensor]):
-    """tokens, dim and device of queries and keys, and what _heads says of each"""
-    if q.dim() != 3 or not q.is_cuda:
-        raise ValueError("q must be a 3-D bf16 tensor [tokens x heads x dim] on a GPU")
+    """tokens, dim and device index of queries and keys, and what _heads says of each"""
+    index = q.get_device()
+    if index < 0:
+        raise ValueError("q must be on a GPU")
+    qh = _heads(q, index, "q")
     tokens, _, dim = q.shape
-    if k is not None and (k.dim() != 3 or k.shape[0] != tokens or k.shape[2] != dim):
+    kh = _heads(k, index, "k")
+    if k is not None and (k.shape[0] != tokens or k.shape[2] != dim):
         raise ValueError("q and k must agree in tokens and dim")
-    return tokens, dim, q.device, _heads(q, q.device, "q"), _heads(k, q.device, "k")
+    return tokens, dim, index, qh, kh
 
 
-def _like(x: Optional[torch.Tensor], out: Optional[torch.Tensor], device, what: str):
-    """the output for x: the one given, after its checks, or a new one"""
+def _like(x: Optional[torch.Tensor], out: Optional[torch.Tensor], index: int, what: str):
+    """the output for x, the one given or a new one, and its address and strides"""
     if x is None:
         if out is not None:
             raise ValueError("%s given without its input" % what)
-        return None
+        return None, 0, 0, 0
     if out is None:
-        return torch.empty(x.shape, dtype=_BF16, device=device)
+        out = torch.empty_like(x)
+        lt, lh, _ = out.stride()
+        return out, out.data_ptr(), lt, lh
+    p, lt, lh, _ = _heads(out, index, what)
     if out.shape != x.shape:
         raise ValueError("%s must have shape %s" % (what, tuple(x.shape)))
-    return out
+    return out, p, lt, lh
 
 
 def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor], freqs: Optional[torch.Tensor],
          layout: str = "half", scale: float = 1.0, inverse: bool = False, out=None, stream=None):
     """mx_rope: (q, k) with the first 2 * len(freqs) elements of every head rotated by
     positions[token] * freqs (rope_frequencies).  q, k: bf16 [tokens x heads x dim], any token and
-    head strides; k may be None.  layout "half": pairs (i, i + len(freqs)), "interleaved": (2 i,
+    head strides (new outputs have theirs in the same order, without gaps); k may be None.  layout "half": pairs (i, i + len(freqs)), "interleaved": (2 i,
     2 i + 1).  scale multiplies what is rotated; inverse turns the other way, which with the same
     scale is the backward pass.  `out` = (q_out, k_out)."""
-    tokens, dim, dev, qh, kh = _qk(q, k)
-    pos, fr, pt, rot, lay = _rotation(tokens, dim, dev, positions, freqs, layout)
+    tokens, dim, index, qh, kh = _qk(q, k)
+    rotation = _rotation(tokens, dim, index, positions, freqs, layout)
     oq, ok = (None, None) if out is None else out
+    dev = q.device
     with _scope(dev, stream):
-        oq, ok = _like(q, oq, dev, "q_out"), _like(k, ok, dev, "k_out")
-        qo, ko = _heads(oq, dev, "q_out"), _heads(ok, dev, "k_out")
-        _check(lib().mx_rope(*qh, *kh, tokens, dim, pos, pt, fr, rot, lay, scale, 1 if inverse else 0, *qo[:3], *ko[:3],
-                             _current(dev)))
+        oq, *qo = _like(q, oq, index, "q_out")
+        ok, *ko = _like(k, ok, index, "k_out")
+        _check(lib().mx_rope(*qh, *kh, tokens, dim, *rotation, scale, 1 if inverse else 0, *qo, *ko, _current(dev)))
     return oq, ok
 
 
@@ -854,15 +863,15 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[
     """mx_qk_norm_rope: the RMS norm of every head of q and k (bf16 [tokens x heads x dim], as in
     rope), times q_weight or k_weight ([dim], float32 or bfloat16, or None), then rope, in one
     pass.  Without freqs the norm alone."""
-    tokens, dim, dev, qh, kh = _qk(q, k)
+    tokens, dim, index, qh, kh = _qk(q, k)
+    dev = q.device
     wq, wk, p = _param(q_weight, dim, dev, "q_weight"), _param(k_weight, dim, dev, "k_weight"), _param_type(q_weight, k_weight)
-    pos, fr, pt, rot, lay = _rotation(tokens, dim, dev, positions, freqs, layout)
+    rotation = _rotation(tokens, dim, index, positions, freqs, layout)
     oq, ok = (None, None) if out is None else out
     with _scope(dev, stream):
-        oq, ok = _like(q, oq, dev, "q_out"), _like(k, ok, dev, "k_out")
-        qo, ko = _heads(oq, dev, "q_out"), _heads(ok, dev, "k_out")
-        _check(lib().mx_qk_norm_rope(*qh, *kh, tokens, dim, wq, wk, p, eps, pos, pt, fr, rot, lay, scale, *qo[:3], *ko[:3],
-                                     _current(dev)))
+        oq, *qo = _like(q, oq, index, "q_out")
+        ok, *ko = _like(k, ok, index, "k_out")
+        _check(lib().mx_qk_norm_rope(*qh, *kh, tokens, dim, wq, wk, p, eps, *rotation, scale, *qo, *ko, _current(dev)))
     return oq, ok
 
 
@@ -875,20 +884,21 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch
     of what qk_norm_rope returned for the same arguments; dxq, dxk are bf16, the weights'
     gradients float32, None without weight_grad (dxk and dk_weight also without k).  `out` =
     (dxq, dxk)."""
-    tokens, dim, dev, qh, kh = _qk(q, k)
+    tokens, dim, index, qh, kh = _qk(q, k)
     if dq.shape != q.shape or (dk is None) != (k is None) or (dk is not None and dk.shape != k.shape):
         raise ValueError("dq and dk must agree in shape with q and k")
-    gq, gk = _heads(dq, dev, "dq"), _heads(dk, dev, "dk")
+    dev = q.device
+    gq, gk = _heads(dq, index, "dq"), _heads(dk, index, "dk")
     wq, wk, p = _param(q_weight, dim, dev, "q_weight"), _param(k_weight, dim, dev, "k_weight"), _param_type(q_weight, k_weight)
-    pos, fr, pt, rot, lay = _rotation(tokens, dim, dev, positions, freqs, layout)
+    rotation = _rotation(tokens, dim, index, positions, freqs, layout)
     oq, ok = (None, None) if out is None else out
     with _scope(dev, stream):
-        oq, ok = _like(q, oq, dev, "dxq"), _like(k, ok, dev, "dxk")
-        qo, ko = _heads(oq, dev, "dxq"), _heads(ok, dev, "dxk")
+        oq, *qo = _like(q, oq, index, "dxq")
+        ok, *ko = _like(k, ok, index, "dxk")
         dwq = torch.empty((dim,), dtype=_F32, device=dev) if weight_grad else None
         dwk = torch.empty((dim,), dtype=_F32, device=dev) if weight_grad and k is not None else None
         need = lib().mx_qk_norm_rope_backward_workspace(tokens, qh[3], kh[3], dim) if weight_grad else 0
         ws = torch.empty((need,), dtype=_U8, device=dev) if need else None
-        _check(lib().mx_qk_norm_rope_backward(*gq[:3], *gk[:3], *qh, *kh, tokens, dim, wq, wk, p, eps, pos, pt, fr, rot, lay,
-                                              scale, *qo[:3], *ko[:3], _ptr(dwq), _ptr(dwk), _ptr(ws), need, _current(dev)))
+        _check(lib().mx_qk_norm_rope_backward(*gq[:3], *gk[:3], *qh, *kh, tokens, dim, wq, wk, p, eps, *rotation, scale, *qo,
+                                              *ko, _ptr(dwq), _ptr(dwk), _ptr(ws), need, _current(dev)))
     return oq, ok, dwq, dwk

@@ -90,15 +90,34 @@ struct Map {
         else return elem(s);
     }
 
-    __device__ __forceinline__ void load(float (&v)[NS], const uint16_t *p, bool live) const {
+    // a lane's bf16 elements as they are in memory, zeros where there are none: two per word, or one (V = 0)
+    static constexpr int RAW = V ? V : NS;
+    // NT: past the caches
+    typedef uint32_t Vec __attribute__((ext_vector_type(V ? V / 2 : 1), aligned(2)));
+    template <bool NT>
+    __device__ __forceinline__ void fetch(uint32_t (&w)[RAW], const uint16_t *p, bool live) const {
         if constexpr (V > 0) {
-            uint32_t w[V];
-#pragma unroll
-            for (int i = 0; i < V; i++) w[i] = 0u;
+            Vec a = {}, b = {};
             if (live && act) {
-                __builtin_memcpy(&w[0], p + o0, 2 * V);
-                __builtin_memcpy(&w[V / 2], p + o1, 2 * V);
+                const Vec *const pa = reinterpret_cast<const Vec *>(p + o0), *const pb = reinterpret_cast<const Vec *>(p + o1);
+                a = NT ? __builtin_nontemporal_load(pa) : *pa;
+                b = NT ? __builtin_nontemporal_load(pb) : *pb;
             }
+#pragma unroll
+            for (int i = 0; i < V / 2; i++) {
+                w[i] = a[i];
+                w[V / 2 + i] = b[i];
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < NS; s++) {
+                const int e = elem(s);
+                w[s] = live && e >= 0 ? (uint32_t)p[e] : 0u;
+            }
+        }
+    }
+    __device__ __forceinline__ void unpack(float (&v)[NS], const uint32_t (&w)[RAW]) const {
+        if constexpr (V > 0) {
 #pragma unroll
             for (int i = 0; i < V; i++) {
                 v[2 * i] = bf16_lo(w[i]);
@@ -106,20 +125,32 @@ struct Map {
             }
         } else {
 #pragma unroll
-            for (int s = 0; s < NS; s++) {
-                const int e = elem(s);
-                v[s] = live && e >= 0 ? __uint_as_float((uint32_t)p[e] << 16) : 0.f;
-            }
+            for (int s = 0; s < NS; s++) v[s] = bf16_lo(w[s]);
         }
     }
+    __device__ __forceinline__ void load(float (&v)[NS], const uint16_t *p, bool live) const {
+        uint32_t w[RAW];
+        fetch<false>(w, p, live);
+        unpack(v, w);
+    }
+    template <bool NT>
     __device__ __forceinline__ void store(uint16_t *p, const float (&v)[NS], bool live) const {
         if constexpr (V > 0) {
-            uint32_t w[V];
+            Vec a, b;
 #pragma unroll
-            for (int i = 0; i < V; i++) w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[2 * i], v[2 * i + 1]}, v2bf));
+            for (int i = 0; i < V / 2; i++) {
+                a[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[2 * i], v[2 * i + 1]}, v2bf));
+                b[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[V + 2 * i], v[V + 2 * i + 1]}, v2bf));
+            }
+            Vec *const pa = reinterpret_cast<Vec *>(p + o0), *const pb = reinterpret_cast<Vec *>(p + o1);
             if (live && act) {
-                __builtin_memcpy(p + o0, &w[0], 2 * V);
-                __builtin_memcpy(p + o1, &w[V / 2], 2 * V);
+                if constexpr (NT) {
+                    __builtin_nontemporal_store(a, pa);
+                    __builtin_nontemporal_store(b, pb);
+                } else {
+                    *pa = a;
+                    *pb = b;
+                }
             }
         } else {
 #pragma unroll
@@ -201,7 +232,7 @@ __device__ __forceinline__ void make_angles(float2 *cs, const RopeArgs &a, int64
 }
 
 // Forward.  A token's heads are `passes` passes of 64 / L, queries first; `parts` waves share them, `per` each.
-template <bool NORM, int V, int L, bool INTER>
+template <bool NORM, int V, int L, bool INTER, bool NT>
 __global__ __launch_bounds__(64 * kHW) void k_heads(RopeArgs a, FastDiv parts, int per) {
     typedef Map<V, L, INTER> M;
     constexpr int G = 64 / L;
@@ -226,7 +257,6 @@ __global__ __launch_bounds__(64 * kHW) void k_heads(RopeArgs a, FastDiv parts, i
         if constexpr (NORM) m.load_weight(w, h.weight, a.param_bf16);
         const uint16_t *const px = h.x + tok * h.xt;
         uint16_t *const po = h.out + tok * h.ot;
-#pragma unroll 2
         for (int p = lo; p < hi; p++) {
             const int head = p * G + sub;
             const bool live = head < h.heads;
@@ -241,114 +271,137 @@ __global__ __launch_bounds__(64 * kHW) void k_heads(RopeArgs a, FastDiv parts, i
                 for (int s = 0; s < M::NS; s++) v[s] = v[s] * rstd * w[s];
             }
             m.rotate(v, cs, sign);
-            m.store(po + head * h.oh, v, live);
+            m.template store<NT>(po + head * h.oh, v, live);
         }
     }
 }
 
-// Backward of the norm and the rotation: a workgroup's waves take every gridDim-th token, all heads.
-template <int V, int L, bool INTER>
-__global__ __launch_bounds__(64 * kHW) void k_heads_bwd(RopeArgs a) {
+// Backward of the norm and the rotation.  The first gq workgroups take the queries, the others the keys (a wave then
+// has one weight and one sum of its gradient); waves take every so many-th token, and fetch the next pass's x and dy
+// while they work on one.
+template <int V, int L, bool INTER, bool NT>
+__global__ __launch_bounds__(64 * kHW, V ? 4 : 1) void k_heads_bwd(RopeArgs a, int gq) {
     typedef Map<V, L, INTER> M;
     constexpr int G = 64 / L;
     __shared__ union {
         float2 cs[kHW][kMaxPairs];
-        float sum[kHW][2][kHeadMaxDim];
+        float sum[kHW][kHeadMaxDim];
     } sh;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = lane / L;
+    const bool keys = (int)blockIdx.x >= gq;
+    const HeadSet &h = a.s[keys];
+    const int64_t step = (int64_t)(keys ? gridDim.x - gq : gq) * kHW;
+    int64_t tok = (int64_t)(blockIdx.x - (keys ? gq : 0)) * kHW + wave;
     const M m(lane, a.dim, a.rot);
     const float rn = 1.0f / (float)a.dim;
-    float acc[2][M::NS];
+    float acc[M::NS], w[M::NS];
+    m.load_weight(w, h.weight, a.param_bf16);
 #pragma unroll
-    for (int si = 0; si < 2; si++)
-#pragma unroll
-        for (int s = 0; s < M::NS; s++) acc[si][s] = 0.f;
-    for (int64_t tok = (int64_t)blockIdx.x * kHW + wave; tok < a.tokens; tok += (int64_t)gridDim.x * kHW) {
+    for (int s = 0; s < M::NS; s++) acc[s] = 0.f;
+    uint32_t rx[M::RAW], rd[M::RAW];
+    const auto fetch = [&](int64_t t, int p) {
+        const int head = p + sub;
+        const bool live = t < a.tokens && head < h.heads;
+        m.template fetch<NT>(rx, h.x + t * h.xt + head * h.xh, live);
+        m.template fetch<NT>(rd, h.dy + t * h.dt + head * h.dh, live);
+    };
+    fetch(tok, 0);
+    for (; tok < a.tokens; tok += step) {
         make_angles(sh.cs[wave], a, tok, lane);
-        float2 cs[M::H];
-        m.angles(cs, sh.cs[wave]);
-#pragma unroll
-        for (int si = 0; si < 2; si++) {
-            const HeadSet &h = a.s[si];
-            float w[M::NS];
-            m.load_weight(w, h.weight, a.param_bf16);
-            const uint16_t *const px = h.x + tok * h.xt, *const pd = h.dy + tok * h.dt;
-            uint16_t *const po = h.out + tok * h.ot;
-            for (int p = 0; p < h.heads; p += G) {
-                const int head = p + sub;
-                const bool live = head < h.heads;
-                float v[M::NS], u[M::NS];
-                m.load(v, px + head * h.xh, live);
-                m.load(u, pd + head * h.dh, live);
+        uint16_t *const po = h.out + tok * h.ot;
+        for (int p = 0; p < h.heads; p += G) {
+            const int head = p + sub;
+            const bool live = head < h.heads;
+            float v[M::NS], u[M::NS];
+            m.unpack(v, rx);
+            m.unpack(u, rd);
+            const bool more = p + G < h.heads;
+            fetch(more ? tok : tok + step, more ? p + G : 0);
+            {
+                float2 cs[M::H];
+                m.angles(cs, sh.cs[wave]);
                 m.rotate(u, cs, -1.f);
-                float sq = 0.f, sg = 0.f;
-#pragma unroll
-                for (int s = 0; s < M::NS; s++) {
-                    sq = __builtin_fmaf(v[s], v[s], sq);
-                    sg = __builtin_fmaf(u[s] * w[s], v[s], sg);
-                }
-                const float rstd = live ? rsqrt1(__builtin_fmaf(group_sum<L>(sq), rn, a.eps)) : 0.f;
-                const float mean = group_sum<L>(sg) * rstd * rn;  // of g * xh
-#pragma unroll
-                for (int s = 0; s < M::NS; s++) {
-                    const float xh = v[s] * rstd;
-                    acc[si][s] = __builtin_fmaf(u[s], xh, acc[si][s]);
-                    v[s] = __builtin_fmaf(-xh, mean, u[s] * w[s]) * rstd;
-                }
-                m.store(po + head * h.oh, v, live);
             }
+            float sq = 0.f, sg = 0.f;
+#pragma unroll
+            for (int s = 0; s < M::NS; s++) {
+                sq = __builtin_fmaf(v[s], v[s], sq);
+                sg = __builtin_fmaf(u[s] * w[s], v[s], sg);
+            }
+            const float rstd = live ? rsqrt1(__builtin_fmaf(group_sum<L>(sq), rn, a.eps)) : 0.f;
+            const float mean = group_sum<L>(sg) * rstd * rn;  // of g * xh
+#pragma unroll
+            for (int s = 0; s < M::NS; s++) {
+                const float xh = v[s] * rstd;
+                acc[s] = __builtin_fmaf(u[s], xh, acc[s]);
+                v[s] = __builtin_fmaf(-xh, mean, u[s] * w[s]) * rstd;
+            }
+            m.template store<NT>(po + head * h.oh, v, live);
         }
     }
     if (!a.s[0].dw && !a.s[1].dw) return;
     __syncthreads();  // the angles are done with
 #pragma unroll
-    for (int si = 0; si < 2; si++)
+    for (int s = 0; s < M::NS; s++) {
+        float v = acc[s];
 #pragma unroll
-        for (int s = 0; s < M::NS; s++) {
-            float v = acc[si][s];
-#pragma unroll
-            for (int o = L; o < 64; o *= 2) v += __shfl_xor(v, o);
-            const int e = m.index(s);
-            if (sub == 0 && m.act && e >= 0) sh.sum[wave][si][e] = v;
-        }
+        for (int o = L; o < 64; o *= 2) v += __shfl_xor(v, o);
+        const int e = m.index(s);
+        if (sub == 0 && m.act && e >= 0) sh.sum[wave][e] = v;
+    }
     __syncthreads();
-    float *const d = a.ws + (int64_t)blockIdx.x * 2 * a.dim;
-    for (int i = threadIdx.x; i < 2 * a.dim; i += 64 * kHW) {
-        const int si = i >= a.dim, e = i - si * a.dim;
+    float *const d = a.ws + (int64_t)blockIdx.x * a.dim;
+    for (int i = threadIdx.x; i < a.dim; i += 64 * kHW) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kHW; w++) v += sh.sum[w][si][e];
+        for (int w = 0; w < kHW; w++) v += sh.sum[w][i];
         d[i] = v;
     }
 }
 
-// the workgroups' sums: 64 elements of both weights per workgroup, sixteen waves taking every sixteenth chunk
-constexpr int kSW = 16;
-__global__ __launch_bounds__(64 * kSW) void k_heads_dw(const float *ws, int chunks, int dim, float *dwq, float *dwk) {
-    __shared__ float s[kSW][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = blockIdx.x * 64 + lane;
+// The workgroups' sums: 16 elements of one weight per workgroup, 64 groups of lanes taking every 64th row of the
+// workspace, eight of them under way at a time.
+constexpr int kSC = 16, kSR = 64, kSL = 8;
+__global__ __launch_bounds__(kSC * kSR) void k_heads_dw(const float *ws, int gq, int gk, int dim, float *dwq, float *dwk) {
+    __shared__ float s[kSR][kSC + 1];
+    const int col = threadIdx.x % kSC, row = threadIdx.x / kSC, i = blockIdx.x * kSC + col;
+    float *const out = blockIdx.y ? dwk : dwq;
+    if (!out) return;  // the whole workgroup
+    const int n = blockIdx.y ? gk : gq;
+    const float *const p = ws + (blockIdx.y ? (int64_t)gq * dim : 0) + i;
     float v = 0.f;
-    if (i < 2 * dim)
-        for (int c = wave; c < chunks; c += kSW) v += ws[(int64_t)c * 2 * dim + i];
-    s[wave][lane] = v;
-    __syncthreads();
-    if (wave > 0 || i >= 2 * dim) return;
-    v = 0.f;
+    if (i < dim)
+        for (int c = row; c < n; c += kSR * kSL) {
+            float t[kSL];
 #pragma unroll
-    for (int w = 0; w < kSW; w++) v += s[w][lane];
-    float *const out = i < dim ? dwq : dwk;
-    if (out) out[i < dim ? i : i - dim] = v;
+            for (int k = 0; k < kSL; k++) t[k] = p[(int64_t)min(c + k * kSR, n - 1) * dim];
+#pragma unroll
+            for (int k = 0; k < kSL; k++) v += c + k * kSR < n ? t[k] : 0.f;
+        }
+    s[row][col] = v;
+    __syncthreads();
+    for (int half = kSR / 2; half > 0; half /= 2) {
+        if (row < half) s[row][col] += s[row + half][col];
+        __syncthreads();
+    }
+    if (row == 0 && i < dim) out[i] = s[0][col];
 }
 
-int64_t bwd_groups(int64_t tokens) {
-    const int64_t n = (tokens + kHW - 1) / kHW;
-    return n < 1024 ? n : 1024;
+// workgroups of the backward pass for queries and keys: 1024 in all, four per CU, shared by their heads, as far as
+// there are tokens for their waves
+void bwd_groups(int64_t tokens, int64_t hq, int64_t hk, int &gq, int &gk) {
+    const int64_t most = (tokens + kHW - 1) / kHW, q = hq + hk > 0 ? (1024 * hq + (hq + hk) / 2) / (hq + hk) : 0;
+    const auto cut = [&](int64_t n, int64_t heads) { return (int)(heads > 0 ? n < 1 ? 1 : n < most ? n : most : 0); };
+    gq = cut(q, hq);
+    gk = cut(1024 - q, hk);
 }
 
-template <int V, int L, bool INTER>
-hipError_t launch_as(const RopeArgs &all, int op, hipStream_t s) {
+template <int V, int L, bool INTER, bool NT>
+hipError_t launch_nt(const RopeArgs &all, int op, hipStream_t s) {
     if (op == NORM_ROPE_BWD) {
-        hipLaunchKernelGGL((k_heads_bwd<V, L, INTER>), dim3((unsigned)bwd_groups(all.tokens)), dim3(64 * kHW), 0, s, all);
+        int gq, gk;
+        bwd_groups(all.tokens, all.s[0].heads, all.s[1].heads, gq, gk);
+        hipLaunchKernelGGL((k_heads_bwd<V, L, INTER, NT>), dim3((unsigned)(gq + gk)), dim3(64 * kHW), 0, s, all, gq);
         return hipGetLastError();
     }
     constexpr int G = 64 / L;
@@ -366,12 +419,24 @@ hipError_t launch_as(const RopeArgs &all, int op, hipStream_t s) {
             h.out += t * h.ot;
         }
         const dim3 grid((unsigned)((a.tokens * parts + kHW - 1) / kHW));
-        if (op == ROPE) hipLaunchKernelGGL((k_heads<false, V, L, INTER>), grid, dim3(64 * kHW), 0, s, a, FastDiv((uint32_t)parts), (int)per);
-        else hipLaunchKernelGGL((k_heads<true, V, L, INTER>), grid, dim3(64 * kHW), 0, s, a, FastDiv((uint32_t)parts), (int)per);
+        if (op == ROPE) hipLaunchKernelGGL((k_heads<false, V, L, INTER, NT>), grid, dim3(64 * kHW), 0, s, a, FastDiv((uint32_t)parts), (int)per);
+        else hipLaunchKernelGGL((k_heads<true, V, L, INTER, NT>), grid, dim3(64 * kHW), 0, s, a, FastDiv((uint32_t)parts), (int)per);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+template <int V, int L, bool INTER>
+hipError_t launch_as(const RopeArgs &a, int op, hipStream_t s) {
+    // Outputs of more than 64 MB are written past the caches, and the backward pass's inputs read past them: what is
+    // behind these tensors stays in the 256 MB last-level cache.  8192 tokens of 40 heads of 128 (84 MB), inputs in
+    // turn: norm and rotation 35 and 28 us, backward 58 and 52 (outputs alone 56); 72 heads, rotation 67 and 65, and
+    // with loads past the caches 68.
+    const int64_t n = a.tokens * ((int64_t)a.s[0].heads + a.s[1].heads) * a.dim;
+    if constexpr (V > 0)
+        if (n > (int64_t)1 << 25) return launch_nt<V, L, INTER, true>(a, op, s);
+    return launch_nt<V, L, INTER, false>(a, op, s);
 }
 
 template <bool INTER>
@@ -389,7 +454,9 @@ hipError_t launch_layout(const RopeArgs &a, int op, hipStream_t s) {
 }  // namespace
 
 int64_t heads_workspace(int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t dim) {
-    return heads_q + heads_k > 0 ? bwd_groups(tokens) * 2 * dim : 0;
+    int gq, gk;
+    bwd_groups(tokens, heads_q, heads_k, gq, gk);
+    return (int64_t)(gq + gk) * dim;
 }
 
 hipError_t launch_heads(const RopeArgs &a, int op, hipStream_t s) {
@@ -397,9 +464,10 @@ hipError_t launch_heads(const RopeArgs &a, int op, hipStream_t s) {
     if (a.tokens > 0 && a.s[0].heads + (int64_t)a.s[1].heads > 0)
         e = a.interleaved ? launch_layout<true>(a, op, s) : launch_layout<false>(a, op, s);
     if (e != hipSuccess || op != NORM_ROPE_BWD || (!a.s[0].dw && !a.s[1].dw)) return e;
-    const int chunks = a.s[0].heads + (int64_t)a.s[1].heads > 0 ? (int)bwd_groups(a.tokens) : 0;
-    hipLaunchKernelGGL(k_heads_dw, dim3((unsigned)((2 * a.dim + 63) / 64)), dim3(64 * kSW), 0, s, (const float *)a.ws, chunks,
-                       a.dim, a.s[0].dw, a.s[1].dw);
+    int gq, gk;
+    bwd_groups(a.tokens, a.s[0].heads, a.s[1].heads, gq, gk);
+    hipLaunchKernelGGL(k_heads_dw, dim3((unsigned)((a.dim + kSC - 1) / kSC), 2), dim3(kSC * kSR), 0, s, (const float *)a.ws, gq,
+                       gk, a.dim, a.s[0].dw, a.s[1].dw);
     return hipGetLastError();
 }
 
