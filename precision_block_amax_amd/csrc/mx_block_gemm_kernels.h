@@ -23,6 +23,8 @@
 // data without cancellation.  Both to bf16, FP8 and fp32 sums: 8192 x 6144 x 4096
 // 187 and 367 us, 1000 x 4096 x 28672 157 and 225, 48 x 4096 x 14336 16.0 and 16.9.
 #pragma once
+#include <math.h>
+
 #include "mx_block_group.h"
 #include "mx_block_internal.h"
 #include "mx_gemm_kernels.h"
@@ -39,7 +41,16 @@ using ArgsOf = std::conditional_t<GRP == NOT, BlockGemmArgs, GroupedGemmArgs>;
 // The tile of C, PM rows each, that this workgroup computes, g made the product of its group; false: none is left for it.
 template <int GRP, int PM>
 __device__ __forceinline__ bool take_tile(ArgsOf<GRP> &g, int &tm, int &tn) {
-    const auto add = [&](auto *&p, int64_t n) { p += n; };
+    // p + n, which all lanes share, in scalar registers: buffer descriptors are made from it
+    const auto add = [&](auto *&p, int64_t n) {
+        const uint64_t a = (uint64_t)(uintptr_t)(p + n);
+        const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)a), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+        p = reinterpret_cast<std::remove_reference_t<decltype(p)>>((uintptr_t)((uint64_t)hi << 32 | lo));
+    };
+    const auto scalar = [](Group e) {
+        return Group{__builtin_amdgcn_readfirstlane(e.index), __builtin_amdgcn_readfirstlane(e.start),
+                     __builtin_amdgcn_readfirstlane(e.count), __builtin_amdgcn_readfirstlane(e.first)};
+    };
     if constexpr (GRP == NOT) {
         tile_index(g.tiles_m, g.tiles_n, tm, tn);
     } else if constexpr (GRP == ROWS) {
@@ -47,7 +58,7 @@ __device__ __forceinline__ bool take_tile(ArgsOf<GRP> &g, int &tm, int &tn) {
         const int tiles = group_units(chunk, g.ends, g.groups, g.rows);
         if ((int)blockIdx.x >= tiles * g.tiles_n) return false;
         tile_index(tiles, g.tiles_n, tm, tn);
-        const Group e = group_of_unit(chunk, g.ends, g.groups, g.rows, tm);
+        const Group e = scalar(group_of_unit(chunk, g.ends, g.groups, g.rows, tm));
         tm -= e.first;
         add(g.a, e.start * g.lda);
         add(g.as, e.start);
@@ -58,7 +69,7 @@ __device__ __forceinline__ bool take_tile(ArgsOf<GRP> &g, int &tm, int &tn) {
     } else {
         const int per = g.tiles_m * g.tiles_n, index = (int)blockIdx.x / per;
         tile_index_of((int)blockIdx.x - index * per, g.tiles_m, g.tiles_n, tm, tn);
-        const Group e = group_number<kBlk>(g.ends, g.groups, g.rows, index);
+        const Group e = scalar(group_number<kBlk>(g.ends, g.groups, g.rows, index));
         // ends that the operands were not made with must not lead past them
         const int blocks = g.K / kBlk, first = min(e.first, blocks);
         add(g.a, (int64_t)first * kBlk);
@@ -338,17 +349,20 @@ constexpr int kDead = (int)0x80000000u;  // a lane offset beyond every buffer: t
 // rings of their own, and their sums meet at the end: a 128 x 128 tile has work for four waves of 64 x 64
 // only, and a SIMD with one wave neither multiplies while it reads LDS nor the other way round.
 // PF: prefetch into L2 (below).
-struct Cfg256x256 { static constexpr int TI = 4, WM = 2, WN = 4, KG = 1; static constexpr bool PF = false; };
-struct Cfg256x128 { static constexpr int TI = 2, WM = 4, WN = 2, KG = 1; static constexpr bool PF = false; };
-struct Cfg128x128 { static constexpr int TI = 2, WM = 2, WN = 2, KG = 2; static constexpr bool PF = false; };
+// PER: workgroups per CU that registers and LDS are to leave room for.
+struct Cfg256x256 { static constexpr int TI = 4, WM = 2, WN = 4, KG = 1, PER = 1; static constexpr bool PF = false; };
+struct Cfg256x128 { static constexpr int TI = 2, WM = 4, WN = 2, KG = 1, PER = 1; static constexpr bool PF = false; };
+struct Cfg128x128 { static constexpr int TI = 2, WM = 2, WN = 2, KG = 2, PER = 1; static constexpr bool PF = false; };
 struct Cfg128x128Far : Cfg128x128 { static constexpr bool PF = true; };
+struct Cfg128x128Two { static constexpr int TI = 2, WM = 2, WN = 2, KG = 1, PER = 2; static constexpr bool PF = false; };
+struct Cfg64x128 { static constexpr int TI = 1, WM = 2, WN = 2, KG = 1, PER = 3; static constexpr bool PF = false; };
 
 // RAG: K ends inside a chunk of 16 bytes.  The stages leave that chunk out, and its products are added after them
 // from registers (a branch for it in the loop made the compiler spill: up to 200 registers).  256 x 256 tiles spill
 // 48 registers there, 24 instructions after the loop and none in it: 8192 x 6144 x 4095 to bf16 217 us beside 194 of
 // 4096; 4104 238, rows of 4112 bytes, whose 128 of a stage lie in two lines.
 template <int FA, int FB, bool BT, bool FP8SUMS, class CFG, bool RAG, int GRP>
-__global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN * CFG::KG / 4) void k_block_gemm_pipe(ArgsOf<GRP> g) {
+__global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN * CFG::KG * CFG::PER / 4) void k_block_gemm_pipe(ArgsOf<GRP> g) {
     constexpr int TI = CFG::TI, WM = CFG::WM, WN = CFG::WN, NS = 2, KG = CFG::KG;
     static_assert(KG == 1 || (KG == 2 && TI == 2), "the join swaps two rows of tiles");
     constexpr int NW = WM * WN, PM = WM * TI * 32, PN = WN * 64;
@@ -568,9 +582,17 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
         fa[0] = frag(pa, 0);
         fb[0] = frag(pb, 0);
     }
-    for (int it = 0; it < nit; it += 2) {
-        stage(0, it);
-        stage(1, it + 1);
+    if constexpr (GRP == NOT || TI > 2) {  // (256 x 256 tiles have no registers for a third copy of the stage)
+        for (int it = 0; it < nit; it += 2) {
+            stage(0, it);
+            stage(1, it + 1);
+        }
+    } else {  // groups may have one block of K only: no stage is for nothing; 1536 x 2048 of it, 128 times 389 -> 344 us
+        for (int it = 0; it + 1 < nit; it += 2) {
+            stage(0, it);
+            stage(1, it + 1);
+        }
+        if (nit & 1) stage(0, nit - 1);
     }
     {
         float4 sb[4];
@@ -1006,29 +1028,85 @@ inline bool grouped_aligned(const GroupedGemmArgs &g, int64_t nk) {
            g.lda < lim_code && g.ldb < lim_code && g.ldsa <= lim_scale && g.ldsb <= lim_scale;
 }
 
+// What a kernel would take for `tiles` of it, in us: rounds of 256 CUs with `per` workgroups each, a full round a + b
+// for each block of K; the last one, with fewer workgroups per CU, from `first` of that (one of them) on.
+struct Rate {
+    int per;
+    float a, b, first;
+    float us(float tiles, int64_t nk) const {
+        const float slots = 256.f * per, full = floorf(tiles / slots), rest = ceilf((tiles - full * slots) / 256.f);
+        const float part = rest == 0.f ? 0.f : per == 1 ? 1.f : first + (1.f - first) * (rest - 1.f) / (float)(per - 1);
+        return (full + part) * (a + b * (float)nk);
+    }
+};
+
+// The kernel for a product by rows.  The host knows how many rows and groups there are, not how the rows are dealt out,
+// so tiles are counted as for rows that fall on groups at random: groups (1 - exp(-mean)) of them have rows, each half a
+// tile and a little more at its end.  The rates below were fitted to measured times (us, MI355X, weights taking turns)
+// of groups x N x K from 1 x 4096 x 4096 to 128 x 1536 x 2048 and 8 x 28672 x 4096 with means of 1/16 to 8192 rows, the
+// most popular group ten times the least; the kernel that they choose is the fastest or within a tenth of it in most of
+// these.  FP8 sums, B in tiles:
+//   128 x 1536 x 2048   mean of 1/16  8 x 16 tiles 9, 64 x 128 12, 128 x 128 13
+//                       4             115, 64, 67       64  91 (64 x 128), 91, 256 x 256 105, 64 x 32 227
+//                       128           124, 114, 120     512  344, 291, 263
+//   8 x 2048 x 14336    1             8 x 16 20, 64 x 32 31, 128 x 128 in two groups 75, in one 100
+//                       32            101, 67, 80, 95   256  593, 200, 156, 123, 256 x 256 162
+//   8 x 28672 x 4096    8             236 (8 x 16), 64 x 128 197, 128 x 128 202    2048  2787, 2262, 256 x 256 1788
 template <int FA, int FB, bool BT, bool FP8SUMS>
 hipError_t launch_grouped_as(GroupedGemmArgs g, hipStream_t s) {
-    const int64_t mean = (g.M + g.groups - 1) / g.groups;  // rows of a group
+    const int64_t nk = (g.K + kBlk - 1) / kBlk;
     if (g.M == 1) g.lda = (g.K + 15) / 16 * 16;  // a single row has no stride
     if (g.N == 1) g.ldb = (g.K + 15) / 16 * 16;
-    if (!grouped_aligned(g, (g.K + kBlk - 1) / kBlk) || g.K < 16) {
+    if (!grouped_aligned(g, nk) || g.K < 16) {
         g.tiles_n = (g.N + GB - 1) / GB;
         hipLaunchKernelGGL((k_block_gemm<FA, FB, BT, FP8SUMS, ROWS>),
                            dim3((unsigned)(grouped_units(g.M, g.groups, GB) * g.tiles_n)), dim3(GNT), 0, s, g);
         return hipGetLastError();
     }
-    // (tiles of 8 rows and 16 columns, counted in 32 bits together with their threads)
-    if (grouped_units(g.M, g.groups, 8) * ((g.N + 15) / 16) < (int64_t)1 << 22) {
-        if (mean <= 8) return launch_grouped_few<FA, FB, BT, FP8SUMS, 1, 1, 2>(g, s);
-        if (mean <= 16) return launch_grouped_few<FA, FB, BT, FP8SUMS, 2, 1, 2>(g, s);
-        if (mean <= 32) return launch_grouped_few<FA, FB, BT, FP8SUMS, 4, 1, 3>(g, s);
+    const float rows = (float)g.M, met = (float)g.groups * (1.f - expf(-rows / (float)g.groups));
+    // tiles of m x n, for want of the groups' sizes a tenth more than that estimate
+    const auto tiles = [&](int m, int n) {
+        const float tn = (float)((g.N + n - 1) / n);
+        return g.groups == 1 ? ceilf(rows / m) * tn : fmaxf(met, rows / m + 0.6f * met) * 1.1f * tn;
+    };
+    const auto fits = [&](int m, int n) {  // workgroups and their threads in 32 bits
+        return grouped_units(g.M, g.groups, m) * ((g.N + n - 1) / n) < (int64_t)1 << 22;
+    };
+    enum { FEW8, FEW16, FEW64, SPLIT, TWO, HALF, BIG } best = TWO;
+    float least = Rate{2, 3.f, !FP8SUMS ? 1.85f : BT ? 1.1f : 1.25f, !FP8SUMS ? 0.56f : 0.65f}.us(tiles(128, 128), nk);
+    const auto offer = [&](decltype(best) k, float us) {
+        if (us < least) {
+            least = us;
+            best = k;
+        }
+    };
+    if (FP8SUMS && fits(64, 128)) offer(HALF, Rate{3, 1.f, 1.2f, 0.6f}.us(tiles(64, 128), nk));
+    if (FP8SUMS && BT) {
+        const float t = tiles(256, 256);
+        offer(BIG, Rate{1, 4.f, t > 256.f ? 1.75f : 1.3f, 0.f}.us(t, nk));
     }
-    if constexpr (FP8SUMS && BT) {
-        if (mean >= 512) return launch_grouped_rows<FA, FB, BT, FP8SUMS, Cfg256x256>(g, s);
-    } else {
-        if (mean >= 512) return launch_grouped_rows<FA, FB, BT, FP8SUMS, Cfg256x128>(g, s);
+    // one round at most, and sure of it: a second one has every CU wait for its few
+    if (tiles(128, 128) <= 282.f && (8 * rows <= 128.f * g.groups || tiles(128, 128) <= 220.f || g.groups == 1))
+        offer(SPLIT, Rate{1, 2.f, FP8SUMS ? 0.6f : 0.87f, 0.f}.us(fminf(tiles(128, 128), 256.f), nk));
+    if (fits(64, 32)) offer(FEW64, Rate{1, 3.f, 0.16f, 0.f}.us(tiles(64, 32), nk));
+    if (fits(8, 16)) {
+        offer(FEW16, Rate{2, 3.6f, 0.115f, 0.7f}.us(tiles(16, 16), nk));
+        offer(FEW8, Rate{2, 3.5f, 0.11f, 0.7f}.us(tiles(8, 16), nk));
     }
-    return launch_grouped_rows<FA, FB, BT, FP8SUMS, Cfg128x128>(g, s);
+    switch (best) {
+    case FEW8: return launch_grouped_few<FA, FB, BT, FP8SUMS, 1, 1, 2>(g, s);
+    case FEW16: return launch_grouped_few<FA, FB, BT, FP8SUMS, 2, 1, 2>(g, s);
+    case FEW64: return launch_grouped_few<FA, FB, BT, FP8SUMS, 8, 2, 1>(g, s);
+    case SPLIT: return launch_grouped_rows<FA, FB, BT, FP8SUMS, Cfg128x128>(g, s);
+    case HALF:
+        if constexpr (FP8SUMS) return launch_grouped_rows<FA, FB, BT, FP8SUMS, Cfg64x128>(g, s);
+        break;
+    case BIG:
+        if constexpr (FP8SUMS && BT) return launch_grouped_rows<FA, FB, BT, FP8SUMS, Cfg256x256>(g, s);
+        break;
+    case TWO: break;
+    }
+    return launch_grouped_rows<FA, FB, BT, FP8SUMS, Cfg128x128Two>(g, s);
 }
 
 template <int FA, int FB, bool FP8SUMS>
@@ -1040,8 +1118,12 @@ hipError_t launch_grouped_k_as(GroupedGemmArgs g, hipStream_t s) {
                            dim3(GNT), 0, s, g);
         return hipGetLastError();
     }
-    if (g.M > 128) return launch_grouped_cols<FA, FB, FP8SUMS, Cfg256x128>(g, s);
-    return launch_grouped_cols<FA, FB, FP8SUMS, Cfg128x128>(g, s);
+    // Two workgroups per CU, one writing while the other multiplies.  In at most one round of one per CU two groups of
+    // waves for each tile, if there is K to share: 4 x 512 x 512 with a mean of 512 rows 16.7 against 18.3, of 4096 80
+    // against 94, of 32 9.9 against 8.7; 8 x 1024 x 1024 (two rounds), 128 rows 20 against 12.5.
+    const int64_t tiles = (int64_t)((g.M + 127) / 128) * ((g.N + 127) / 128) * g.groups;
+    if (tiles <= 256 && g.K >= (int64_t)512 * g.groups) return launch_grouped_cols<FA, FB, FP8SUMS, Cfg128x128>(g, s);
+    return launch_grouped_cols<FA, FB, FP8SUMS, Cfg128x128Two>(g, s);
 }
 
 template <int FA, int FB>
