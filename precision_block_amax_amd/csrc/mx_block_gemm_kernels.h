@@ -772,7 +772,6 @@ __device__ __forceinline__ v4f few_block(const Frag2 &a, const Frag2 &b) {
 // holds, and reaches only rows of C that do not exist
 template <int FA, int FB, bool BT, bool FP8SUMS, int AI, int NT, int S, int GRP>
 __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(ArgsOf<GRP> g) {
-    static_assert(GRP != COLS, "a group without columns has no block");
     constexpr int MT = (AI + 1) / 2, DM = 16 * MT, DN = 16 * NT, JP = DN + 4;
     constexpr int OB = MT * 2048, OS = OB + NT * 2048, BLK = OS + 512;  // a block: A's rows, B's, scales of A, of B
     constexpr int LPB = AI + 2 * NT + 2;                                // loads per block
@@ -783,6 +782,7 @@ __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(ArgsOf<GRP> g) {
     int tm, tn;
     if (!take_tile<GRP, 8 * AI>(g, tm, tn)) return;
     const int m0 = tm * 8 * AI, n0 = tn * DN;
+    if (GRP == COLS && g.K == 0) return zero_tile<8 * AI, DN, 64 * DW>(g, m0, n0);
     const int nk = (g.K + kBlk - 1) / kBlk, ktail = g.K - (nk - 1) * kBlk;
     const int lda = (int)g.lda, ldb = (int)g.ldb, mrows = min(8 * AI, g.M - m0), nrows = min(DN, g.N - n0);
     // rows end at a multiple of 16 bytes: an aligned 16 bytes that hold a byte of the row
@@ -1011,6 +1011,15 @@ hipError_t launch_grouped_rows(GroupedGemmArgs g, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <int FA, int FB, bool FP8SUMS>
+hipError_t launch_grouped_cols_few(GroupedGemmArgs g, hipStream_t s) {
+    g.tiles_m = (g.M + 63) / 64;
+    g.tiles_n = (g.N + 31) / 32;
+    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, false, FP8SUMS, 8, 2, 1, COLS>),
+                       dim3((unsigned)(g.tiles_m * g.tiles_n * g.groups)), dim3(64 * DW), 0, s, g);
+    return hipGetLastError();
+}
+
 template <int FA, int FB, bool FP8SUMS, class CFG>
 hipError_t launch_grouped_cols(GroupedGemmArgs g, hipStream_t s) {
     constexpr int PM = CFG::WM * CFG::TI * 32, PN = CFG::WN * 64;
@@ -1118,11 +1127,15 @@ hipError_t launch_grouped_k_as(GroupedGemmArgs g, hipStream_t s) {
                            dim3(GNT), 0, s, g);
         return hipGetLastError();
     }
-    // Two workgroups per CU, one writing while the other multiplies.  In at most one round of one per CU two groups of
-    // waves for each tile, if there is K to share: 4 x 512 x 512 with a mean of 512 rows 16.7 against 18.3, of 4096 80
-    // against 94, of 32 9.9 against 8.7; 8 x 1024 x 1024 (two rounds), 128 rows 20 against 12.5.
-    const int64_t tiles = (int64_t)((g.M + 127) / 128) * ((g.N + 127) / 128) * g.groups;
-    if (tiles <= 256 && g.K >= (int64_t)512 * g.groups) return launch_grouped_cols<FA, FB, FP8SUMS, Cfg128x128>(g, s);
+    // Two workgroups per CU, one writing while the other multiplies.  Where there are few tiles and each has blocks of K
+    // to share, eight waves share those of a 64 x 32 tile (up to two rounds of them), or two groups of waves those of a
+    // 128 x 128 tile (one round).  us, fp32 sums, in this order the three: one group of 384 x 80, 12867 rows 111, 19, 90;
+    // 1024 x 1024, 8192 rows 74, 31, 61, 128 rows 8.3, 9.0, 8.5; 4096 x 4096, 8192 rows 268, 420, 276; 4 x 512 x 512
+    // with a mean of 512 rows 17.5, 10.6, 16.9; 8 x 1024 x 1024 (two rounds of 128 x 128), 128 rows 12, 62, 18.
+    const bool share = g.K >= (int64_t)512 * g.groups;
+    const auto tiles = [&](int m, int n) { return (int64_t)((g.M + m - 1) / m) * ((g.N + n - 1) / n) * g.groups; };
+    if (share && tiles(64, 32) <= 512) return launch_grouped_cols_few<FA, FB, FP8SUMS>(g, s);
+    if (share && tiles(128, 128) <= 256) return launch_grouped_cols<FA, FB, FP8SUMS, Cfg128x128>(g, s);
     return launch_grouped_cols<FA, FB, FP8SUMS, Cfg128x128Two>(g, s);
 }
 

@@ -216,7 +216,9 @@ hipError_t launch_forms(const uint16_t *x, int64_t rows, int64_t cols, int64_t l
     // than it pushes out.  Through the cache and past it, with outputs over the same memory call after call:
     // 28672 x 4096 in tiles, both forms 91 and 75 us, 8192 x 4096 (67 MB, partly still cached), one form 18.6 and
     // 20.0; with outputs in turn 92 either way, and 21.3 and 20.0.
-    const bool whole = cols % 8 == 0, nt = whole && rows * cols > (int64_t)1 << 26;
+    // By groups 16384 x 4096 is past that: outputs in turn, transposed form 45.8 and 39.6, both 59 and 50; 8192 x 4096
+    // 18.9 and 21.1, 30 and 30.
+    const bool whole = cols % 8 == 0, nt = whole && rows * cols + (GROUPED ? 1 : 0) > (int64_t)1 << 26;
 #define MX_Q(fr, ft, row, tr)                                                                                             \
     do {                                                                                                                  \
         if (nt) hipLaunchKernelGGL((k_block_quantize<fr, ft, row, tr, TILE, true, true, GRP>), grid, block, 0, s, x, rows,     \

@@ -226,6 +226,22 @@ def test_cols_of_every_kernel(mx, M, N, fa, fb):
             check(mx.block_gemm_grouped_k(*a, fa, *b, fb, ends, out_dtype=dtype, full_sums=full), C, S, 8, full)
 
 
+@pytest.mark.parametrize("groups", [1, 3])
+@pytest.mark.parametrize("M,N", [(384, 80), (65, 33), (1, 500), (700, 900), (1100, 600)])
+def test_long_columns_of_few_tiles(mx, groups, M, N):
+    """waves that share the blocks of K: whole eighths and not, a group without rows among them"""
+    import torch
+    for rows in (700, 3000, 5000):
+        sizes = [rows] if groups == 1 else [rows * 2, 0, rows]
+        ends = ends_of(sizes)
+        a = mx.block_quantize_grouped(data(sum(sizes), M, seed=31), ends, "e5m2")
+        b = mx.block_quantize_grouped(data(sum(sizes), N, seed=32), ends, "e4m3")
+        C, S = grp.gemm_k(a, "e5m2", b, "e4m3", ends.tolist())
+        for dtype, full in ((torch.bfloat16, False), (torch.bfloat16, True), (torch.float32, True)):
+            check(mx.block_gemm_grouped_k(*a, "e5m2", *b, "e4m3", ends, out_dtype=dtype, full_sums=full), C, S,
+                  ref.cdiv(max(sizes), 128), full)
+
+
 def test_unaligned_columns(mx):
     import torch
     sizes = [5, 0, 300, 130]
