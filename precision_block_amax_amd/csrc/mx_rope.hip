@@ -16,7 +16,7 @@
 // for all heads that a wave meets, then go through the workspace to a second kernel;
 // every sum is in a fixed order, so the same inputs give the same bits.
 //
-// A wave takes the heads of one token, 64 / L at a time: a head is 16 elements of
+// A wave takes heads of one token, 64 / L at a time: a head is 16 elements of
 // each of L lanes, two vectors of eight.  In the half layout these are the two
 // halves of eight pairs, so pairs never cross lanes and a head's sums are a DPP tree
 // over L lanes.  Everything is fp32 until the one rounding to bf16.
@@ -74,8 +74,9 @@ struct Map {
             o0 = o1 = 0;
         }
     }
-    // (V = 0) element of a slot, -1: none
+    // element of a slot, -1: none
     __device__ __forceinline__ int elem(int s) const {
+        if constexpr (V > 0) return !act ? -1 : s < V ? o0 + s : o1 + s - V;
         const int i = s & 7, second = s >> 3;
         if (i < 4) {
             const int j = l + 64 * i;
@@ -84,19 +85,14 @@ struct Map {
         const int e = nrot + l + 64 * (i - 4 + 4 * second);
         return e < dim ? e : -1;
     }
-    // element of any slot; V > 0: of a lane that has elements
-    __device__ __forceinline__ int index(int s) const {
-        if constexpr (V > 0) return s < V ? o0 + s : o1 + s - V;
-        else return elem(s);
-    }
 
-    // a lane's bf16 elements as they are in memory, zeros where there are none: two per word, or one (V = 0)
-    static constexpr int RAW = V ? V : NS;
+    // a lane's bf16 elements as they are in memory, zeros where there are none: two per word, or one (V = 0, 1)
+    static constexpr int RAW = V > 1 ? V : NS;
     // NT: past the caches
-    typedef uint32_t Vec __attribute__((ext_vector_type(V ? V / 2 : 1), aligned(2)));
+    typedef uint32_t Vec __attribute__((ext_vector_type(V > 1 ? V / 2 : 1), aligned(2)));
     template <bool NT>
     __device__ __forceinline__ void fetch(uint32_t (&w)[RAW], const uint16_t *p, bool live) const {
-        if constexpr (V > 0) {
+        if constexpr (V > 1) {
             Vec a = {}, b = {};
             if (live && act) {
                 const Vec *const pa = reinterpret_cast<const Vec *>(p + o0), *const pb = reinterpret_cast<const Vec *>(p + o1);
@@ -117,7 +113,7 @@ struct Map {
         }
     }
     __device__ __forceinline__ void unpack(float (&v)[NS], const uint32_t (&w)[RAW]) const {
-        if constexpr (V > 0) {
+        if constexpr (V > 1) {
 #pragma unroll
             for (int i = 0; i < V; i++) {
                 v[2 * i] = bf16_lo(w[i]);
@@ -135,7 +131,7 @@ struct Map {
     }
     template <bool NT>
     __device__ __forceinline__ void store(uint16_t *p, const float (&v)[NS], bool live) const {
-        if constexpr (V > 0) {
+        if constexpr (V > 1) {
             Vec a, b;
 #pragma unroll
             for (int i = 0; i < V / 2; i++) {
@@ -171,7 +167,7 @@ struct Map {
             return;
         }
         const float *const q = reinterpret_cast<const float *>(p);
-        if constexpr (V > 0) {
+        if constexpr (V > 1) {
             if (act) {
                 __builtin_memcpy(&v[0], q + o0, 4 * V);
                 __builtin_memcpy(&v[V], q + o1, 4 * V);
@@ -231,48 +227,45 @@ __device__ __forceinline__ void make_angles(float2 *cs, const RopeArgs &a, int64
     __builtin_amdgcn_wave_barrier();
 }
 
-// Forward.  A token's heads are `passes` passes of 64 / L, queries first; `parts` waves share them, `per` each.
+// Forward.  A token's heads are passes of 64 / L, queries first, a wave for each: its own angles cost a wave less than
+// waiting does for its next heads.  8192 tokens of 72 heads of 128, rotation: a wave for nine passes 65 us, for three
+// 59.5, for two 57, for one 53 (5.7 TB/s); 40 heads, norm and rotation 28 for five, 27 for one.
+// Lanes of fewer than 16 elements have as many passes more (8192 tokens of 40 heads of 128, 20 rotated: 139 us an element at a time, 27 so).
+template <int V>
+constexpr int kPasses = V == 0 ? 1 : 8 / V;
 template <bool NORM, int V, int L, bool INTER, bool NT>
-__global__ __launch_bounds__(64 * kHW) void k_heads(RopeArgs a, FastDiv parts, int per) {
+__global__ __launch_bounds__(64 * kHW) void k_heads(RopeArgs a, FastDiv parts, int passes) {
     typedef Map<V, L, INTER> M;
     constexpr int G = 64 / L;
     __shared__ float2 sCS[kHW][kMaxPairs];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = lane / L;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t item = blockIdx.x * kHW + wave, tok = parts.div(item);
     if (tok >= a.tokens) return;  // a whole wave; no barriers of the workgroup below
-    const int p0 = (int)(item - tok * parts.d) * per;
+    const int p0 = (int)(item - tok * parts.d) * kPasses<V>, pq = (a.s[0].heads + G - 1) / G;
     const M m(lane, a.dim, a.rot);
     make_angles(sCS[wave], a, tok, lane);
     float2 cs[M::H];
     m.angles(cs, sCS[wave]);
-    const float sign = !NORM && a.inverse ? -1.f : 1.f, rn = 1.0f / (float)a.dim;
-    int base = 0;
-#pragma unroll 1
-    for (int si = 0; si < 2; si++) {
-        const HeadSet &h = a.s[si];
-        const int n = (h.heads + G - 1) / G, lo = max(p0 - base, 0), hi = min(p0 + per - base, n);
-        base += n;
-        if (lo >= hi) continue;
-        float w[M::NS];
-        if constexpr (NORM) m.load_weight(w, h.weight, a.param_bf16);
-        const uint16_t *const px = h.x + tok * h.xt;
-        uint16_t *const po = h.out + tok * h.ot;
-        for (int p = lo; p < hi; p++) {
-            const int head = p * G + sub;
-            const bool live = head < h.heads;
-            float v[M::NS];
-            m.load(v, px + head * h.xh, live);
-            if constexpr (NORM) {
-                float sq = 0.f;
 #pragma unroll
-                for (int s = 0; s < M::NS; s++) sq = __builtin_fmaf(v[s], v[s], sq);
-                const float rstd = rsqrt1(__builtin_fmaf(group_sum<L>(sq), rn, a.eps));
+    for (int i = 0; i < kPasses<V>; i++) {
+        const int p = p0 + i;
+        if (p >= passes) break;
+        const HeadSet &h = a.s[p >= pq];
+        const int head = (p >= pq ? p - pq : p) * G + lane / L;
+        const bool live = head < h.heads;
+        float v[M::NS];
+        m.load(v, h.x + tok * h.xt + head * h.xh, live);
+        if constexpr (NORM) {
+            float w[M::NS], sq = 0.f;
+            m.load_weight(w, h.weight, a.param_bf16);
 #pragma unroll
-                for (int s = 0; s < M::NS; s++) v[s] = v[s] * rstd * w[s];
-            }
-            m.rotate(v, cs, sign);
-            m.template store<NT>(po + head * h.oh, v, live);
+            for (int s = 0; s < M::NS; s++) sq = __builtin_fmaf(v[s], v[s], sq);
+            const float rstd = rsqrt1(__builtin_fmaf(group_sum<L>(sq), 1.0f / (float)a.dim, a.eps));
+#pragma unroll
+            for (int s = 0; s < M::NS; s++) v[s] = v[s] * rstd * w[s];
         }
+        m.rotate(v, cs, !NORM && a.inverse ? -1.f : 1.f);
+        m.template store<NT>(h.out + tok * h.ot + head * h.oh, v, live);
     }
 }
 
@@ -346,8 +339,8 @@ __global__ __launch_bounds__(64 * kHW, V ? 4 : 1) void k_heads_bwd(RopeArgs a, i
         float v = acc[s];
 #pragma unroll
         for (int o = L; o < 64; o *= 2) v += __shfl_xor(v, o);
-        const int e = m.index(s);
-        if (sub == 0 && m.act && e >= 0) sh.sum[wave][e] = v;
+        const int e = m.elem(s);
+        if (sub == 0 && e >= 0) sh.sum[wave][e] = v;
     }
     __syncthreads();
     float *const d = a.ws + (int64_t)blockIdx.x * a.dim;
@@ -406,9 +399,7 @@ hipError_t launch_nt(const RopeArgs &all, int op, hipStream_t s) {
     }
     constexpr int G = 64 / L;
     const int64_t passes = ((int64_t)all.s[0].heads + G - 1) / G + ((int64_t)all.s[1].heads + G - 1) / G;
-    // waves enough to fill the chip, each with as many of a token's passes as that leaves
-    const int64_t want = (8192 + all.tokens - 1) / all.tokens, parts0 = want < passes ? want : passes;
-    const int64_t per = (passes + parts0 - 1) / parts0, parts = (passes + per - 1) / per;
+    const int64_t parts = (passes + kPasses<V> - 1) / kPasses<V>;
     const int64_t most = ((int64_t)1 << 25) / parts;  // tokens per launch: waves and threads in 32 bits
     for (int64_t t = 0; t < all.tokens; t += most) {
         RopeArgs a = all;
@@ -419,8 +410,8 @@ hipError_t launch_nt(const RopeArgs &all, int op, hipStream_t s) {
             h.out += t * h.ot;
         }
         const dim3 grid((unsigned)((a.tokens * parts + kHW - 1) / kHW));
-        if (op == ROPE) hipLaunchKernelGGL((k_heads<false, V, L, INTER, NT>), grid, dim3(64 * kHW), 0, s, a, FastDiv((uint32_t)parts), (int)per);
-        else hipLaunchKernelGGL((k_heads<true, V, L, INTER, NT>), grid, dim3(64 * kHW), 0, s, a, FastDiv((uint32_t)parts), (int)per);
+        if (op == ROPE) hipLaunchKernelGGL((k_heads<false, V, L, INTER, NT>), grid, dim3(64 * kHW), 0, s, a, FastDiv((uint32_t)parts), (int)passes);
+        else hipLaunchKernelGGL((k_heads<true, V, L, INTER, NT>), grid, dim3(64 * kHW), 0, s, a, FastDiv((uint32_t)parts), (int)passes);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -448,6 +439,12 @@ hipError_t launch_layout(const RopeArgs &a, int op, hipStream_t s) {
         return launch_as<8, 32, INTER>(a, op, s);
     }
     if (a.dim % 8 == 0 && a.rot % 8 == 0 && a.dim <= 128) return launch_as<4, 16, INTER>(a, op, s);
+    if (a.dim % 4 == 0 && a.rot % 4 == 0) {
+        if (a.dim <= 64) return launch_as<2, 16, INTER>(a, op, s);
+        if (a.dim <= 128) return launch_as<2, 32, INTER>(a, op, s);
+        if (a.dim <= 256) return launch_as<2, 64, INTER>(a, op, s);
+    }
+    if (a.dim % 2 == 0 && a.dim <= 128) return launch_as<1, 64, INTER>(a, op, s);
     return launch_as<0, 64, INTER>(a, op, s);
 }
 
