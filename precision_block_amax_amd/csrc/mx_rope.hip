@@ -57,6 +57,7 @@ __device__ __forceinline__ float group_sum(float v) {
 template <int V, int L, bool INTER>
 struct Map {
     static constexpr int H = V ? V : 8, NS = 2 * H;
+    static constexpr bool kPairwise = INTER && V == 1;  // a vector of one element holds no pair
     int o0, o1, l;
     bool act, rot;  // (V > 0) the lane has elements; they are rotated
     int dim, pairs, nrot;
@@ -66,9 +67,12 @@ struct Map {
         if constexpr (V > 0) {
             act = 2 * V * l < dim;
             rot = 2 * V * l < nrot;
-            const bool halves = !INTER && rot;
-            o0 = halves ? V * l : 2 * V * l;
-            o1 = halves ? pairs + V * l : 2 * V * l + V;
+            // neighbouring lanes' vectors lie side by side, those of the rotated part and those of the rest, in either
+            // layout (with a lane's two vectors side by side, two loads read every line: interleaved, 8192 tokens
+            // of 40 heads of 128, backward 64 us, forward 32)
+            const int k = rot ? l : l - nrot / (2 * V), base = rot ? 0 : nrot, half = (rot ? nrot : dim - nrot) / 2;
+            o0 = kPairwise && rot ? 2 * l : base + V * k;
+            o1 = kPairwise && rot ? 2 * l + 1 : base + half + V * k;
         } else {
             act = rot = true;
             o0 = o1 = 0;
@@ -185,7 +189,10 @@ struct Map {
     __device__ __forceinline__ void angles(float2 (&cs)[H], const float2 *all) const {
 #pragma unroll
         for (int i = 0; i < H; i++) {
-            if constexpr (V > 0) cs[i] = all[rot ? V * l + i : 0];
+            // the lane's slots are elements V l .. and pairs + V l ..: of the half layout the pairs V l .., of the
+            // interleaved one V l / 2 .. and as many from (pairs + V l) / 2 on
+            if constexpr (V > 1 && INTER) cs[i] = all[!rot ? 0 : i < V / 2 ? V / 2 * l + i : pairs / 2 + V / 2 * l + i - V / 2];
+            else if constexpr (V > 0) cs[i] = all[rot ? V * l + i : 0];
             else cs[i] = all[i < 4 && l + 64 * i < pairs ? l + 64 * i : 0];
         }
     }
@@ -270,8 +277,10 @@ __global__ __launch_bounds__(64 * kHW) void k_heads(RopeArgs a, FastDiv parts, i
 }
 
 // Backward of the norm and the rotation.  The first gq workgroups take the queries, the others the keys (a wave then
-// has one weight and one sum of its gradient); waves take every so many-th token, and fetch the next pass's x and dy
-// while they work on one.
+// has one weight and one sum of its gradient).  Waves take every so many-th token, so that what all of them read at a
+// time lies together, and fetch the next pass's x and dy while they work on one.  8192 tokens of 40 heads of 128: 52 us; with
+// a range of passes for each wave 66, with every so many-th pass instead of token 58 (32768
+// tokens, interleaved: 226 and 263).
 template <int V, int L, bool INTER, bool NT>
 __global__ __launch_bounds__(64 * kHW, V ? 4 : 1) void k_heads_bwd(RopeArgs a, int gq) {
     typedef Map<V, L, INTER> M;
@@ -380,25 +389,33 @@ __global__ __launch_bounds__(kSC * kSR) void k_heads_dw(const float *ws, int gq,
     if (row == 0 && i < dim) out[i] = s[0][col];
 }
 
-// workgroups of the backward pass for queries and keys: 1024 in all, four per CU, shared by their heads, as far as
-// there are tokens for their waves
-void bwd_groups(int64_t tokens, int64_t hq, int64_t hk, int &gq, int &gk) {
-    const int64_t most = (tokens + kHW - 1) / kHW, q = hq + hk > 0 ? (1024 * hq + (hq + hk) / 2) / (hq + hk) : 0;
-    const auto cut = [&](int64_t n, int64_t heads) { return (int)(heads > 0 ? n < 1 ? 1 : n < most ? n : most : 0); };
-    gq = cut(q, hq);
-    gk = cut(1024 - q, hk);
+// Workgroups of the backward pass for queries and keys: 1024 in all, four per CU, shared by their passes, as far as there
+// are tokens for their waves (6 + 1 heads, 8192 tokens: by heads 32 us, by passes 17).
+constexpr int kBwdGroups = 1024;
+void bwd_groups(int64_t tokens, int64_t pq, int64_t pk, int &gq, int &gk) {
+    const int64_t most = (tokens + kHW - 1) / kHW, q = (kBwdGroups * pq + (pq + pk) / 2) / (pq + pk);
+    const auto cut = [&](int64_t n, int64_t passes) { return (int)(passes > 0 ? n < 1 ? 1 : n < most ? n : most : 0); };
+    gq = cut(q, pq);
+    gk = cut(kBwdGroups - q, pk);
+}
+
+hipError_t launch_dw(const RopeArgs &a, int gq, int gk, hipStream_t s) {
+    hipLaunchKernelGGL(k_heads_dw, dim3((unsigned)((a.dim + kSC - 1) / kSC), 2), dim3(kSC * kSR), 0, s, (const float *)a.ws, gq,
+                       gk, a.dim, a.s[0].dw, a.s[1].dw);
+    return hipGetLastError();
 }
 
 template <int V, int L, bool INTER, bool NT>
 hipError_t launch_nt(const RopeArgs &all, int op, hipStream_t s) {
+    constexpr int G = 64 / L;
+    const int64_t pq = ((int64_t)all.s[0].heads + G - 1) / G, pk = ((int64_t)all.s[1].heads + G - 1) / G, passes = pq + pk;
     if (op == NORM_ROPE_BWD) {
         int gq, gk;
-        bwd_groups(all.tokens, all.s[0].heads, all.s[1].heads, gq, gk);
+        bwd_groups(all.tokens, pq, pk, gq, gk);
         hipLaunchKernelGGL((k_heads_bwd<V, L, INTER, NT>), dim3((unsigned)(gq + gk)), dim3(64 * kHW), 0, s, all, gq);
-        return hipGetLastError();
+        const hipError_t e = hipGetLastError();
+        return e != hipSuccess || (!all.s[0].dw && !all.s[1].dw) ? e : launch_dw(all, gq, gk, s);
     }
-    constexpr int G = 64 / L;
-    const int64_t passes = ((int64_t)all.s[0].heads + G - 1) / G + ((int64_t)all.s[1].heads + G - 1) / G;
     const int64_t parts = (passes + kPasses<V> - 1) / kPasses<V>;
     const int64_t most = ((int64_t)1 << 25) / parts;  // tokens per launch: waves and threads in 32 bits
     for (int64_t t = 0; t < all.tokens; t += most) {
@@ -451,21 +468,15 @@ hipError_t launch_layout(const RopeArgs &a, int op, hipStream_t s) {
 }  // namespace
 
 int64_t heads_workspace(int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t dim) {
-    int gq, gk;
-    bwd_groups(tokens, heads_q, heads_k, gq, gk);
-    return (int64_t)(gq + gk) * dim;
+    // a row for each workgroup: kBwdGroups, one more where a set's share rounds to none
+    const int64_t most = 2 * ((tokens + kHW - 1) / kHW);
+    return heads_q + heads_k > 0 ? (most < kBwdGroups + 1 ? most : kBwdGroups + 1) * dim : 0;
 }
 
 hipError_t launch_heads(const RopeArgs &a, int op, hipStream_t s) {
-    hipError_t e = hipSuccess;
     if (a.tokens > 0 && a.s[0].heads + (int64_t)a.s[1].heads > 0)
-        e = a.interleaved ? launch_layout<true>(a, op, s) : launch_layout<false>(a, op, s);
-    if (e != hipSuccess || op != NORM_ROPE_BWD || (!a.s[0].dw && !a.s[1].dw)) return e;
-    int gq, gk;
-    bwd_groups(a.tokens, a.s[0].heads, a.s[1].heads, gq, gk);
-    hipLaunchKernelGGL(k_heads_dw, dim3((unsigned)((a.dim + kSC - 1) / kSC), 2), dim3(kSC * kSR), 0, s, (const float *)a.ws, gq,
-                       gk, a.dim, a.s[0].dw, a.s[1].dw);
-    return hipGetLastError();
+        return a.interleaved ? launch_layout<true>(a, op, s) : launch_layout<false>(a, op, s);
+    return op == NORM_ROPE_BWD && (a.s[0].dw || a.s[1].dw) ? launch_dw(a, 0, 0, s) : hipSuccess;
 }
 
 }  // namespace mx
