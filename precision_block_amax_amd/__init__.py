@@ -415,7 +415,12 @@ def _current(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+_FP8 = {"e4m3": E4M3, "e5m2": E5M2}
+
+
 def _fp8(f: Union[str, int]) -> int:
+    if f in _FP8:
+        return _FP8[f]
     f = _fmt(f)
     if f == E2M1:
         raise ValueError("block-128 operands are e4m3 or e5m2")
@@ -576,15 +581,34 @@ def block_quantize_grouped_dual(x: torch.Tensor, ends: torch.Tensor, fmt_row, fm
     return cr, sr, ct, st
 
 
-def _stacked(t: torch.Tensor, dtype: torch.dtype, groups: int, rows: int, width: int, device, what: str) -> Tuple[int, int]:
-    """group and row strides (elements) of a [groups x rows x width] tensor with contiguous rows"""
-    if t.dtype is not dtype or t.shape != (groups, rows, width) or t.device != device:
-        raise ValueError("%s must be %s of shape (%d, %d, %d) on %s" % (what, dtype, groups, rows, width, device))
-    lg, ld, step = t.stride()
-    if step != 1 and width > 1 and t.numel():
+def _strides(t: torch.Tensor, dtype: torch.dtype, shape: Tuple[int, ...], index: int, what: str) -> Tuple[int, ...]:
+    """the strides (elements) of a tensor of this type, shape and GPU with contiguous rows"""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        raise ValueError("%s must be %s of shape %s on GPU %d" % (what, dtype, tuple(shape), index))
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1 and t.numel():
         raise ValueError("the rows of %s must be contiguous" % what)
-    ld = ld if rows > 1 else width
-    return (lg if groups > 1 else rows * ld), ld
+    return st
+
+
+def _stacked(t: torch.Tensor, dtype: torch.dtype, shape: Tuple[int, int, int], index: int, what: str) -> Tuple[int, int]:
+    """group and row strides (elements) of a [groups x rows x width] tensor; what has one row or group has no stride"""
+    lg, ld, _ = _strides(t, dtype, shape, index, what)
+    if shape[1] <= 1:
+        ld = shape[2]
+    return lg if shape[0] > 1 else shape[1] * ld, ld
+
+
+def _grouped_types(a_codes: torch.Tensor, fa, fb, ends: torch.Tensor, out_dtype: torch.dtype) -> Tuple[int, int, int, int]:
+    """formats, the number of groups and the device index"""
+    if out_dtype is not _BF16 and out_dtype is not _F32:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    index = a_codes.get_device()
+    if index < 0:
+        raise ValueError("operands must be on a GPU")
+    if ends.dtype is not torch.int32 or ends.dim() != 1 or ends.get_device() != index or not ends.is_contiguous():
+        raise ValueError("ends must be contiguous int32 of one dimension on GPU %d" % index)
+    return _fp8(fa), _fp8(fb), ends.shape[0], index
 
 
 def block_gemm_grouped(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_codes: torch.Tensor, b_scales: torch.Tensor, fb,
@@ -596,25 +620,26 @@ def block_gemm_grouped(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_code
     weights as one [groups * N x K] matrix may be viewed as B for the product and for its gradient
     (include/mx.h).  Rows of C behind the last end are left as they are.  out_dtype and full_sums
     as in block_gemm."""
-    f_a, f_b = _fp8(fa), _fp8(fb)
-    if a_codes.dim() != 2 or a_scales.dim() != 2 or b_codes.dim() != 3 or b_scales.dim() != 3 or not a_codes.is_cuda:
-        raise ValueError("expected a 2-D A and a 3-D B on a GPU")
-    dev = a_codes.device
-    groups = _ends(ends, dev)
-    (M, K), N = a_codes.shape, b_codes.shape[1]
-    if out_dtype is not _BF16 and out_dtype is not _F32:
-        raise ValueError("out_dtype must be float32 or bfloat16")
+    f_a, f_b, groups, index = _grouped_types(a_codes, fa, fb, ends, out_dtype)
+    sa, sb = a_codes.shape, b_codes.shape
+    if len(sa) != 2 or len(sb) != 3 or sb[0] != groups or sb[2] != sa[1] or b_scales.dim() != 3:
+        raise ValueError("expected A [rows x K], B [%d x N x K] and B's scales for each of them" % groups)
+    (M, K), N = sa, sb[1]
     kb, tiles = _cdiv(K, BLOCK), _cdiv(N, BLOCK)
     tile = tiles != N and b_scales.shape[2] == tiles
-    lda = _rows_of(a_codes, _U8, M, K, dev, "A's codes")
-    ldsa = _rows_of(a_scales, _F32, kb, M, dev, "A's scales")
-    ldbg, ldb = _stacked(b_codes, _U8, groups, N, K, dev, "B's codes")
-    ldsbg, ldsb = _stacked(b_scales, _F32, groups, kb, tiles if tile else N, dev, "B's scales")
+    lda, _ = _strides(a_codes, _U8, sa, index, "A's codes")
+    ldsa, _ = _strides(a_scales, _F32, (kb, M), index, "A's scales")
+    if M <= 1:
+        lda = K
+    if kb <= 1:
+        ldsa = M
+    ldbg, ldb = _stacked(b_codes, _U8, sb, index, "B's codes")
+    ldsbg, ldsb = _stacked(b_scales, _F32, (groups, kb, tiles if tile else N), index, "B's scales")
+    bf16, dev = out_dtype is _BF16, a_codes.device
     ldc = N if out is None else _rows_of(out, out_dtype, M, N, dev, "out")
     with _scope(dev, stream):
         if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        bf16 = out_dtype is _BF16
+            out = torch.empty_strided((M, N), (N, 1), dtype=out_dtype, device=dev)
         _check(lib().mx_block_gemm_grouped(a_codes.data_ptr(), lda, a_scales.data_ptr(), ldsa, f_a, b_codes.data_ptr(), ldbg, ldb,
                                            b_scales.data_ptr(), ldsbg, ldsb, f_b, 1 if tile else 0, ends.data_ptr(), groups, M,
                                            N, K, out.data_ptr(), OUT_BF16 if bf16 else OUT_F32, ldc,
@@ -629,25 +654,21 @@ def block_gemm_grouped_k(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_co
     [M x cols] and B [N x cols] as block_quantize_grouped gives them for the same ends: the
     groups' weight gradients.  An empty group's C is zeros.  out_dtype and full_sums as in
     block_gemm."""
-    f_a, f_b = _fp8(fa), _fp8(fb)
-    if a_codes.dim() != 2 or b_codes.dim() != 2 or a_scales.dim() != 2 or b_scales.dim() != 2 or not a_codes.is_cuda:
-        raise ValueError("expected 2-D operands on a GPU")
-    dev = a_codes.device
-    groups = _ends(ends, dev)
-    (M, K), N = a_codes.shape, b_codes.shape[0]
-    if b_codes.shape[1] != K:
-        raise ValueError("A and B disagree on the columns")
-    if out_dtype is not _BF16 and out_dtype is not _F32:
-        raise ValueError("out_dtype must be float32 or bfloat16")
+    f_a, f_b, groups, index = _grouped_types(a_codes, fa, fb, ends, out_dtype)
+    sa, sb = a_codes.shape, b_codes.shape
+    if len(sa) != 2 or len(sb) != 2 or sa[1] != sb[1]:
+        raise ValueError("expected A [M x cols] and B [N x cols]")
+    (M, K), N = sa, sb[0]
     kb = _cdiv(K, BLOCK)
+    dev = a_codes.device
     lda = _rows_of(a_codes, _U8, M, K, dev, "A's codes")
     ldb = _rows_of(b_codes, _U8, N, K, dev, "B's codes")
     ldsa = _rows_of(a_scales, _F32, kb, M, dev, "A's scales")
     ldsb = _rows_of(b_scales, _F32, kb, N, dev, "B's scales")
-    ldcg, ldc = (M * N, N) if out is None else _stacked(out, out_dtype, groups, M, N, dev, "out")
+    ldcg, ldc = (M * N, N) if out is None else _stacked(out, out_dtype, (groups, M, N), index, "out")
     with _scope(dev, stream):
         if out is None:
-            out = torch.empty((groups, M, N), dtype=out_dtype, device=dev)
+            out = torch.empty_strided((groups, M, N), (M * N, N, 1), dtype=out_dtype, device=dev)
         bf16 = out_dtype is _BF16
         _check(lib().mx_block_gemm_grouped_k(a_codes.data_ptr(), lda, a_scales.data_ptr(), ldsa, f_a, b_codes.data_ptr(), ldb,
                                              b_scales.data_ptr(), ldsb, f_b, ends.data_ptr(), groups, M, N, K, out.data_ptr(),
