@@ -20,6 +20,10 @@
  *     path (FP4-training article, section 02: one fixed orthogonal transform
  *     in place of random rotations), applied along tokens before the FP4
  *     quantization of both weight-gradient operands.
+ *   - Products by expert (MindSpeed-LLM FSDP2 page: quantization of the experts'
+ *     layers, quantize.moe.mx, and Qwen3-30B-A3B, whose attention normalises the
+ *     heads of queries and keys) and rotary positions with Llama-3.1's frequency
+ *     bands: the block-128 calls by group and the calls on heads below.
  *   - The quantized GEMMs of a linear layer (FP4-training article, section
  *     02: forward, activation-gradient and weight-gradient GEMMs), which the
  *     Primus page names as the dominant training cost (GEMM tuning section).
@@ -33,6 +37,7 @@
  *     accumulation).  Inputs and outputs must not overlap.
  *   - bf16 inputs are row-major with a leading dimension `ldx` (elements
  *     between the starts of consecutive rows, ldx >= cols).
+ *     (The calls by group leave what belongs to no group as it was.)
  *   - Outputs are dense row-major (the _panels calls and pair modes write
  *     their codes in the K-panel layout described before them instead):
  *       FP8 codes   : one byte per element;
@@ -43,8 +48,8 @@
  *     element codes 0.  An all-zero block gets scale 0x00.  The sign of zero
  *     is kept (-0 -> 0x80 for FP8, 0x8 for E2M1).
  *   - A size of 0 is a valid empty call: nothing is read or written (except
- *     mx_gemm and mx_block_gemm with K == 0, which write C = 0, and
- *     mx_layer_norm_backward with rows == 0, which writes zero gradients of the
+ *     mx_gemm and the block-128 products with K == 0, which write C = 0, and the
+ *     norms' backward passes without rows, which write zero gradients of the
  *     parameters), and pointers may be NULL.
  *
  * Errors (no call throws, no call aborts):

@@ -275,6 +275,40 @@ def test_ends_that_are_no_ranges(mx):
         check(mx.block_gemm_grouped_k(*ones, "e4m3", *ones, "e4m3", t), C, S, 3, True)
 
 
+def test_offsets_beyond_31_bits(mx):
+    """C of more than 2^31 elements, by rows and by groups; a stack of weights of more than 2^31 bytes"""
+    import torch
+    free = torch.cuda.mem_get_info()[0]
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB of GPU memory")
+    g = torch.Generator(device="cuda").manual_seed(33)
+    codes = lambda *s: torch.randint(0x20, 0x48, s, device="cuda", generator=g, dtype=torch.uint8)
+    rows, N = 70100, 32768
+    a, b = (codes(rows, 16), torch.ones(1, rows, device="cuda")), (codes(2, N, 16), torch.ones(2, 1, N // 128, device="cuda"))
+    ends = torch.tensor([60000, rows], dtype=torch.int32, device="cuda")
+    c = mx.block_gemm_grouped(*a, "e4m3", *b, "e4m3", ends)
+    v = lambda t: t.view(torch.float8_e4m3fn).double()
+    for lo, i in ((0, 0), (59990, 0), (60000, 1), (rows - 200, 1)):
+        want = v(a[0][lo:lo + 10]) @ v(b[0][i]).t().contiguous()
+        assert ((c[lo:lo + 10].double() - want).abs() <= 2.0 ** -7 * want).all()  # (all terms positive)
+    del c
+    a, b = (codes(16384, 1152), torch.ones(9, 16384, device="cuda")), (codes(16384, 1152), torch.ones(9, 16384, device="cuda"))
+    ends = torch.arange(128, 1153, 128, dtype=torch.int32, device="cuda")
+    c = mx.block_gemm_grouped_k(*a, "e4m3", *b, "e4m3", ends, out_dtype=torch.bfloat16, full_sums=True)
+    for i in (0, 7, 8):
+        cut = slice(128 * i, 128 * i + 128)
+        want = v(a[0][-40:, cut].contiguous()) @ v(b[0][:, cut].contiguous()).t().contiguous()
+        assert ((c[i, -40:].double() - want).abs() <= (2.0 ** -8 + 130 * 2.0 ** -24) * want).all()
+    del c, a, b
+    w = (codes(3, 32768, 32768), torch.ones(3, 256, 256, device="cuda"))
+    a = (codes(40, 32768), torch.ones(256, 40, device="cuda"))
+    ends = torch.tensor([7, 7, 40], dtype=torch.int32, device="cuda")
+    c = mx.block_gemm_grouped(*a, "e4m3", *w, "e4m3", ends, out_dtype=torch.float32)
+    for lo, hi, i in ((0, 7, 0), (7, 40, 2)):
+        want = v(a[0][lo:hi]) @ v(w[0][i, -300:]).t().contiguous()
+        assert ((c[lo:hi, -300:].double() - want).abs() <= (130 + 256) * 2.0 ** -24 * want).all()
+
+
 def test_special_values(mx):
     """a NaN scale or code reaches its own row, or its own group, only"""
     import torch

@@ -197,6 +197,29 @@ def test_refusals(mx):
             call()
 
 
+def test_offsets_beyond_31_bits(mx):
+    """more than 2^31 elements, tokens outermost and heads outermost"""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of GPU memory")
+    T, H, D = 270000, 64, 128
+    g = torch.Generator(device="cuda").manual_seed(13)
+    q = torch.empty(T, H, D, dtype=torch.bfloat16, device="cuda")
+    q.normal_(generator=g)
+    f, w = mx.rope_frequencies(D, 500000.0), (1 + 0.3 * torch.randn(D, device="cuda", generator=g)).bfloat16()
+    pos = torch.arange(T, device="cuda")
+    at = torch.tensor([0, 1, 131072, T // 2 + 7, T - 1], device="cuda")
+    y, _ = mx.rope(q, None, pos, f)
+    close(y[at], *ref.rotate(q[at], pos[at], f, "half"))
+    dx, _, dw, _ = mx.qk_norm_rope_backward(y, None, q, None, w, None, pos, f, weight_grad=False)
+    want, _, mag, _ = ref.norm_rope_backward(y[at], q[at], w, pos[at], f, 1e-5, "half")
+    close(dx[at], want, mag)
+    del dx
+    outer = q.view(H, T, D).transpose(0, 1)
+    y, _ = mx.qk_norm_rope(outer, None, w, None, pos, f)
+    close(y[at], *ref.norm_rope(outer[at], w, pos[at], f, 1e-5, "half"))
+
+
 def test_empty(mx):
     import torch
     q, k, w, pos, f, (dq, dk) = data(4, 3, 2, 64, 11, 64)
