@@ -916,10 +916,10 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch
     with _scope(dev, stream):
         oq, *qo = _like(q, oq, index, "dxq")
         ok, *ko = _like(k, ok, index, "dxk")
-        dwq = torch.empty((dim,), dtype=_F32, device=dev) if weight_grad else None
-        dwk = torch.empty((dim,), dtype=_F32, device=dev) if weight_grad and k is not None else None
+        dwq = torch.empty_strided((dim,), (1,), dtype=_F32, device=dev) if weight_grad else None
+        dwk = torch.empty_strided((dim,), (1,), dtype=_F32, device=dev) if weight_grad and k is not None else None
         need = lib().mx_qk_norm_rope_backward_workspace(tokens, qh[3], kh[3], dim) if weight_grad else 0
-        ws = torch.empty((need,), dtype=_U8, device=dev) if need else None
+        ws = torch.empty_strided((need,), (1,), dtype=_U8, device=dev) if need else None
         _check(lib().mx_qk_norm_rope_backward(*gq[:3], *gk[:3], *qh, *kh, tokens, dim, wq, wk, p, eps, *rotation, scale, *qo,
                                               *ko, _ptr(dwq), _ptr(dwk), _ptr(ws), need, _current(dev)))
     return oq, ok, dwq, dwk
