@@ -733,8 +733,8 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
 }
 
 // ---------------------------------------------------------------------------
-// Kernel for few rows: tiles of 8 AI x 16 NT of C, a workgroup's eight waves each
-// taking every eighth block of K for the whole tile, joined in LDS.
+// Kernel for few rows: tiles of 8 AI x 16 NT of C, a workgroup's DW waves each
+// taking every DW-th block of K for the whole tile, joined in LDS.
 //
 // With one row the product is bound by B's bytes.  16 rows of B per workgroup
 // make 256 workgroups from N = 4096 on, and the waves' blocks in flight cover
@@ -745,8 +745,6 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
 // 14336 took 28 us at 16 bytes per clock and CU, whatever was in flight; through
 // LDS 16 us, 3.7 TB/s of its operands, and 256 times A besides from L2.  1 x 6144 x
 // 4096 takes 7.5 us, 3.4 TB/s, of which launch and a first read's latency are half.
-constexpr int DW = 8;  // waves
-
 struct Frag2 {
     uint4 c[2];
 };
@@ -770,7 +768,9 @@ __device__ __forceinline__ v4f few_block(const Frag2 &a, const Frag2 &b) {
 
 // AI: loads of 8 rows of A; with an odd AI the rest of the matrix instruction's 16 rows is whatever LDS
 // holds, and reaches only rows of C that do not exist
-template <int FA, int FB, bool BT, bool FP8SUMS, int AI, int NT, int S, int GRP>
+// (eight waves, or four by groups of rows, where there are more workgroups: one token's 8 of 128 x 1536 x 2048 9.7 -> 8.1 us,
+// one row of each of 128 66 -> 48)
+template <int FA, int FB, bool BT, bool FP8SUMS, int AI, int NT, int S, int GRP, int DW>
 __global__ __launch_bounds__(64 * DW) void k_block_gemm_few(ArgsOf<GRP> g) {
     constexpr int MT = (AI + 1) / 2, DM = 16 * MT, DN = 16 * NT, JP = DN + 4;
     constexpr int OB = MT * 2048, OS = OB + NT * 2048, BLK = OS + 512;  // a block: A's rows, B's, scales of A, of B
@@ -914,8 +914,8 @@ template <int FA, int FB, bool BT, bool FP8SUMS, int AI, int NT, int S>
 hipError_t launch_block_gemm_few(BlockGemmArgs g, hipStream_t s) {
     g.tiles_m = (g.M + 8 * AI - 1) / (8 * AI);
     g.tiles_n = (g.N + 16 * NT - 1) / (16 * NT);
-    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, BT, FP8SUMS, AI, NT, S, NOT>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
-                       dim3(64 * DW), 0, s, g);
+    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, BT, FP8SUMS, AI, NT, S, NOT, 8>), dim3((unsigned)(g.tiles_m * g.tiles_n)),
+                       dim3(512), 0, s, g);
     return hipGetLastError();
 }
 
@@ -996,8 +996,8 @@ hipError_t launch_block_gemm_as(BlockGemmArgs g, hipStream_t s) {
 template <int FA, int FB, bool BT, bool FP8SUMS, int AI, int NT, int S>
 hipError_t launch_grouped_few(GroupedGemmArgs g, hipStream_t s) {
     g.tiles_n = (g.N + 16 * NT - 1) / (16 * NT);
-    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, BT, FP8SUMS, AI, NT, S, ROWS>),
-                       dim3((unsigned)(grouped_units(g.M, g.groups, 8 * AI) * g.tiles_n)), dim3(64 * DW), 0, s, g);
+    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, BT, FP8SUMS, AI, NT, S, ROWS, 4>),
+                       dim3((unsigned)(grouped_units(g.M, g.groups, 8 * AI) * g.tiles_n)), dim3(256), 0, s, g);
     return hipGetLastError();
 }
 
@@ -1015,8 +1015,8 @@ template <int FA, int FB, bool FP8SUMS>
 hipError_t launch_grouped_cols_few(GroupedGemmArgs g, hipStream_t s) {
     g.tiles_m = (g.M + 63) / 64;
     g.tiles_n = (g.N + 31) / 32;
-    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, false, FP8SUMS, 8, 2, 1, COLS>),
-                       dim3((unsigned)(g.tiles_m * g.tiles_n * g.groups)), dim3(64 * DW), 0, s, g);
+    hipLaunchKernelGGL((k_block_gemm_few<FA, FB, false, FP8SUMS, 8, 2, 1, COLS, 8>),
+                       dim3((unsigned)(g.tiles_m * g.tiles_n * g.groups)), dim3(512), 0, s, g);
     return hipGetLastError();
 }
 
@@ -1043,9 +1043,12 @@ struct Rate {
     int per;
     float a, b, first;
     float us(float tiles, int64_t nk) const {
-        const float slots = 256.f * per, full = floorf(tiles / slots), rest = ceilf((tiles - full * slots) / 256.f);
-        const float part = rest == 0.f ? 0.f : per == 1 ? 1.f : first + (1.f - first) * (rest - 1.f) / (float)(per - 1);
-        return (full + part) * (a + b * (float)nk);
+        const int full = (int)(tiles / (256.f * per));
+        const float last = tiles / 256.f - (float)(full * per);  // workgroups per CU in the last round
+        int rest = (int)last;
+        rest += (float)rest < last;
+        const float part = rest == 0 ? 0.f : per == 1 ? 1.f : first + (1.f - first) * (float)(rest - 1) / (float)(per - 1);
+        return ((float)full + part) * (a + b * (float)nk);
     }
 };
 
@@ -1053,14 +1056,20 @@ struct Rate {
 // so tiles are counted as for rows that fall on groups at random: groups (1 - exp(-mean)) of them have rows, each half a
 // tile and a little more at its end.  The rates below were fitted to measured times (us, MI355X, weights taking turns)
 // of groups x N x K from 1 x 4096 x 4096 to 128 x 1536 x 2048 and 8 x 28672 x 4096 with means of 1/16 to 8192 rows, the
-// most popular group ten times the least; the kernel that they choose is the fastest or within a tenth of it in most of
-// these.  FP8 sums, B in tiles:
-//   128 x 1536 x 2048   mean of 1/16  8 x 16 tiles 9, 64 x 128 12, 128 x 128 13
-//                       4             115, 64, 67       64  91 (64 x 128), 91, 256 x 256 105, 64 x 32 227
-//                       128           124, 114, 120     512  344, 291, 263
-//   8 x 2048 x 14336    1             8 x 16 20, 64 x 32 31, 128 x 128 in two groups 75, in one 100
-//                       32            101, 67, 80, 95   256  593, 200, 156, 123, 256 x 256 162
-//   8 x 28672 x 4096    8             236 (8 x 16), 64 x 128 197, 128 x 128 202    2048  2787, 2262, 256 x 256 1788
+// most popular group ten times the least; the kernel that they choose was within a tenth of the fastest in 119 of 127 of
+// these.  FP8 sums, B in tiles (8 x 16, 16 x 16, 64 x 32, 128 x 128 in two groups of waves, 128 x 128, 64 x 128, 256 x 256):
+//   128 x 1536 x 2048   mean of 1/16    8.3   8.2   8.8   12    13    12    26
+//                       4                83    79    82   93    67    64    83
+//                       64              488   298   132  116    91    91   104
+//                       128             906   531   204  149   114   123   118
+//                       512            3320  1865   618  421   289   339   260
+//   8 x 2048 x 14336    1                21    22    35   76    99    92   150
+//                       32              100    79    68   80    92    86   150
+//                       128             288   205   119   83    94    96   156
+//                       256             541   369   199  154   114   137   162
+//   8 x 28672 x 4096    2               104   103   116  142   135   125   154
+//                       32              491   330   228  214   196   199   213
+//                       2048          24786 14656  4647 3048  2148  2745  1778
 template <int FA, int FB, bool BT, bool FP8SUMS>
 hipError_t launch_grouped_as(GroupedGemmArgs g, hipStream_t s) {
     const int64_t nk = (g.K + kBlk - 1) / kBlk;
@@ -1082,25 +1091,28 @@ hipError_t launch_grouped_as(GroupedGemmArgs g, hipStream_t s) {
         return grouped_units(g.M, g.groups, m) * ((g.N + n - 1) / n) < (int64_t)1 << 22;
     };
     enum { FEW8, FEW16, FEW64, SPLIT, TWO, HALF, BIG } best = TWO;
-    float least = Rate{2, 3.f, !FP8SUMS ? 1.85f : BT ? 1.1f : 1.25f, !FP8SUMS ? 0.56f : 0.65f}.us(tiles(128, 128), nk);
-    const auto offer = [&](decltype(best) k, float us) {
-        if (us < least) {
-            least = us;
+    // the weights' bytes at 5.3 TB/s; few rows: B for each tile at 6.2
+    const float bytes = met * (float)g.N * (float)g.K / 5.3e6f;
+    const auto few_bytes = [&](int m, int n) { return tiles(m, n) * (float)n * (float)g.K / 6.2e6f; };
+    float least = fmaxf(bytes, Rate{2, 3.f, !FP8SUMS ? 1.85f : BT ? 1.1f : 1.25f, !FP8SUMS ? 0.56f : 0.65f}.us(tiles(128, 128), nk));
+    const auto offer = [&](decltype(best) k, float floor, float us) {
+        if (fmaxf(floor, us) < least) {
+            least = fmaxf(floor, us);
             best = k;
         }
     };
-    if (FP8SUMS && fits(64, 128)) offer(HALF, Rate{3, 1.f, 1.2f, 0.6f}.us(tiles(64, 128), nk));
+    if (FP8SUMS && fits(64, 128)) offer(HALF, bytes, Rate{3, 1.f, 1.2f, 0.6f}.us(tiles(64, 128), nk));
     if (FP8SUMS && BT) {
         const float t = tiles(256, 256);
-        offer(BIG, Rate{1, 4.f, t > 256.f ? 1.75f : 1.3f, 0.f}.us(t, nk));
+        offer(BIG, bytes, Rate{1, 4.f, t > 256.f ? 1.75f : 1.3f, 0.f}.us(t, nk));
     }
     // one round at most, and sure of it: a second one has every CU wait for its few
-    if (tiles(128, 128) <= 282.f && (8 * rows <= 128.f * g.groups || tiles(128, 128) <= 220.f || g.groups == 1))
-        offer(SPLIT, Rate{1, 2.f, FP8SUMS ? 0.6f : 0.87f, 0.f}.us(fminf(tiles(128, 128), 256.f), nk));
-    if (fits(64, 32)) offer(FEW64, Rate{1, 3.f, 0.16f, 0.f}.us(tiles(64, 32), nk));
+    if (tiles(128, 128) <= 282.f && (8 * rows <= 128.f * g.groups || tiles(128, 128) <= 230.f || g.groups == 1))
+        offer(SPLIT, bytes, Rate{1, 4.5f, FP8SUMS ? 0.57f : 0.85f, 0.f}.us(fminf(tiles(128, 128), 256.f), nk));
+    if (fits(64, 32)) offer(FEW64, few_bytes(64, 32), Rate{3, 3.f, FP8SUMS ? 0.47f : 0.52f, 0.55f}.us(tiles(64, 32), nk));
     if (fits(8, 16)) {
-        offer(FEW16, Rate{2, 3.6f, 0.115f, 0.7f}.us(tiles(16, 16), nk));
-        offer(FEW8, Rate{2, 3.5f, 0.11f, 0.7f}.us(tiles(8, 16), nk));
+        offer(FEW16, few_bytes(16, 16), Rate{4, 3.2f, 0.17f, 0.6f}.us(tiles(16, 16), nk));
+        offer(FEW8, few_bytes(8, 16), Rate{4, 3.1f, 0.165f, 0.6f}.us(tiles(8, 16), nk));
     }
     switch (best) {
     case FEW8: return launch_grouped_few<FA, FB, BT, FP8SUMS, 1, 1, 2>(g, s);

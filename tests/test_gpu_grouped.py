@@ -275,6 +275,35 @@ def test_ends_that_are_no_ranges(mx):
         check(mx.block_gemm_grouped_k(*ones, "e4m3", *ones, "e4m3", t), C, S, 3, True)
 
 
+@pytest.mark.parametrize("groups", [64, 65, 255, 256, 257, 511, 700, 1025])
+def test_many_groups(mx, groups):
+    """as many groups as one read of the ends holds, and more: rows at either side of its border and behind it"""
+    import torch
+    g = torch.Generator().manual_seed(groups)
+    sizes = torch.randint(0, 3, (groups,), generator=g)
+    sizes[torch.randint(0, groups, (3,), generator=g)] = 140
+    sizes[-1] = 5
+    sizes = sizes.tolist()
+    rows, ends = sum(sizes) + 4, ends_of(sizes)
+    e = ends.tolist()
+    x, y = data(rows, 64, seed=34), data(rows, 48, seed=35)
+    k = grp.bound(rows, groups)
+    out = lambda n: (torch.zeros(n, k, dtype=torch.uint8, device="cuda"), torch.zeros(k // 128, n, device="cuda"))
+    qx, qy = mx.block_quantize_grouped(x, ends, "e4m3", out=out(64)), mx.block_quantize_grouped(y, ends, "e5m2", out=out(48))
+    for got, want in ((qx, grp.quantize(x, e, "e4m3")), (qy, grp.quantize(y, e, "e5m2"))):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    C, S = grp.gemm_k(qy, "e5m2", qx, "e4m3", e)
+    check(mx.block_gemm_grouped_k(*qy, "e5m2", *qx, "e4m3", ends), C, S, 2, True)
+    a, w = mx.block_quantize(x, "e4m3"), data(groups, 40, 64, seed=36)
+    cw, sw = mx.block_quantize(w.view(groups * 40, 64), "e4m3")
+    b = (cw.view(groups, 40, 64), sw.view(1, groups, 40).transpose(0, 1))
+    C, S = grp.gemm(a, "e4m3", b, "e4m3", e, False)
+    c = torch.full((rows, 40), 9.0, device="cuda")
+    mx.block_gemm_grouped(*a, "e4m3", *b, "e4m3", ends, out_dtype=torch.float32, out=c)
+    check(c[:rows - 4], C[:rows - 4], S[:rows - 4], 1, True)
+    assert (c[rows - 4:] == 9).all()
+
+
 def test_offsets_beyond_31_bits(mx):
     """C of more than 2^31 elements, by rows and by groups; a stack of weights of more than 2^31 bytes"""
     import torch
