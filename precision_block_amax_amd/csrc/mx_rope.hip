@@ -7,7 +7,7 @@
 // 2 pi less the nearest whole number: what is left is exact to p * 2^-53 turns,
 // then rounded to fp32, 2^-25 of a turn, 2^-23 of its radius (fp32 products of far
 // positions, 2^17 and more, would be off by 2^-8 and more).  One lane makes one
-// angle; they go through LDS to the lanes that need them, once for all heads.
+// angle; they go through LDS to the lanes that need them, for all heads of a wave.
 //
 // Norm: xh = x * rstd, rstd = 1 / sqrt(mean(x^2) + eps) over the head, y = rope(xh * w).
 // Backward, with u = inverse rotation of dy, g = u * w:
@@ -20,6 +20,13 @@
 // each of L lanes, two vectors of eight.  In the half layout these are the two
 // halves of eight pairs, so pairs never cross lanes and a head's sums are a DPP tree
 // over L lanes.  Everything is fp32 until the one rounding to bf16.
+//
+// Bound by memory: 2 bytes read and 2 written per element, backward 4 and 2.  Measured
+// with inputs in turn, heads of 128: rotation of 8192 tokens x 72 heads (302 MB) 50 us,
+// 6.0 TB/s; norm and rotation of 8192 x 40 (168 MB) 28 us, 6.0 TB/s, backward (252 MB) 51
+// us, 4.9 TB/s, and 4.5 for the weights' sums; of 32768 x 40 114 us and 198.  A copy
+// reaches 5.2 from HBM; part of these inputs is still in the last-level cache.
+// One token: 2.5 us, launch and latency.
 #include <type_traits>
 
 #include "mx_block_util.h"
@@ -330,8 +337,10 @@ __global__ __launch_bounds__(64 * kHW, V ? 4 : 1) void k_heads_bwd(RopeArgs a, i
                 sq = __builtin_fmaf(v[s], v[s], sq);
                 sg = __builtin_fmaf(u[s] * w[s], v[s], sg);
             }
-            const float rstd = live ? rsqrt1(__builtin_fmaf(group_sum<L>(sq), rn, a.eps)) : 0.f;
-            const float mean = group_sum<L>(sg) * rstd * rn;  // of g * xh
+            sq = group_sum<L>(sq);
+            sg = group_sum<L>(sg);
+            const float rstd = live ? rsqrt1(__builtin_fmaf(sq, rn, a.eps)) : 0.f;
+            const float mean = sg * rstd * rn;  // of g * xh
 #pragma unroll
             for (int s = 0; s < M::NS; s++) {
                 const float xh = v[s] * rstd;
