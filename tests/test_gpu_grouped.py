@@ -87,6 +87,29 @@ def test_quantize(mx, sizes, behind, cols):
         assert (rc[live:] == 0x11).all() and (rs[:, live:] == 3).all()
 
 
+@pytest.mark.parametrize("rows,cols", [(16500, 4096), (500, 200), (500, 208), (500, 203)])
+def test_quantize_formats(mx, rows, cols):
+    """every pair of formats, and more than 2^26 elements, against each group quantized by itself"""
+    import torch
+    ends = ends_of([rows // 3, 0, 129, rows // 2])                        # of 500 rows the last end is cut
+    live = min(int(ends[-1]), rows)
+    x = data(rows, cols, seed=45)
+    pieces = list(zip(grp.ranges(ends.tolist(), rows), grp.blocks(ends.tolist(), rows)))
+    for fr in ("e4m3", "e5m2"):
+        for ft in ("e4m3", "e5m2"):
+            rc, rs, tc, ts = mx.block_quantize_grouped_dual(x, ends, fr, ft)
+            wc, ws = mx.block_quantize(x[:live], fr)
+            assert torch.equal(rc[:live], wc) and torch.equal(rs[:, :live], ws)
+            oc, os = mx.block_quantize_grouped(x, ends, ft)
+            for (lo, hi), (b0, b1) in pieces:
+                if hi == lo:
+                    continue
+                wc, ws = mx.block_quantize(x[lo:hi], ft, "transpose")
+                for codes, scales in ((tc, ts), (oc, os)):
+                    assert torch.equal(codes[:, 128 * b0:128 * b0 + hi - lo], wc) and torch.equal(scales[b0:b1], ws)
+                    assert (codes[:, 128 * b0 + hi - lo:128 * b1] == 0).all()
+
+
 # N, K: whole tiles and not, K in whole blocks, chunks of 16 bytes and neither
 SIZES = [(256, 256), (130, 400), (300, 129), (16, 1), (515, 640), (128, 15), (1, 48)]
 
@@ -126,6 +149,27 @@ def test_rows_of_every_kernel(mx, mean, fa, fb):
         print("case", mean, fa, fb, N, K, tile, flush=True)
         a = mx.block_quantize(data(rows, K, seed=3), fa)
         b = weights(mx, 5, N, K, fb, tile, 4)
+        C, S = grp.gemm(a, fa, b, fb, ends.tolist(), tile)
+        for dtype, full in ((torch.bfloat16, False), (torch.bfloat16, True), (torch.float32, True)):
+            check(mx.block_gemm_grouped(*a, fa, *b, fb, ends, out_dtype=dtype, full_sums=full), C, S, ref.cdiv(K, 128), full)
+
+
+# groups, rows, N, K where 128 x 128 tiles in two groups of waves are taken (with fp32 sums, with FP8 sums), 128 x 128,
+# and 256 x 256 (FP8 sums, B in tiles)
+@pytest.mark.parametrize("groups,rows,N,K", [(16, 80, 2048, 512), (16, 79, 2040, 505), (16, 80, 2048, 1536), (16, 79, 2040, 1531),
+                                             (5, 300, 4096, 1152), (5, 299, 4090, 1147),
+                                             (16, 2600, 2048, 512), (16, 2599, 2044, 505)])
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e5m2")])
+def test_rows_of_large_tiles(mx, groups, rows, N, K, fa, fb):
+    import torch
+    print("case", groups, rows, N, K, fa, fb, flush=True)
+    share = [i % 5 for i in range(groups)]                                # none, or one to four parts
+    sizes = [rows * w // sum(share) for w in share]
+    sizes[-1] += rows - sum(sizes)
+    ends = ends_of(sizes)
+    a = mx.block_quantize(data(rows, K, seed=41), fa)
+    for tile in (True, False):
+        b = weights(mx, groups, N, K, fb, tile, 42)
         C, S = grp.gemm(a, fa, b, fb, ends.tolist(), tile)
         for dtype, full in ((torch.bfloat16, False), (torch.bfloat16, True), (torch.float32, True)):
             check(mx.block_gemm_grouped(*a, fa, *b, fb, ends, out_dtype=dtype, full_sums=full), C, S, ref.cdiv(K, 128), full)
@@ -240,6 +284,24 @@ def test_long_columns_of_few_tiles(mx, groups, M, N):
         for dtype, full in ((torch.bfloat16, False), (torch.bfloat16, True), (torch.float32, True)):
             check(mx.block_gemm_grouped_k(*a, "e5m2", *b, "e4m3", ends, out_dtype=dtype, full_sums=full), C, S,
                   ref.cdiv(max(sizes), 128), full)
+
+
+# few tiles: the blocks of K shared by eight waves, by two groups of waves; one row of tiles
+@pytest.mark.parametrize("sizes", [[1500], [700, 0, 1300], [0, 900, 129, 600]], ids=str)
+@pytest.mark.parametrize("M,N", [(130, 70), (1050, 1100), (64, 33)])
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e5m2")])
+def test_columns_shared(mx, sizes, M, N, fa, fb):
+    import torch
+    rows, ends = sum(sizes), ends_of(sizes)
+    a = mx.block_quantize_grouped(data(rows, M, seed=43), ends, fa)
+    b = mx.block_quantize_grouped(data(rows, N, seed=44), ends, fb)
+    C, S = grp.gemm_k(a, fa, b, fb, ends.tolist())
+    buf = torch.full((M, a[0].shape[1] + 3), 0x7F, dtype=torch.uint8, device="cuda")
+    odd = buf[:, 1:1 + a[0].shape[1]]                                     # rows of no alignment: the general kernel
+    odd.copy_(a[0])
+    for dtype, full in ((torch.bfloat16, False), (torch.bfloat16, True), (torch.float32, True)):
+        for codes in (a[0], odd):
+            check(mx.block_gemm_grouped_k(codes, a[1], fa, *b, fb, ends, out_dtype=dtype, full_sums=full), C, S, 12, full)
 
 
 def test_unaligned_columns(mx):

@@ -89,6 +89,31 @@ def test_backward(mx, tokens, hq, hk, dim, rot, layout):
     assert mx.qk_norm_rope_backward(dq, dk, q, k, *w, pos, f, weight_grad=False)[2:] == (None, None)
 
 
+# more than 2^25 elements, which go past the caches: a size of head for every width of load, and below it the one that
+# the other tests have no head for
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("hq,hk,dim,rot,n", [(8, 2, 64, 64, 1 << 25), (7, 2, 128, 96, 1 << 25), (3, 2, 256, 64, 1 << 25),
+                                             (3, 1, 512, 512, 1 << 25), (9, 3, 72, 24, 1 << 25), (5, 4, 36, 12, 1 << 25),
+                                             (6, 1, 100, 20, 1 << 25), (3, 2, 148, 20, 1 << 25), (4, 3, 50, 26, 1 << 25),
+                                             (3, 2, 148, 20, 4000)])
+def test_large(mx, hq, hk, dim, rot, n, layout):
+    import torch
+    tokens = n // ((hq + hk) * dim) + 3
+    q, k, w, pos, f, (dq, dk) = data(tokens, hq, hk, dim, 14, rot)
+    out = mx.rope(q, k, pos, f, layout=layout)
+    for x, y in zip((q, k), out):
+        assert torch.equal(y[..., rot:], x[..., rot:])
+        close(y, *ref.rotate(x, pos, f, layout))
+    out = mx.qk_norm_rope(q, k, *w, pos, f, eps=1e-6, layout=layout)
+    for x, wt, y in zip((q, k), w, out):
+        close(y, *ref.norm_rope(x, wt, pos, f, 1e-6, layout))
+    out = mx.qk_norm_rope_backward(dq, dk, q, k, *w, pos, f, eps=1e-6, layout=layout)
+    for x, d, wt, dx, dw in zip((q, k), (dq, dk), w, out[:2], out[2:]):
+        want, wantw, mag, magw = ref.norm_rope_backward(d, x, wt, pos, f, 1e-6, layout)
+        close(dx, want, mag)
+        assert ((dw.double() - wantw).abs() <= 2.0 ** -15 * magw).all()
+
+
 def test_gradient_is_the_difference(mx):
     """dx and dweight along a direction against differences of the definition's forward pass"""
     import torch
