@@ -474,8 +474,9 @@ mx_status_t mx_block_gemm_sums(const void *a_codes, int64_t lda, const float *a_
  * group i is the rows from ends[i - 1] (0 for the first) to ends[i] - 1, ends not
  * decreasing and at most `rows`.  Groups may be empty; rows from the last end on
  * belong to none, and what is at their place in an output is left as it was.  (An
- * end below the one before it or above `rows` is taken as these; nothing outside
- * the buffers is touched whatever ends holds.)  At most 2^16 groups.
+ * end below the one before it or above `rows` is taken as these, but see
+ * mx_block_gemm_grouped_k; nothing outside the buffers is touched whatever ends
+ * holds.)  At most 2^16 groups.
  *
  * Operands whose reduction dimension is the rows (both of a weight gradient) have
  * their blocks of 128 start anew at every group: block b of the transposed form is
@@ -528,12 +529,20 @@ mx_status_t mx_block_gemm_grouped(const void *a_codes, int64_t lda, const float 
  * and [.. N].  C[g] [M x ldc] at c + g * ldc_group elements, ldc_group >= (M - 1) *
  * ldc + N.  An empty group's C is zeros.  Types, sums and accuracy as in
  * mx_block_gemm_sums, K being the group's rows.
+ * This call does not know how many rows the operands were made of: no end may lie
+ * above them (it would claim blocks that nobody wrote; what is read stays within cols).
+ * mx_block_gemm_grouped_k_rows takes their number, and ends above it as the quantizers do.
  */
 mx_status_t mx_block_gemm_grouped_k(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa,
                                     mx_format_t fa, const void *b_codes, int64_t ldb, const float *b_scales,
                                     int64_t ldsb, mx_format_t fb, const int32_t *ends, int64_t groups, int64_t M,
                                     int64_t N, int64_t cols, void *c, mx_out_t out, int64_t ldc_group, int64_t ldc,
                                     mx_sums_t sums, void *stream);
+mx_status_t mx_block_gemm_grouped_k_rows(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa,
+                                         mx_format_t fa, const void *b_codes, int64_t ldb, const float *b_scales,
+                                         int64_t ldsb, mx_format_t fb, const int32_t *ends, int64_t groups,
+                                         int64_t rows, int64_t M, int64_t N, int64_t cols, void *c, mx_out_t out,
+                                         int64_t ldc_group, int64_t ldc, mx_sums_t sums, void *stream);
 
 /*
  * ---------------------------------------------------------------------------

@@ -90,10 +90,11 @@ def lib() -> ctypes.CDLL:
         L.mx_block_quantize_grouped_dual.argtypes = [P, i64, i64, i64, P, i64, i32, P, i64, P, i64, i32, P, i64, P, i64, P]
         L.mx_block_gemm_grouped.argtypes = [P, i64, P, i64, i32, P, i64, i64, P, i64, i64, i32, i32, P, i64, i64, i64, i64, P,
                                             i32, i64, i32, P]
-        L.mx_block_gemm_grouped_k.argtypes = [P, i64, P, i64, i32, P, i64, P, i64, i32, P, i64, i64, i64, i64, P, i32, i64, i64,
-                                              i32, P]
+        cols_args = [P, i64, P, i64, i32, P, i64, P, i64, i32, P, i64], [i64, i64, i64, P, i32, i64, i64, i32, P]
+        L.mx_block_gemm_grouped_k.argtypes = cols_args[0] + cols_args[1]
+        L.mx_block_gemm_grouped_k_rows.argtypes = cols_args[0] + [i64] + cols_args[1]
         for fn in (L.mx_block_quantize_grouped, L.mx_block_quantize_grouped_dual, L.mx_block_gemm_grouped,
-                   L.mx_block_gemm_grouped_k):
+                   L.mx_block_gemm_grouped_k, L.mx_block_gemm_grouped_k_rows):
             fn.restype = ctypes.c_int
         f64 = ctypes.c_double
         heads, rotation = [P, i64, i64, i64] * 2 + [i64, i64], [P, i32, P, i64, i32, f32]
@@ -649,11 +650,12 @@ def block_gemm_grouped(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_code
 
 def block_gemm_grouped_k(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_codes: torch.Tensor, b_scales: torch.Tensor, fb,
                          ends: torch.Tensor, out_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
-                         stream=None, full_sums: bool = False) -> torch.Tensor:
+                         stream=None, full_sums: bool = False, rows: Optional[int] = None) -> torch.Tensor:
     """mx_block_gemm_grouped_k: C[groups x M x N], C[i] = A . B^T over the columns of group i, for A
     [M x cols] and B [N x cols] as block_quantize_grouped gives them for the same ends: the
-    groups' weight gradients.  An empty group's C is zeros.  out_dtype and full_sums as in
-    block_gemm."""
+    groups' weight gradients.  An empty group's C is zeros.  rows: how many the operands were
+    quantized from; ends above it are taken as it, as the quantizers do.  Without it no end may lie
+    above the rows.  out_dtype and full_sums as in block_gemm."""
     f_a, f_b, groups, index = _grouped_types(a_codes, fa, fb, ends, out_dtype)
     sa, sb = a_codes.shape, b_codes.shape
     if len(sa) != 2 or len(sb) != 2 or sa[1] != sb[1]:
@@ -670,10 +672,11 @@ def block_gemm_grouped_k(a_codes: torch.Tensor, a_scales: torch.Tensor, fa, b_co
         if out is None:
             out = torch.empty_strided((groups, M, N), (M * N, N, 1), dtype=out_dtype, device=dev)
         bf16 = out_dtype is _BF16
-        _check(lib().mx_block_gemm_grouped_k(a_codes.data_ptr(), lda, a_scales.data_ptr(), ldsa, f_a, b_codes.data_ptr(), ldb,
-                                             b_scales.data_ptr(), ldsb, f_b, ends.data_ptr(), groups, M, N, K, out.data_ptr(),
-                                             OUT_BF16 if bf16 else OUT_F32, ldcg, ldc, 1 if full_sums or not bf16 else 0,
-                                             _current(dev)))
+        _check(lib().mx_block_gemm_grouped_k_rows(a_codes.data_ptr(), lda, a_scales.data_ptr(), ldsa, f_a, b_codes.data_ptr(),
+                                                  ldb, b_scales.data_ptr(), ldsb, f_b, ends.data_ptr(), groups,
+                                                  K if rows is None else rows, M, N, K, out.data_ptr(),
+                                                  OUT_BF16 if bf16 else OUT_F32, ldcg, ldc, 1 if full_sums or not bf16 else 0,
+                                                  _current(dev)))
     return out
 
 

@@ -156,6 +156,39 @@ mx_status_t check_grouped(int64_t groups, int fa, int fb, int out, int sums) {
     return MX_OK;
 }
 
+// rows: what ends are cut to
+mx_status_t block_gemm_grouped_k(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa, int f_a,
+                                 const void *b_codes, int64_t ldb, const float *b_scales, int64_t ldsb, int f_b,
+                                 const int32_t *ends, int64_t groups, int64_t rows, int64_t M, int64_t N, int64_t cols, void *c,
+                                 int o, int64_t ldc_group, int64_t ldc, int su, void *stream) {
+    mx_status_t st = check_grouped(groups, f_a, f_b, o, su);
+    if (st != MX_OK) return st;
+    if (rows < 0 || M < 0 || N < 0 || cols < 0 || cols % kBlk != 0) return MX_ERR_INVALID_ARG;
+    if (lda < cols || ldb < cols || ldsa < M || ldsb < N || ldc < N) return MX_ERR_INVALID_ARG;
+    if (M == 0 || N == 0 || groups == 0) return MX_OK;
+    if (!c || !ends || (cols > 0 && (!a_codes || !a_scales || !b_codes || !b_scales))) return MX_ERR_INVALID_ARG;
+    const int64_t size = o == MX_OUT_BF16 ? 2 : 4;
+    const Range one = rows_at(c, M, ldc, N, size);
+    if (one.n < 0 || (groups > 1 && (ldc_group < one.n / size || ldc_group > INT64_MAX / size))) return MX_ERR_INVALID_ARG;
+    const Range r[6] = {rows_at(a_codes, M, lda, cols, 1), rows_at(a_scales, cols / kBlk, ldsa, M, 4),
+                        rows_at(b_codes, N, ldb, cols, 1), rows_at(b_scales, cols / kBlk, ldsb, N, 4),
+                        run(ends, groups > INT64_MAX / 4 ? -1 : groups * 4),
+                        groups > 1 ? pieces(c, groups, ldc_group * size, one.n) : one};
+    if ((st = check_ranges(r, 6, 5)) != MX_OK) return st;
+    if (rows >= kMaxDim || M >= kMaxDim || N >= kMaxDim || cols >= kMaxDim || groups > kMaxGroups ||
+        blocks(M) * blocks(N) >= ((int64_t)1 << 22) / groups)
+        return MX_ERR_UNSUPPORTED;
+    if ((st = check_device()) != MX_OK) return st;
+    GroupedGemmArgs g{};
+    static_cast<BlockGemmArgs &>(g) = {(const uint8_t *)a_codes, (const uint8_t *)b_codes, a_scales, b_scales, c, lda, ldb,
+                                       ldsa, ldsb, ldc, (int)M, (int)N, (int)cols, o == MX_OUT_BF16, 0, 0};
+    g.ends = ends;
+    g.groups = (int)groups;
+    g.rows = (int)rows;
+    g.ldcg = groups > 1 ? ldc_group : 0;
+    return launched(launch_block_gemm_grouped_k(g, f_a, f_b, su == MX_SUMS_FP8, (hipStream_t)stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -256,33 +289,16 @@ mx_status_t mx_block_gemm_grouped_k(const void *a_codes, int64_t lda, const floa
                                     const void *b_codes, int64_t ldb, const float *b_scales, int64_t ldsb, mx_format_t fb,
                                     const int32_t *ends, int64_t groups, int64_t M, int64_t N, int64_t cols, void *c,
                                     mx_out_t out, int64_t ldc_group, int64_t ldc, mx_sums_t sums, void *stream) {
-    const int f_a = raw(fa), f_b = raw(fb), o = raw(out), su = raw(sums);
-    mx_status_t st = check_grouped(groups, f_a, f_b, o, su);
-    if (st != MX_OK) return st;
-    if (M < 0 || N < 0 || cols < 0 || cols % kBlk != 0) return MX_ERR_INVALID_ARG;
-    if (lda < cols || ldb < cols || ldsa < M || ldsb < N || ldc < N) return MX_ERR_INVALID_ARG;
-    if (M == 0 || N == 0 || groups == 0) return MX_OK;
-    if (!c || !ends || (cols > 0 && (!a_codes || !a_scales || !b_codes || !b_scales))) return MX_ERR_INVALID_ARG;
-    const int64_t size = o == MX_OUT_BF16 ? 2 : 4;
-    const Range one = rows_at(c, M, ldc, N, size);
-    if (one.n < 0 || (groups > 1 && (ldc_group < one.n / size || ldc_group > INT64_MAX / size))) return MX_ERR_INVALID_ARG;
-    const Range r[6] = {rows_at(a_codes, M, lda, cols, 1), rows_at(a_scales, cols / kBlk, ldsa, M, 4),
-                        rows_at(b_codes, N, ldb, cols, 1), rows_at(b_scales, cols / kBlk, ldsb, N, 4),
-                        run(ends, groups > INT64_MAX / 4 ? -1 : groups * 4),
-                        groups > 1 ? pieces(c, groups, ldc_group * size, one.n) : one};
-    if ((st = check_ranges(r, 6, 5)) != MX_OK) return st;
-    if (M >= kMaxDim || N >= kMaxDim || cols >= kMaxDim || groups > kMaxGroups ||
-        blocks(M) * blocks(N) >= ((int64_t)1 << 22) / groups)
-        return MX_ERR_UNSUPPORTED;
-    if ((st = check_device()) != MX_OK) return st;
-    GroupedGemmArgs g{};
-    static_cast<BlockGemmArgs &>(g) = {(const uint8_t *)a_codes, (const uint8_t *)b_codes, a_scales, b_scales, c, lda, ldb,
-                                       ldsa, ldsb, ldc, (int)M, (int)N, (int)cols, o == MX_OUT_BF16, 0, 0};
-    g.ends = ends;
-    g.groups = (int)groups;
-    g.rows = (int)cols;
-    g.ldcg = groups > 1 ? ldc_group : 0;
-    return launched(launch_block_gemm_grouped_k(g, f_a, f_b, su == MX_SUMS_FP8, (hipStream_t)stream));
+    return block_gemm_grouped_k(a_codes, lda, a_scales, ldsa, raw(fa), b_codes, ldb, b_scales, ldsb, raw(fb), ends, groups, cols,
+                                M, N, cols, c, raw(out), ldc_group, ldc, raw(sums), stream);
+}
+
+mx_status_t mx_block_gemm_grouped_k_rows(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa, mx_format_t fa,
+                                         const void *b_codes, int64_t ldb, const float *b_scales, int64_t ldsb, mx_format_t fb,
+                                         const int32_t *ends, int64_t groups, int64_t rows, int64_t M, int64_t N, int64_t cols,
+                                         void *c, mx_out_t out, int64_t ldc_group, int64_t ldc, mx_sums_t sums, void *stream) {
+    return block_gemm_grouped_k(a_codes, lda, a_scales, ldsa, raw(fa), b_codes, ldb, b_scales, ldsb, raw(fb), ends, groups, rows,
+                                M, N, cols, c, raw(out), ldc_group, ldc, raw(sums), stream);
 }
 
 mx_status_t mx_layer_norm(const void *x_bf16, int64_t rows, int64_t cols, int64_t ldx, const void *weight,
