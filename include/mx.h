@@ -663,8 +663,9 @@ mx_status_t mx_rope(const void *q_bf16, int64_t ldq, int64_t ldq_head, int64_t q
  *     xh = x * rstd, rstd = 1 / sqrt(mean(x^2) + eps), y = rotation of xh * weight,
  * weight the `dim` values (of `param` type, NULL: 1) that all query heads, or all
  * key heads, share.  One pass, fp32 until y's one rounding.  eps >= 0, finite;
- * rot = 0 leaves the norm alone (positions and freqs may then be NULL).  As in
- * mx_layer_norm, a head of zeros with eps = 0 gives NaN.
+ * rot = 0 leaves the norm alone (positions and freqs may then be NULL).  Heads of
+ * any finite elements are normalised, also where their squares leave fp32's range
+ * (which mx_layer_norm's rows may not); a head of zeros with eps = 0 gives NaN.
  */
 mx_status_t mx_qk_norm_rope(const void *q_bf16, int64_t ldq, int64_t ldq_head, int64_t q_heads, const void *k_bf16,
                             int64_t ldk, int64_t ldk_head, int64_t k_heads, int64_t tokens, int64_t dim,
@@ -677,9 +678,10 @@ mx_status_t mx_qk_norm_rope(const void *q_bf16, int64_t ldq, int64_t ldq_head, i
  * mx_qk_norm_rope_backward -- with dy the gradient of y, u the transposed rotation
  * of dy and g = u * weight:
  *     dx = rstd * (g - xh * mean(g * xh)),  dweight = sum over tokens and heads of u * xh
- * from x as the forward call read it (rstd is made again).  dx: bf16, rounded once;
- * dq_weight, dk_weight: fp32 [dim], overwritten (zeros where there are no tokens or
- * no heads), either may be NULL.  workspace as in mx_layer_norm_backward,
+ * from x as the forward call read it (rstd is made again; the products g * x are fp32
+ * numbers).  dx: bf16, rounded once; dq_weight, dk_weight: fp32 [dim], overwritten
+ * (zeros where there are no tokens or no heads), either may be NULL.  workspace as in
+ * mx_layer_norm_backward,
  * mx_qk_norm_rope_backward_workspace(tokens, q_heads, k_heads, dim) bytes.  Sums are
  * in a fixed order: the same inputs give the same bits.
  */

@@ -241,6 +241,13 @@ __device__ __forceinline__ void make_angles(float2 *cs, const RopeArgs &a, int64
     __builtin_amdgcn_wave_barrier();
 }
 
+// A power of two that brings a head's squares back into fp32 where m, their mean plus eps, has left it (elements of 2^59
+// and more) or lies where their small ones have (below 2^-100): for any finite bf16 elements the sum of the scaled
+// squares is within 2^-66 .. 2^125, or zero.  1 for all others, whose bits it leaves alone.
+__device__ __forceinline__ float head_factor(float m) {
+    return m >= 0x1p-100f && m < INFINITY ? 1.f : m < 1.f ? 0x1p100f : 0x1p-70f;
+}
+
 // Forward.  A token's heads are passes of 64 / L, queries first, a wave for each: its own angles cost a wave less than
 // waiting does for its next heads.  8192 tokens of 72 heads of 128, rotation: a wave for nine passes 65 us, for three
 // 59.5, for two 57, for one 53 (5.7 TB/s); 40 heads, norm and rotation 28 for five, 27 for one.
@@ -274,7 +281,19 @@ __global__ __launch_bounds__(64 * kHW) void k_heads(RopeArgs a, FastDiv parts, i
             m.load_weight(w, h.weight, a.param_bf16);
 #pragma unroll
             for (int s = 0; s < M::NS; s++) sq = __builtin_fmaf(v[s], v[s], sq);
-            const float rstd = rsqrt1(__builtin_fmaf(group_sum<L>(sq), 1.0f / (float)a.dim, a.eps));
+            const float rn = 1.0f / (float)a.dim;
+            float m2 = __builtin_fmaf(group_sum<L>(sq), rn, a.eps);
+            const float f = head_factor(m2);
+            if (__any(f != 1.f)) {  // hardly ever; the whole wave, as group_sum moves across lanes
+                sq = 0.f;
+#pragma unroll
+                for (int s = 0; s < M::NS; s++) {
+                    v[s] *= f;
+                    sq = __builtin_fmaf(v[s], v[s], sq);
+                }
+                m2 = __builtin_fmaf(group_sum<L>(sq), rn, a.eps * f * f);
+            }
+            const float rstd = rsqrt1(m2);
 #pragma unroll
             for (int s = 0; s < M::NS; s++) v[s] = v[s] * rstd * w[s];
         }
@@ -339,13 +358,31 @@ __global__ __launch_bounds__(64 * kHW, V ? 4 : 1) void k_heads_bwd(RopeArgs a, i
             }
             sq = group_sum<L>(sq);
             sg = group_sum<L>(sg);
-            const float rstd = live ? rsqrt1(__builtin_fmaf(sq, rn, a.eps)) : 0.f;
-            const float mean = sg * rstd * rn;  // of g * xh
+            float m2 = __builtin_fmaf(sq, rn, a.eps);
+            const float f = live ? head_factor(m2) : 1.f;
+            const bool scaled = __any(f != 1.f);
+            if (scaled) {  // hardly ever
+                sq = sg = 0.f;
+#pragma unroll
+                for (int s = 0; s < M::NS; s++) {
+                    v[s] *= f;
+                    sq = __builtin_fmaf(v[s], v[s], sq);
+                    sg = __builtin_fmaf(u[s] * w[s], v[s], sg);
+                }
+                sg = group_sum<L>(sg);
+                m2 = __builtin_fmaf(group_sum<L>(sq), rn, a.eps * f * f);
+            }
+            const float rstd = live ? rsqrt1(m2) : 0.f;  // of x * f
+            const float mean = sg * rstd * rn;           // of g * xh
 #pragma unroll
             for (int s = 0; s < M::NS; s++) {
                 const float xh = v[s] * rstd;
                 acc[s] = __builtin_fmaf(u[s], xh, acc[s]);
                 v[s] = __builtin_fmaf(-xh, mean, u[s] * w[s]) * rstd;
+            }
+            if (scaled) {
+#pragma unroll
+                for (int s = 0; s < M::NS; s++) v[s] *= f;
             }
             m.template store<NT>(po + head * h.oh, v, live);
         }
