@@ -216,9 +216,15 @@ hipError_t launch_forms(const uint16_t *x, int64_t rows, int64_t cols, int64_t l
     // than it pushes out.  Through the cache and past it, with outputs over the same memory call after call:
     // 28672 x 4096 in tiles, both forms 91 and 75 us, 8192 x 4096 (67 MB, partly still cached), one form 18.6 and
     // 20.0; with outputs in turn 92 either way, and 21.3 and 20.0.
-    // By groups 16384 x 4096 is past that: outputs in turn, transposed form 45.8 and 39.6, both 59 and 50; 8192 x 4096
-    // 18.9 and 21.1, 30 and 30.
-    const bool whole = cols % 8 == 0, nt = whole && rows * cols + (GROUPED ? 1 : 0) > (int64_t)1 << 26;
+    // By groups, outputs over the same memory every other call, the two cross where input and outputs come to 144 MiB.
+    // Rows x 4096, 8 groups, through the caches and past them: transposed form 8192 19.1 and 21.1, 10240 23.5 and
+    // 25.2, 12288 (144 MiB) 32.1 and 32.0, 14336 40 and 36, 16384 45 and 39; both forms 8192 (128 MiB) 29.2 and 29.7, 9216
+    // (144) 34.4 and 32.3, 12288 46 and 41, 16384 60 and 50; x 2048 and x 7168 alike.  With more outputs in turn than the
+    // last-level cache holds the latter is up to 12% faster with 8 groups at all of these sizes, with 128 up to 4% slower
+    // (16384 x 4096, rows of the transposed form 255 * 128 bytes apart, 63 and 72, both forms 81 and 93).
+    const bool whole = cols % 8 == 0;
+    const bool far = GROUPED ? rows * cols * (r.codes && t.codes ? 4 : 3) > (int64_t)144 << 20 : rows * cols > (int64_t)1 << 26;
+    const bool nt = whole && far;
 #define MX_Q(fr, ft, row, tr)                                                                                             \
     do {                                                                                                                  \
         if (nt) hipLaunchKernelGGL((k_block_quantize<fr, ft, row, tr, TILE, true, true, GRP>), grid, block, 0, s, x, rows,     \
