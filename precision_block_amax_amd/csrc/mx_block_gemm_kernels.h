@@ -587,7 +587,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN * CFG::KG, CFG::WM * CFG::WN
             stage(0, it);
             stage(1, it + 1);
         }
-    } else {  // groups may have one block of K only: no stage is for nothing; 1536 x 2048 of it, 128 times 389 -> 344 us
+    } else {  // groups may have one block of K only: no stage is for nothing; 1536 x 2048 of it, 128 times, operands in the last-level cache, 389 -> 344 us
         for (int it = 0; it + 1 < nit; it += 2) {
             stage(0, it);
             stage(1, it + 1);
@@ -1054,22 +1054,39 @@ struct Rate {
 
 // The kernel for a product by rows.  The host knows how many rows and groups there are, not how the rows are dealt out,
 // so tiles are counted as for rows that fall on groups at random: groups (1 - exp(-mean)) of them have rows, each half a
-// tile and a little more at its end.  The rates below were fitted to measured times (us, MI355X, weights taking turns)
-// of groups x N x K from 1 x 4096 x 4096 to 128 x 1536 x 2048 and 8 x 28672 x 4096 with means of 1/16 to 8192 rows, the
-// most popular group ten times the least; the kernel that they choose was within a tenth of the fastest in 119 of 127 of
-// these.  FP8 sums, B in tiles (8 x 16, 16 x 16, 64 x 32, 128 x 128 in two groups of waves, 128 x 128, 64 x 128, 256 x 256):
-//   128 x 1536 x 2048   mean of 1/16    8.3   8.2   8.8   12    13    12    26
+// tile and a little more at its end.  The rates were fitted to measured times (us, MI355X, weights taking turns) of groups x N x K from 1 x 4096 x 4096 to 128 x 1536 x 2048 and 8 x 28672 x 4096 with means
+// of 1/16 to 8192 rows, the most popular group ten times the least.  What they choose was within a tenth of the fastest kernel
+// in 79 of 83 of these with FP8 sums and B in tiles (at worst 1.14 times), in 39 of 45 with B's scales by column (1.20: 8 x
+// 14336 x 4096, mean 8) and in 42 of 45 with fp32 sums (1.14).  In this order: 8 x 16, 16 x 16, 64 x 32, 128 x 128 in two
+// groups of waves, 128 x 128, 64 x 128, 256 x 256.  FP8 sums, B in tiles:
+//   128 x 1536 x 2048   mean of 1/16    8.4   8.3   8.8   12    13    12    26
 //                       4                83    79    82   93    67    64    83
-//                       64              488   298   132  116    91    91   104
-//                       128             906   531   204  149   114   123   118
-//                       512            3320  1865   618  421   289   339   260
-//   8 x 2048 x 14336    1                21    22    35   76    99    92   150
-//                       32              100    79    68   80    92    86   150
-//                       128             288   205   119   83    94    96   156
-//                       256             541   369   199  154   114   137   162
-//   8 x 28672 x 4096    2               104   103   116  142   135   125   154
-//                       32              491   330   228  214   196   199   213
-//                       2048          24786 14656  4647 3048  2148  2745  1778
+//                       64              487   298   132  116    91    91   104
+//                       128             906   530   205  149   114   123   120
+//                       512            3313  1865   619  420   291   342   264
+//   8 x 2048 x 14336    1                21    22    35   75    99    93   150
+//                       32              100    78    68   80    92    86   150
+//                       128             288   205   118   82    94    95   155
+//                       256             538   376   198  158   123   142   163
+//   8 x 28672 x 4096    2               102   101   114  139   133   123   151
+//                       32              489   331   228  221   209   214   224
+//                       2048          24787 14636  4689 3051  2146  2744  1809
+// B's scales by column:
+//   128 x 1536 x 2048   4                84    80    97   96    71    66
+//                       128             903   532   248  153   121   128
+//                       512            3310  1864   760  429   320   361
+//   8 x 14336 x 4096    8                98    95   114  127   114   121
+//                       128             812   487   247  174   138   157
+//                       2048          12214  7247  2645 1561  1215  1443
+//   8 x 2048 x 14336    128             297   208   124   86    99    99
+// fp32 sums:
+//   128 x 1536 x 2048   4                85    82    85  110    86
+//                       128             972   555   223  184   155
+//                       512            3644  1990   702  539   451
+//   8 x 14336 x 4096    8               101    95   100  125   111
+//                       128             858   500   234  198   178
+//                       2048          13056  7471  2657 1995  1751
+//   8 x 2048 x 14336    128             315   204   120   99   115
 template <int FA, int FB, bool BT, bool FP8SUMS>
 hipError_t launch_grouped_as(GroupedGemmArgs g, hipStream_t s) {
     const int64_t nk = (g.K + kBlk - 1) / kBlk;

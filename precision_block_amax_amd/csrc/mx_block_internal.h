@@ -41,12 +41,13 @@ struct BlockGemmArgs {
 // A product for each group of rows (or of columns of the operands), `ends` as in mx_block_group.h
 struct GroupedGemmArgs : BlockGemmArgs {
     const int32_t *ends;
-    int groups, rows;              // rows: what ends are cut to
+    int groups, rows;              // rows: what ends are cut to (M, or what the columns were made of)
     int64_t ldbg, ldsbg, ldcg;     // from one group's B, its scales or C to the next one's
 };
 
-// Rows: A's and C's rows in groups, B a matrix per group.  M is the number of rows, 0 < N, K; K == 0 clears C's rows.
-// K: A's and B's columns in groups, every group from a block of its own on; K columns in all, a C per group.
+// Rows: A's and C's rows in groups, B a matrix per group.  M is the number of rows, M, N > 0; K == 0 clears the groups' rows.
+// K: A's and B's columns in groups, every group from a block of its own on; K columns in all, a multiple of 128 (0: every
+// group is empty), a C per group.
 hipError_t launch_block_gemm_grouped(const GroupedGemmArgs &g, int fa, int fb, bool b_tile, bool fp8_sums, hipStream_t stream);
 hipError_t launch_block_gemm_grouped_k(const GroupedGemmArgs &g, int fa, int fb, bool fp8_sums, hipStream_t stream);
 

@@ -82,7 +82,8 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
 }
 
 // 1 / sqrt(v), good to 2^-23: the instruction's value and one Newton step, in 5 operations for 30 of a square root
-// and a division.  Zero, very small, infinite and NaN v take those; all lanes hold the same v.
+// and a division.  Zero, very small, infinite and NaN v take those, in a branch that is left to the lanes that
+// need it: lanes may hold different v (a head's, several to a wave, or a row's).
 __device__ __forceinline__ float rsqrt1(float v) {
     if (!(v >= 0x1p-100f && v < INFINITY)) return 1.0f / __builtin_sqrtf(v);
     const float y = __builtin_amdgcn_rsqf(v);

@@ -23,8 +23,8 @@
 //
 // Bound by memory: 2 bytes read and 2 written per element, backward 4 and 2.  Measured
 // with inputs in turn, heads of 128: rotation of 8192 tokens x 72 heads (302 MB) 50 us,
-// 6.0 TB/s; norm and rotation of 8192 x 40 (168 MB) 28 us, 6.0 TB/s, backward (252 MB) 51
-// us, 4.9 TB/s, and 4.5 for the weights' sums; of 32768 x 40 114 us and 198.  A copy
+// 6.0 TB/s; norm and rotation of 8192 x 40 (168 MB) 27 to 29 us, 6.0 TB/s, backward (252 MB)
+// 52 to 54 us, 4.8 TB/s, and 4 to 5 for the weights' sums; of 32768 x 40 114 us and 197 in all.  A copy
 // reaches 5.2 from HBM; part of these inputs is still in the last-level cache.
 // One token: 2.5 us, launch and latency.
 #include <type_traits>
