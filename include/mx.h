@@ -511,9 +511,9 @@ mx_status_t mx_block_quantize_grouped_dual(const void *x_bf16, int64_t rows, int
  * of groups * N rows, N a multiple of 128, qualify in both forms: with
  * MX_BLOCK_TILE ldb_group = N * ldb, ldsb_group = N / 128 (ldsb = groups * that);
  * its transposed form is B for the gradient of A: ldb_group = N, ldsb_group = N /
- * 128 * ldsb.  Types, sums, accuracy, limits and alignment as in
- * mx_block_gemm_sums; ldb_group a multiple of 16 is the fast case.  K = 0 writes
- * zeros to the groups' rows.
+ * 128 * ldsb.  Types, sums, accuracy, limits (for the most tiles that the groups
+ * may take) and alignment as in mx_block_gemm_sums; ldb_group a multiple of 16 is
+ * the fast case.  K = 0 writes zeros to the groups' rows.
  */
 mx_status_t mx_block_gemm_grouped(const void *a_codes, int64_t lda, const float *a_scales, int64_t ldsa, mx_format_t fa,
                                   const void *b_codes, int64_t ldb_group, int64_t ldb, const float *b_scales,
@@ -527,8 +527,8 @@ mx_status_t mx_block_gemm_grouped(const void *a_codes, int64_t lda, const float 
  * A [M x cols] and B [N x cols] as mx_block_quantize_grouped writes them for the same
  * ends, cols a multiple of 128 that holds all the groups' blocks; scales [cols / 128][M]
  * and [.. N].  C[g] [M x ldc] at c + g * ldc_group elements, ldc_group >= (M - 1) *
- * ldc + N.  An empty group's C is zeros.  Types, sums and accuracy as in
- * mx_block_gemm_sums, K being the group's rows.
+ * ldc + N.  An empty group's C is zeros.  Types, sums, accuracy and limits (for the
+ * tiles of all groups) as in mx_block_gemm_sums, K being the group's rows.
  * This call does not know how many rows the operands were made of: no end may lie
  * above them (it would claim blocks that nobody wrote; what is read stays within cols).
  * mx_block_gemm_grouped_k_rows takes their number, and ends above it as the quantizers do.
