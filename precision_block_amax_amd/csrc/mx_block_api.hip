@@ -184,7 +184,9 @@ mx_status_t block_gemm_grouped_k(const void *a_codes, int64_t lda, const float *
                                        ldsa, ldsb, ldc, (int)M, (int)N, (int)cols, o == MX_OUT_BF16, 0, 0};
     g.ends = ends;
     g.groups = (int)groups;
-    g.rows = (int)rows;
+    // a group past the columns has no blocks, whatever its end: ends may as well be cut to them, which keeps a group's rows
+    // rounded up to blocks within 31 bits
+    g.rows = (int)(rows < cols ? rows : cols);
     g.ldcg = groups > 1 ? ldc_group : 0;
     return launched(launch_block_gemm_grouped_k(g, f_a, f_b, su == MX_SUMS_FP8, (hipStream_t)stream));
 }

@@ -114,6 +114,20 @@ def test_more_routed_than_held(mx):
         assert torch.equal(out, step())
 
 
+@pytest.mark.parametrize("rows", [384, 385, 1 << 20, 2 ** 31 - 128, 2 ** 31 - 127, 2 ** 31 - 1])
+@pytest.mark.parametrize("ends", [[2 ** 31 - 1], [100, 2 ** 31 - 1, 2 ** 31 - 1], [0, 2 ** 31 - 100, 5], [200, 384, 1 << 30]], ids=str)
+def test_more_rows_than_columns(mx, rows, ends):
+    """a number of rows beyond the columns: groups have the blocks that there are"""
+    import torch
+    e = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    for M, N in ((70, 40), (150, 300)):
+        a, b = ((torch.full((n, 384), 0x38, dtype=torch.uint8, device="cuda"), torch.ones(3, n, device="cuda")) for n in (M, N))
+        C, S = grp.gemm_k(a, "e4m3", b, "e4m3", ends)
+        for dtype in (torch.float32, torch.bfloat16):
+            c = mx.block_gemm_grouped_k(*a, "e4m3", *b, "e4m3", e, out_dtype=dtype, rows=rows)
+            check(c, C, S, 3, dtype is torch.float32)
+
+
 def test_refusals(mx):
     import torch
     e = torch.tensor([100, 200], dtype=torch.int32, device="cuda")
